@@ -343,6 +343,119 @@ int qkv_cte_run_noalloc(qkv_cte_plan_t plan, const uint8_t* A, const float* a_sc
  * library follows. */
 int qkv_cte_noalloc_status(void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the projection in a transformer block. They are additions of
+ * this library (the page names the AdaLN producer and the cos/sin caches but defines
+ * neither). Like the rest they are stream-ordered and asynchronous, own no memory,
+ * check their arguments before any launch and run on the current device, which must
+ * be the one that holds the tensors. Calls may overlap on the GPU unless they share a
+ * workspace.
+ * ------------------------------------------------------------------------- */
+
+/* Element types: bf16, fp16 (both 2 bytes) and fp32. */
+enum { QKV_CTE_DTYPE_BF16 = 0, QKV_CTE_DTYPE_FP16 = 1, QKV_CTE_DTYPE_FP32 = 2 };
+
+/* Layer norm of each row: y = (x - mean) * rstd * weight + bias with mean and variance
+ * over the row's `cols` elements, rstd = 1 / sqrt(variance + eps). Adaptive norms pass
+ * weight = 1 + scale and bias = shift. Statistics and products are fp32, y is rounded
+ * once.
+ *
+ * x, y        : dtype [rows, cols], rows x_row_stride / y_row_stride elements apart (an
+ *               input's stride may be 0: one row for all), elements contiguous. y may be
+ *               x itself (same pointer and stride) and must not overlap it otherwise; two
+ *               column ranges of one wide tensor do not overlap.
+ * weight, bias: param_dtype [cols] or NULL (1 and 0)
+ * mean, rstd  : fp32 [rows] outputs, or NULL: what the backward pass takes
+ * dtype       : QKV_CTE_DTYPE_*; param_dtype: the same, or QKV_CTE_DTYPE_FP32
+ * Any cols >= 1 and any element-aligned pointers are taken; 16-byte aligned pointers and
+ * strides and whole 16-byte rows run fastest. rows == 0 launches nothing. Returns 0, -1
+ * (null or overlapping buffers, strides, types, eps), -2 (alignment to the element,
+ * rows > INT32_MAX), -3 or -4. */
+int qkv_cte_layer_norm(const void* x, int64_t x_row_stride, const void* weight, const void* bias, void* y,
+                       int64_t y_row_stride, float* mean, float* rstd, int64_t rows, int32_t cols, float eps,
+                       int32_t dtype, int32_t param_dtype, void* stream);
+
+/* Gradients of qkv_cte_layer_norm from dy and the saved statistics, with
+ * xh = (x - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - mean_cols(g) - xh * mean_cols(g * xh)),
+ *   dweight = sum_rows(dy * xh), dbias = sum_rows(dy).
+ * dy, x       : dtype [rows, cols] with row strides (0: one row for all)
+ * weight      : param_dtype [cols] or NULL (1)
+ * mean, rstd  : fp32 [rows], as the forward pass wrote them
+ * dx          : dtype [rows, cols] or NULL; may be dy or x itself
+ * dweight, dbias: param_dtype [cols] or NULL; overwritten (zeros when rows == 0). Summed
+ *               in fp32 in a fixed order and rounded once: equal calls give equal bits.
+ * workspace   : qkv_cte_layer_norm_backward_workspace(rows, cols) bytes, 256-byte aligned;
+ *               NULL is fine without dweight and dbias, or without rows. Its contents need
+ *               no preparation.
+ * Returns 0, -1, -2, -3 or -4 as qkv_cte_layer_norm. */
+int qkv_cte_layer_norm_backward(const void* dy, int64_t dy_row_stride, const void* x, int64_t x_row_stride,
+                                const void* weight, const float* mean, const float* rstd, void* dx,
+                                int64_t dx_row_stride, void* dweight, void* dbias, int64_t rows, int32_t cols,
+                                int32_t dtype, int32_t param_dtype, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Workspace bytes of qkv_cte_layer_norm_backward (host only). Returns 0, -1 or -2. */
+int qkv_cte_layer_norm_backward_workspace(int64_t rows, int32_t cols, size_t* bytes);
+
+/* Rotary positions with several axes (time, height, width of a video's patches, ...):
+ * the cos/sin tables qkv_cte_run takes, and the rotation of a tensor that does not come
+ * out of the projection (cached keys, gradients). A head's d_head/2 pairs are divided
+ * among the axes in order, axis i taking axis_dims[i]/2 pairs; pair p turns by
+ * position[axis(p)] * theta^(-e(p)):
+ *   PER_AXIS: e = 2j / axis_dims[i] for the axis's pair j (each axis spans the spectrum);
+ *   SHARED  : e = 2p / d_head (one spectrum over the head; the axis only picks the position).
+ * ROTATE_HALF pairs lanes (p, p + d_head/2), as qkv_cte_run does; INTERLEAVED pairs
+ * lanes (2p, 2p + 1). Angles keep their accuracy for any int32 position. */
+enum { QKV_CTE_ROPE_PER_AXIS = 0, QKV_CTE_ROPE_SHARED = 1 };
+enum { QKV_CTE_ROPE_ROTATE_HALF = 0, QKV_CTE_ROPE_INTERLEAVED = 1 };
+
+typedef struct {
+    int32_t d_head;        /* even, <= 512 */
+    int32_t n_axes;        /* 1 to 4 */
+    int32_t axis_dims[4];  /* lanes per axis: even, > 0, adding up to d_head */
+    int32_t spectrum;      /* QKV_CTE_ROPE_PER_AXIS / _SHARED */
+    int32_t pairing;       /* QKV_CTE_ROPE_ROTATE_HALF / _INTERLEAVED */
+    double theta;          /* base, >= 1 */
+} qkv_cte_rope_desc;
+
+typedef struct qkv_cte_rope_plan_s* qkv_cte_rope_plan_t;
+
+/* Validate `desc` (host only) and create a plan; it holds host memory only and may be
+ * used by any number of threads and streams at once. Returns 0, -1 or -2 (d_head > 512). */
+int qkv_cte_rope_plan(qkv_cte_rope_plan_t* out, const qkv_cte_rope_desc* desc);
+
+/* Release a plan. NULL is a no-op. */
+void qkv_cte_rope_destroy(qkv_cte_rope_plan_t plan);
+
+/* Where a row stands (one of the two, device memory):
+ * positions: int32 [seq, n_axes], a batch's positions pos_batch_stride elements after the
+ *            previous one's (0: every batch uses the same);
+ * grids    : int32 [batch, n_axes], sizes of each batch's grid; row s stands at the s-th
+ *            point of the grid (last axis fastest), and rows behind the grid's end are
+ *            padding: not rotated (tables: cos 1, sin 0).
+ *
+ * cos_table, sin_table: fp32 [batch * seq, d_head], 16-byte aligned (qkv_cte_run wants
+ *            32); each pair's value at both of its lanes.
+ * No rows: nothing is launched. Returns 0, -1, -2, -3 or -4. */
+int qkv_cte_rope_tables(qkv_cte_rope_plan_t plan, int64_t batch, int64_t seq, const int32_t* positions,
+                        int64_t pos_batch_stride, const int32_t* grids, float* cos_table, float* sin_table,
+                        void* stream);
+
+/* y = x rotated: lo' = lo cos - hi sin, hi' = hi cos + lo sin in fp32, rounded once;
+ * inverse = 1 turns back (the gradient of the rotation, which is its transpose).
+ * x, y: dtype [batch, seq, heads, d_head] with the strides given in elements (lanes
+ *       contiguous): [B, S, n, d], [B, n, S, d], or the head columns of a fused projection
+ *       output alike. y may be x itself (same pointer and strides); otherwise they must not
+ *       overlap (column ranges of one wide tensor do not), and y's elements must be
+ *       distinct. Padding rows are copied, or left alone in place.
+ * Pointers and strides that keep whole 16-byte groups of pairs run fastest; any
+ * element-aligned ones are taken. Returns 0, -1, -2, -3 or -4. */
+int qkv_cte_rope_apply(qkv_cte_rope_plan_t plan, const void* x, int64_t x_batch_stride, int64_t x_row_stride,
+                       int64_t x_head_stride, void* y, int64_t y_batch_stride, int64_t y_row_stride,
+                       int64_t y_head_stride, int64_t batch, int64_t seq, int32_t heads, const int32_t* positions,
+                       int64_t pos_batch_stride, const int32_t* grids, int32_t dtype, int32_t inverse, void* stream);
+
 /* Release a plan. NULL is a no-op. */
 void qkv_cte_destroy(qkv_cte_plan_t plan);
 

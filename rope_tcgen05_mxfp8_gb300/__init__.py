@@ -17,3 +17,8 @@ from .qkv_cte import (  # noqa: F401
     qkv_cte_run_host, qkv_cte_host_scratch_bytes,
     qkv_cte_status, qkv_cte_version,
 )
+from .block_ops import (  # noqa: F401
+    QKV_CTE_DTYPE_BF16, QKV_CTE_DTYPE_FP16, QKV_CTE_DTYPE_FP32, QKV_CTE_ROPE_INTERLEAVED, QKV_CTE_ROPE_PER_AXIS,
+    QKV_CTE_ROPE_ROTATE_HALF, QKV_CTE_ROPE_SHARED, QkvCteRopeAxes, qkv_cte_layer_norm, qkv_cte_layer_norm_backward,
+    qkv_cte_layer_norm_backward_workspace, qkv_cte_rope_desc,
+)

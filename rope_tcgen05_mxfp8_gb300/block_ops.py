@@ -1,0 +1,300 @@
+"""Bindings of the operators around the projection (see include/qkv_cte.h): layer norm
+with its backward pass and rotary positions with several axes.
+
+Argument marshalling only, as in qkv_cte.py: every computation runs in the library's
+kernels. Tensors live on one CUDA device, which need not be the current one; a call
+runs on `stream` (default: that device's current stream) and does not synchronise.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Sequence
+
+import torch
+
+from .qkv_cte import _check, load
+
+QKV_CTE_DTYPE_BF16 = 0
+QKV_CTE_DTYPE_FP16 = 1
+QKV_CTE_DTYPE_FP32 = 2
+QKV_CTE_ROPE_PER_AXIS = 0
+QKV_CTE_ROPE_SHARED = 1
+QKV_CTE_ROPE_ROTATE_HALF = 0
+QKV_CTE_ROPE_INTERLEAVED = 1
+
+_DTYPE = {torch.bfloat16: QKV_CTE_DTYPE_BF16, torch.float16: QKV_CTE_DTYPE_FP16, torch.float32: QKV_CTE_DTYPE_FP32}
+
+
+class qkv_cte_rope_desc(ctypes.Structure):
+    _fields_ = [
+        ("d_head", ctypes.c_int32),
+        ("n_axes", ctypes.c_int32),
+        ("axis_dims", ctypes.c_int32 * 4),
+        ("spectrum", ctypes.c_int32),
+        ("pairing", ctypes.c_int32),
+        ("theta", ctypes.c_double),
+    ]
+
+
+_bound = None
+
+
+def _lib() -> ctypes.CDLL:
+    """The library with the argument types of these entry points set."""
+    global _bound
+    if _bound is not None:
+        return _bound
+    lib = load()
+    P, I64, I32, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+    SIZE = ctypes.c_size_t
+    lib.qkv_cte_layer_norm.argtypes = [P, I64, P, P, P, I64, P, P, I64, I32, F, I32, I32, P]
+    lib.qkv_cte_layer_norm_backward.argtypes = [P, I64, P, I64, P, P, P, P, I64, P, P, I64, I32, I32, I32, P, SIZE, P]
+    lib.qkv_cte_layer_norm_backward_workspace.argtypes = [I64, I32, ctypes.POINTER(SIZE)]
+    lib.qkv_cte_rope_plan.argtypes = [ctypes.POINTER(P), ctypes.POINTER(qkv_cte_rope_desc)]
+    lib.qkv_cte_rope_destroy.argtypes = [P]
+    lib.qkv_cte_rope_tables.argtypes = [P, I64, I64, P, I64, P, P, P, P]
+    lib.qkv_cte_rope_apply.argtypes = [P, P, I64, I64, I64, P, I64, I64, I64, I64, I64, I32, P, I64, P, I32, I32, P]
+    for name in ("layer_norm", "layer_norm_backward", "layer_norm_backward_workspace", "rope_plan", "rope_tables",
+                 "rope_apply"):
+        getattr(lib, "qkv_cte_" + name).restype = ctypes.c_int
+    lib.qkv_cte_rope_destroy.restype = None
+    _bound = lib
+    return lib
+
+
+def _launch(fn, device, stream, *args):
+    """fn(*args, stream) with `device` current."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if device.index == torch.cuda.current_device():
+        return _check(fn(*args, handle))
+    with torch.cuda.device(device):
+        return _check(fn(*args, handle))
+
+
+def _kept(stream, device, *tensors):
+    """Tensors allocated here for work on another stream than the one the allocator knows
+    of: their memory is not handed out again before that work is done."""
+    if stream is None:
+        return
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle == torch.cuda.current_stream(device).cuda_stream:
+        return
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=device)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(s)
+
+
+def _tensor(name: str, t, dtypes, device=None):
+    """t, checked to be a CUDA tensor of one of `dtypes` (on `device`)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, not on {device}")
+    return t
+
+
+def _vector(name: str, t, dtypes, device, n: int) -> Optional[int]:
+    """Address of a contiguous tensor of n elements, or None."""
+    if t is None:
+        return None
+    _tensor(name, t, dtypes, device)
+    if not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name}: must be contiguous with {n} elements, got shape {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(name: str, t, dtypes, device=None, shape=None):
+    """(address, row stride) of [..., cols] as rows; the elements of a row are contiguous."""
+    _tensor(name, t, dtypes, device)
+    if t.dim() < 1:
+        raise ValueError(f"{name}: needs at least one dimension")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} is not {tuple(shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if t.dim() == 1:
+        return t.data_ptr(), t.shape[0]
+    if t.dim() != 2:
+        try:
+            t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(-1, max(t.shape[-1], 1))
+        except RuntimeError:
+            raise ValueError(f"{name}: its rows must be evenly spaced") from None
+    return t.data_ptr(), t.stride(0)
+
+
+def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None, rstd=None, stats=False, stream=None):
+    """Layer norm over the last dimension of x [..., cols] (bf16, fp16 or fp32; rows may be
+    strided). weight, bias: [cols] of x's type or fp32, or None. Returns (y, mean, rstd);
+    the fp32 statistics [...] are written when given or asked for with `stats`, else None.
+    `out` may be x."""
+    px, ldx = _rows("x", x, _DTYPE)
+    dev, cols = x.device, x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    param = weight if weight is not None else bias
+    pdt = param.dtype if isinstance(param, torch.Tensor) else x.dtype
+    if pdt not in (x.dtype, torch.float32):
+        raise TypeError(f"weight and bias: dtype {pdt} is neither {x.dtype} nor torch.float32")
+    pw = _vector("weight", weight, (pdt,), dev, cols)
+    pb = _vector("bias", bias, (pdt,), dev, cols)
+    made = []
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        made.append(out)
+    if stats:
+        if mean is None:
+            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+            made.append(mean)
+        if rstd is None:
+            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+            made.append(rstd)
+    py, ldy = _rows("out", out, (x.dtype,), dev, x.shape)
+    pm = _vector("mean", mean, (torch.float32,), dev, rows)
+    pr = _vector("rstd", rstd, (torch.float32,), dev, rows)
+    _kept(stream, dev, *made)
+    _launch(_lib().qkv_cte_layer_norm, dev, stream, px, ldx, pw, pb, py, ldy, pm, pr, rows, cols, eps, _DTYPE[x.dtype],
+            _DTYPE[pdt])
+    return out, mean, rstd
+
+
+def qkv_cte_layer_norm_backward_workspace(rows: int, cols: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib().qkv_cte_layer_norm_backward_workspace(rows, cols, ctypes.byref(n)))
+    return n.value
+
+
+def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, workspace=None,
+                                stream=None):
+    """Gradients of qkv_cte_layer_norm: (dx, dweight, dbias), the outputs given, or, with
+    none given, all three allocated here (dweight and dbias of weight's type, fp32 without
+    a weight). mean, rstd: the forward pass's statistics. dx may be dy or x."""
+    px, ldx = _rows("x", x, _DTYPE)
+    dev, cols = x.device, x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    pg, ldg = _rows("dy", dy, (x.dtype,), dev, x.shape)
+    param = next((t for t in (weight, dweight, dbias) if isinstance(t, torch.Tensor)), None)
+    pdt = param.dtype if param is not None else torch.float32
+    if pdt not in (x.dtype, torch.float32):
+        raise TypeError(f"weight, dweight and dbias: dtype {pdt} is neither {x.dtype} nor torch.float32")
+    made = []
+    if dx is None and dweight is None and dbias is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dweight = torch.empty(cols, dtype=pdt, device=dev)
+        dbias = torch.empty(cols, dtype=pdt, device=dev)
+        made += [dx, dweight, dbias]
+    pd, ldd = _rows("dx", dx, (x.dtype,), dev, x.shape) if dx is not None else (None, 0)
+    pw = _vector("weight", weight, (pdt,), dev, cols)
+    pdw = _vector("dweight", dweight, (pdt,), dev, cols)
+    pdb = _vector("dbias", dbias, (pdt,), dev, cols)
+    pm = _vector("mean", mean, (torch.float32,), dev, rows)
+    pr = _vector("rstd", rstd, (torch.float32,), dev, rows)
+    ws_bytes, pws = 0, None
+    if (dweight is not None or dbias is not None) and rows:
+        if workspace is None:
+            workspace = torch.empty(qkv_cte_layer_norm_backward_workspace(rows, cols), dtype=torch.uint8, device=dev)
+            made.append(workspace)
+        ws_bytes = workspace.numel()
+        pws = _vector("workspace", workspace, (torch.uint8,), dev, ws_bytes)
+    _kept(stream, dev, *made)
+    _launch(_lib().qkv_cte_layer_norm_backward, dev, stream, pg, ldg, px, ldx, pw, pm, pr, pd, ldd, pdw, pdb, rows,
+            cols, _DTYPE[x.dtype], _DTYPE[pdt], pws, ws_bytes)
+    return dx, dweight, dbias
+
+
+class QkvCteRopeAxes:
+    """Rotary positions with several axes: a plan for heads of `d_head` lanes of which
+    axis i turns `axis_dims[i]`.
+
+    >>> rope = QkvCteRopeAxes(128, (44, 42, 42))
+    >>> cos, sin = rope.tables(1, 32760, grids=grids)      # what QkvCte takes
+    >>> k = rope(k, positions=positions)                   # a tensor of its own
+
+    A row stands either at positions[s] (int32 [S, axes], or [B, S, axes]) or at the s-th
+    point of its batch's grid (grids: int32 [B, axes], last axis fastest; rows behind the
+    grid's end are padding and not rotated).
+    """
+
+    def __init__(self, d_head: int, axis_dims: Sequence[int], theta: float = 10000.0,
+                 spectrum: int = QKV_CTE_ROPE_PER_AXIS, pairing: int = QKV_CTE_ROPE_ROTATE_HALF):
+        self.plan = None
+        dims = [int(v) for v in axis_dims]
+        desc = qkv_cte_rope_desc(d_head, len(dims), (ctypes.c_int32 * 4)(*dims[:4]), spectrum, pairing, theta)
+        plan = ctypes.c_void_p()
+        _check(_lib().qkv_cte_rope_plan(ctypes.byref(plan), ctypes.byref(desc)))
+        self.plan = plan
+        self.d_head, self.n_axes = d_head, len(dims)
+
+    def _where(self, batch, seq, positions, grids, device):
+        if (positions is None) == (grids is None):
+            raise ValueError("give positions or grids (one of them)")
+        if grids is not None:
+            return None, 0, _vector("grids", grids, (torch.int32,), device, batch * self.n_axes)
+        one = seq * self.n_axes
+        per_batch = isinstance(positions, torch.Tensor) and positions.dim() == 3
+        p = _vector("positions", positions, (torch.int32,), device, one * batch if per_batch else one)
+        return p, one if per_batch else 0, None
+
+    def tables(self, batch: int, seq: int, positions=None, grids=None, cos=None, sin=None, stream=None):
+        """(cos, sin): fp32 [batch * seq, d_head], allocated here when not given."""
+        where = grids if grids is not None else positions
+        if not isinstance(where, torch.Tensor):
+            raise ValueError("give positions or grids (one of them)")
+        dev = where.device
+        p, stride, g = self._where(batch, seq, positions, grids, dev)
+        made = []
+        if cos is None:
+            cos = torch.empty(batch * seq, self.d_head, dtype=torch.float32, device=dev)
+            made.append(cos)
+        if sin is None:
+            sin = torch.empty(batch * seq, self.d_head, dtype=torch.float32, device=dev)
+            made.append(sin)
+        n = batch * seq * self.d_head
+        pc, ps = _vector("cos", cos, (torch.float32,), dev, n), _vector("sin", sin, (torch.float32,), dev, n)
+        _kept(stream, dev, *made)
+        _launch(_lib().qkv_cte_rope_tables, dev, stream, self.plan, batch, seq, p, stride, g, pc, ps)
+        return cos, sin
+
+    def __call__(self, x, positions=None, grids=None, out=None, inverse=False, stream=None):
+        """x [B, S, heads, d_head] or [S, heads, d_head] rotated (turned back with
+        `inverse`: the rotation's gradient); any strides with contiguous lanes. `out` may be x."""
+        _tensor("x", x, _DTYPE)
+        if x.dim() not in (3, 4) or x.shape[-1] != self.d_head:
+            raise ValueError(f"x: expected [B, S, heads, {self.d_head}] or [S, heads, {self.d_head}], "
+                             f"got {tuple(x.shape)}")
+        dev = x.device
+        made = out is None
+        if made:
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        _tensor("out", out, (x.dtype,), dev)
+        if out.shape != x.shape:
+            raise ValueError(f"out: shape {tuple(out.shape)} is not {tuple(x.shape)}")
+        for name, t in (("x", x), ("out", out)):
+            if t.stride(-1) != 1:
+                raise ValueError(f"{name}: the last dimension must be contiguous")
+        batch = x.shape[0] if x.dim() == 4 else 1
+        seq, heads = x.shape[-3], x.shape[-2]
+        p, stride, g = self._where(batch, seq, positions, grids, dev)
+        sx, sy = x.stride(), out.stride()
+        bx, by = (sx[0], sy[0]) if x.dim() == 4 else (0, 0)
+        if made:
+            _kept(stream, dev, out)
+        _launch(_lib().qkv_cte_rope_apply, dev, stream, self.plan, x.data_ptr(), bx, sx[-3], sx[-2], out.data_ptr(),
+                by, sy[-3], sy[-2], batch, seq, heads, p, stride, g, _DTYPE[x.dtype], 1 if inverse else 0)
+        return out
+
+    def close(self):
+        if self.plan is not None:
+            _lib().qkv_cte_rope_destroy(self.plan)
+            self.plan = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

@@ -1,0 +1,80 @@
+// Internal interfaces of the block operators (layer norm, rotary positions with several
+// axes, the product with its epilogue): arguments and launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace qkvcte {
+
+// Layer norm. Strides are in elements; the types of x/y and of the parameters are
+// QKV_CTE_DTYPE_* values.
+struct LayerNormArgs {
+  const void* x;
+  long long ldx;
+  const void* weight;  // [cols] or null: 1
+  const void* bias;    // [cols] or null: 0
+  void* y;
+  long long ldy;
+  float* mean;  // [rows] or null
+  float* rstd;  // [rows] or null
+  long long rows;
+  int cols;
+  float eps;
+};
+
+struct LayerNormGradArgs {
+  const void* dy;
+  long long lddy;
+  const void* x;
+  long long ldx;
+  const void* weight;  // [cols] or null: 1
+  const float* mean;
+  const float* rstd;
+  void* dx;  // or null
+  long long lddx;
+  void* dweight;  // [cols] or null
+  void* dbias;    // [cols] or null
+  float* partial;  // [parts][2][cols] column sums of each block, or null: no dweight or dbias
+  int max_parts;
+  long long rows;
+  int cols;
+};
+
+// Blocks whose column sums the backward pass keeps apart (bounds its workspace).
+constexpr int kLayerNormMaxParts = 608;
+
+cudaError_t launch_layer_norm(const LayerNormArgs& a, int dtype, int param_dtype, cudaStream_t s, int num_sms);
+// `sums`: dweight and/or dbias are wanted (with no rows they are zeros).
+cudaError_t launch_layer_norm_backward(const LayerNormGradArgs& a, int dtype, int param_dtype, bool sums,
+                                       cudaStream_t s, int num_sms);
+
+// Rotary positions with several axes.
+constexpr int kRopeMaxAxes = 4;
+constexpr int kRopeMaxPairs = 256;
+
+// What a plan fixes: the head's pairs, their axes and steps.
+struct RopePairs {
+  int d, n_axes;
+  int first_pair[kRopeMaxAxes];               // first pair of each axis
+  unsigned long long step[kRopeMaxPairs];     // turns per position, as a binary fraction of a turn
+};
+
+struct RopeArgs : RopePairs {
+  int batch, seq, heads;
+  const int* positions;         // [seq, n_axes] per batch, or null
+  long long pos_batch_stride;   // 0: one set for every batch
+  const int* grids;             // [batch, n_axes], or null
+  const void* x;
+  void* y;
+  long long xb, xs, xh, yb, ys, yh;  // strides of batch, row and head in elements
+  int inverse;
+};
+
+cudaError_t launch_rope_apply(const RopeArgs& a, int dtype, bool rotate_half, cudaStream_t s);
+// cos_t, sin_t: fp32 [batch * seq, d], 8-byte aligned for interleaved pairs.
+cudaError_t launch_rope_tables(const RopeArgs& a, float* cos_t, float* sin_t, bool rotate_half, cudaStream_t s);
+
+}  // namespace qkvcte

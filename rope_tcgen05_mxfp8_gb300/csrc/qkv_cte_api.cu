@@ -12,6 +12,7 @@
 #include <mutex>
 #include <new>
 
+#include "api_common.h"
 #include "internal.h"
 #include "qkv_cte.h"
 
@@ -43,10 +44,13 @@ struct qkv_cte_plan_s {
 };
 
 namespace {
-
 thread_local char g_last_error[512] = "";
+}  // namespace
 
-__attribute__((format(printf, 2, 3))) int fail(int code, const char* fmt, ...) {
+// Helpers shared with the other front ends (api_common.h).
+namespace qkvcte {
+
+int fail(int code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
@@ -59,12 +63,9 @@ int ok() {
   return QKV_CTE_OK;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace qkvcte
 
-struct DeviceInfo {
-  bool init = false;
-  int major = 0, minor = 0, sms = 0;
-};
+namespace {
 
 constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
@@ -102,6 +103,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+}  // namespace
+
+namespace qkvcte {
+
 // 2D K-major uint8 operand [rows, cols], tiles of box_rows x 128 bytes, 128-byte swizzle.
 int encode_operand(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows,
                    const char* what) {
@@ -134,6 +139,24 @@ int encode_scales(CUtensorMap* m, void* base, const GemmShape& g) {
   if (r != CUDA_SUCCESS) return fail(QKV_CTE_ERR_CUDA, "cuTensorMapEncodeTiled(scales) failed: %d", int(r));
   return QKV_CTE_OK;
 }
+
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+int check_device(DeviceInfo* dev) {
+  int rc = device_info(dev);
+  if (rc != QKV_CTE_OK) return rc;
+  if (!(dev->major == 10 && dev->minor == 3))
+    return fail(QKV_CTE_ERR_ARCH, "device is sm_%d%d; this library is built for sm_103a", dev->major, dev->minor);
+  return QKV_CTE_OK;
+}
+
+}  // namespace qkvcte
+
+namespace {
 
 // N tiles per band: the band's W slab (tile_n * H bytes per N tile) is kept to about
 // 28 MB so that it stays resident in the 129 MB L2 beside the streaming traffic
@@ -575,25 +598,11 @@ int qkv_cte_status(void* workspace, void* stream) {
 
 namespace {
 
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
-
 int check_rows(int64_t tokens, int32_t hidden, const char* who) {
   if (tokens < 0) return fail(QKV_CTE_ERR_INVALID, "%s: tokens must be >= 0", who);
   if (tokens > INT32_MAX) return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: tokens > INT32_MAX", who);
   if (hidden <= 0) return fail(QKV_CTE_ERR_INVALID, "%s: hidden must be > 0", who);
   if (hidden % 16 != 0) return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: hidden %d is not a multiple of 16", who, hidden);
-  return QKV_CTE_OK;
-}
-
-int check_device(DeviceInfo* dev) {
-  int rc = device_info(dev);
-  if (rc != QKV_CTE_OK) return rc;
-  if (!(dev->major == 10 && dev->minor == 3))
-    return fail(QKV_CTE_ERR_ARCH, "device is sm_%d%d; this library is built for sm_103a", dev->major, dev->minor);
   return QKV_CTE_OK;
 }
 
