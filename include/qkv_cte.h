@@ -456,6 +456,55 @@ int qkv_cte_rope_apply(qkv_cte_rope_plan_t plan, const void* x, int64_t x_batch_
                        int64_t y_head_stride, int64_t batch, int64_t seq, int32_t heads, const int32_t* positions,
                        int64_t pos_batch_stride, const int32_t* grids, int32_t dtype, int32_t inverse, void* stream);
 
+/* The product with its epilogue, on the projection's operands:
+ *   O[t, n] = residual[t, n] + gate[n] * act(z[t, n]),
+ *   z[t, n] = (sum_k A[t, k] W[n, k]) * a_scale[t] * w_col_scale[n] + bias[n]
+ * for the output projection (bias, gate, residual), the feed-forward layers (GELU; gate
+ * and residual) and the embeddings (SiLU). Sums, activation and epilogue are fp32, O is
+ * rounded once. Any number of tokens from one on and any output width are taken. */
+enum { QKV_CTE_ACT_NONE = 0,
+       QKV_CTE_ACT_GELU_TANH = 1, /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+       QKV_CTE_ACT_GELU_ERF = 2,  /* 0.5 z (1 + erf(z / sqrt(2))) */
+       QKV_CTE_ACT_SILU = 3 };    /* z / (1 + exp(-z)) */
+
+typedef struct {
+    int64_t tokens;       /* T >= 0, <= INT32_MAX */
+    int32_t in_features;  /* K: a multiple of 32 */
+    int32_t out_features; /* N >= 1 */
+    int32_t act;          /* QKV_CTE_ACT_* */
+    int32_t out_dtype;    /* QKV_CTE_DTYPE_*: of O and of the residual */
+    int32_t input_layout; /* QKV_CTE_INPUT_*: what A holds, as for qkv_cte_run */
+    uint32_t flags;       /* 0 or QKV_CTE_FLAG_TEST_STALL */
+} qkv_cte_linear_desc;
+
+typedef struct qkv_cte_linear_plan_s* qkv_cte_linear_plan_t;
+
+/* Validate `desc` (host only), create a plan and report the workspace a run needs. The
+ * plan holds host memory only. Returns 0, -1, or -2 (in_features % 32, sizes). */
+int qkv_cte_linear_plan(qkv_cte_linear_plan_t* out, const qkv_cte_linear_desc* desc, size_t* workspace_bytes);
+
+/* Release a plan. NULL is a no-op. */
+void qkv_cte_linear_destroy(qkv_cte_linear_plan_t plan);
+
+/* A, a_scale  : as for qkv_cte_run with the plan's input layout ([T, K])
+ * W, w_sf     : uint8 [N, K] e4m3 codes (16-byte aligned) and uint8 [N, K/32] UE8M0 block
+ *               scales (4-byte aligned)
+ * w_col_scale : fp32 [N] or NULL; bias, gate: bf16 [N] or NULL; all 16-byte aligned
+ * residual    : out_dtype [T, N], rows residual_row_stride elements apart (0: one row for
+ *               all), or NULL
+ * O           : out_dtype [T, N], rows out_row_stride elements apart; may be the residual
+ *               itself (same pointer and stride) and overlaps nothing else. Rows of O and of
+ *               the residual that start on 32-byte boundaries run fastest.
+ * workspace   : device scratch of the planned size, 256-byte aligned, holding zeros before
+ *               its first use; runs that overlap on the GPU must not share it. Its first word
+ *               is the status word of qkv_cte_status, which a run sets but never clears.
+ * Stream-ordered, asynchronous, allocates nothing. tokens == 0 launches nothing. Returns
+ * 0, -1, -2, -3 or -4. */
+int qkv_cte_linear_run(qkv_cte_linear_plan_t plan, const void* A, const float* a_scale, const uint8_t* W,
+                       const uint8_t* w_sf, const float* w_col_scale, const uint16_t* bias, const uint16_t* gate,
+                       const void* residual, int64_t residual_row_stride, void* O, int64_t out_row_stride,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
 /* Release a plan. NULL is a no-op. */
 void qkv_cte_destroy(qkv_cte_plan_t plan);
 

@@ -18,7 +18,8 @@ from .qkv_cte import (  # noqa: F401
     qkv_cte_status, qkv_cte_version,
 )
 from .block_ops import (  # noqa: F401
-    QKV_CTE_DTYPE_BF16, QKV_CTE_DTYPE_FP16, QKV_CTE_DTYPE_FP32, QKV_CTE_ROPE_INTERLEAVED, QKV_CTE_ROPE_PER_AXIS,
-    QKV_CTE_ROPE_ROTATE_HALF, QKV_CTE_ROPE_SHARED, QkvCteRopeAxes, qkv_cte_layer_norm, qkv_cte_layer_norm_backward,
-    qkv_cte_layer_norm_backward_workspace, qkv_cte_rope_desc,
+    QKV_CTE_ACT_GELU_ERF, QKV_CTE_ACT_GELU_TANH, QKV_CTE_ACT_NONE, QKV_CTE_ACT_SILU, QKV_CTE_DTYPE_BF16, QKV_CTE_DTYPE_FP16, QKV_CTE_DTYPE_FP32, QKV_CTE_ROPE_INTERLEAVED, QKV_CTE_ROPE_PER_AXIS,
+    QKV_CTE_ROPE_ROTATE_HALF, QKV_CTE_ROPE_SHARED, QkvCteLinear, QkvCteRopeAxes, qkv_cte_layer_norm,
+    qkv_cte_layer_norm_backward,
+    qkv_cte_layer_norm_backward_workspace, qkv_cte_linear_desc, qkv_cte_rope_desc,
 )

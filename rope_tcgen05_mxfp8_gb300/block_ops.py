@@ -1,5 +1,6 @@
 """Bindings of the operators around the projection (see include/qkv_cte.h): layer norm
-with its backward pass and rotary positions with several axes.
+with its backward pass, rotary positions with several axes and the product with bias,
+activation, gate and residual.
 
 Argument marshalling only, as in qkv_cte.py: every computation runs in the library's
 kernels. Tensors live on one CUDA device, which need not be the current one; a call
@@ -12,7 +13,8 @@ from typing import Optional, Sequence
 
 import torch
 
-from .qkv_cte import _check, load
+from .qkv_cte import (QKV_CTE_INPUT_BF16, QKV_CTE_INPUT_PACKED, QKV_CTE_INPUT_ROW_FP8, _check, load,
+                      qkv_cte_status)
 
 QKV_CTE_DTYPE_BF16 = 0
 QKV_CTE_DTYPE_FP16 = 1
@@ -21,6 +23,10 @@ QKV_CTE_ROPE_PER_AXIS = 0
 QKV_CTE_ROPE_SHARED = 1
 QKV_CTE_ROPE_ROTATE_HALF = 0
 QKV_CTE_ROPE_INTERLEAVED = 1
+QKV_CTE_ACT_NONE = 0
+QKV_CTE_ACT_GELU_TANH = 1
+QKV_CTE_ACT_GELU_ERF = 2
+QKV_CTE_ACT_SILU = 3
 
 _DTYPE = {torch.bfloat16: QKV_CTE_DTYPE_BF16, torch.float16: QKV_CTE_DTYPE_FP16, torch.float32: QKV_CTE_DTYPE_FP32}
 
@@ -33,6 +39,18 @@ class qkv_cte_rope_desc(ctypes.Structure):
         ("spectrum", ctypes.c_int32),
         ("pairing", ctypes.c_int32),
         ("theta", ctypes.c_double),
+    ]
+
+
+class qkv_cte_linear_desc(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("in_features", ctypes.c_int32),
+        ("out_features", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("input_layout", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
     ]
 
 
@@ -54,10 +72,14 @@ def _lib() -> ctypes.CDLL:
     lib.qkv_cte_rope_destroy.argtypes = [P]
     lib.qkv_cte_rope_tables.argtypes = [P, I64, I64, P, I64, P, P, P, P]
     lib.qkv_cte_rope_apply.argtypes = [P, P, I64, I64, I64, P, I64, I64, I64, I64, I64, I32, P, I64, P, I32, I32, P]
+    lib.qkv_cte_linear_plan.argtypes = [ctypes.POINTER(P), ctypes.POINTER(qkv_cte_linear_desc), ctypes.POINTER(SIZE)]
+    lib.qkv_cte_linear_destroy.argtypes = [P]
+    lib.qkv_cte_linear_run.argtypes = [P] * 9 + [I64, P, I64, P, SIZE, P]
     for name in ("layer_norm", "layer_norm_backward", "layer_norm_backward_workspace", "rope_plan", "rope_tables",
-                 "rope_apply"):
+                 "rope_apply", "linear_plan", "linear_run"):
         getattr(lib, "qkv_cte_" + name).restype = ctypes.c_int
     lib.qkv_cte_rope_destroy.restype = None
+    lib.qkv_cte_linear_destroy.restype = None
     _bound = lib
     return lib
 
@@ -291,6 +313,78 @@ class QkvCteRopeAxes:
     def close(self):
         if self.plan is not None:
             _lib().qkv_cte_rope_destroy(self.plan)
+            self.plan = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+_BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
+
+
+class QkvCteLinear:
+    """The product with bias, activation, gate and residual: a plan plus its workspace on
+    one device.
+
+    >>> op = QkvCteLinear(tokens, 5120, 20480, act=QKV_CTE_ACT_GELU_TANH, input_layout=QKV_CTE_INPUT_BF16)
+    >>> h = op(x, None, W, w_sf, bias=b)
+    >>> x = out_proj(A, a_scale, W, w_sf, bias=b, gate=g, residual=x, out=x)
+
+    A, a_scale, W and w_sf are the operands of QkvCte; `residual` and `out` are [T, N] of
+    `out_dtype` with contiguous rows (strided rows are fine, and `out` may be `residual`).
+    Calls that overlap on the GPU need an object each: they would share the workspace.
+    """
+
+    def __init__(self, tokens: int, in_features: int, out_features: int, act: int = QKV_CTE_ACT_NONE,
+                 out_dtype=torch.bfloat16, input_layout: int = QKV_CTE_INPUT_ROW_FP8, device=None, flags: int = 0):
+        self.plan = None
+        if out_dtype not in _DTYPE:
+            raise TypeError(f"out_dtype: {out_dtype} not in {tuple(_DTYPE)}")
+        desc = qkv_cte_linear_desc(tokens, in_features, out_features, act, _DTYPE[out_dtype], input_layout, flags)
+        plan, n = ctypes.c_void_p(), ctypes.c_size_t()
+        _check(_lib().qkv_cte_linear_plan(ctypes.byref(plan), ctypes.byref(desc), ctypes.byref(n)))
+        self.plan, self.workspace_bytes = plan, n.value
+        self.shape, self.in_features, self.out_dtype, self.input_layout = (
+            (tokens, out_features), in_features, out_dtype, input_layout)
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if dev.index is None:
+            dev = torch.device(dev.type, torch.cuda.current_device())
+        self.device = dev
+        self.workspace = torch.zeros(max(self.workspace_bytes, 256), dtype=torch.uint8, device=dev)
+
+    def __call__(self, A, a_scale, W, w_sf, bias=None, gate=None, residual=None, out=None, w_col_scale=None,
+                 stream=None):
+        (T, N), K, dev = self.shape, self.in_features, self.device
+        layout = self.input_layout
+        pa = _vector("A", A, _BF16_BITS if layout == QKV_CTE_INPUT_BF16 else (torch.uint8,), dev,
+                     T * (K + 4 if layout == QKV_CTE_INPUT_PACKED else K))
+        ps = _vector("a_scale", a_scale, (torch.float32,), dev, T)
+        pw = _vector("W", W, (torch.uint8,), dev, N * K)
+        pf = _vector("w_sf", w_sf, (torch.uint8,), dev, N * (K // 32))
+        pc = _vector("w_col_scale", w_col_scale, (torch.float32,), dev, N)
+        pb = _vector("bias", bias, _BF16_BITS, dev, N)
+        pg = _vector("gate", gate, _BF16_BITS, dev, N)
+        pr, ldr = _rows("residual", residual, (self.out_dtype,), dev, (T, N)) if residual is not None else (None, 0)
+        if out is None:
+            out = torch.empty(T, N, dtype=self.out_dtype, device=dev)
+            _kept(stream, dev, out)
+        po, ldo = _rows("out", out, (self.out_dtype,), dev, (T, N))
+        _launch(_lib().qkv_cte_linear_run, dev, stream, self.plan, pa, ps, pw, pf, pc, pb, pg, pr, ldr, po, ldo,
+                self.workspace.data_ptr(), self.workspace.numel())
+        return out
+
+    def status(self, stream=None) -> int:
+        """Synchronise and raise QkvCteError if a bounded device wait of a run since the
+        last call ran out."""
+        with torch.cuda.device(self.device):
+            return qkv_cte_status(self.workspace, stream)
+
+    def close(self):
+        if self.plan is not None:
+            _lib().qkv_cte_linear_destroy(self.plan)
             self.plan = None
 
     def __del__(self):

@@ -30,11 +30,20 @@ int check_device(DeviceInfo* dev);
 // Whether [a, a + na) and [b, b + nb) share a byte (null or empty: no).
 bool overlaps(const void* a, size_t na, const void* b, size_t nb);
 
+// Whether two blocks of `rows` rows share a byte: rows of a_row (b_row, or the same) bytes,
+// a_stride and b_stride bytes apart. Blocks of one stride whose rows lie side by side (two
+// column ranges of one wide tensor) do not.
+bool strided_rows_overlap(const void* a, int64_t a_stride, const void* b, int64_t b_stride, int64_t rows,
+                          int64_t a_row, int64_t b_row = 0);
+
 // 2D K-major uint8 operand [rows, cols], tiles of box_rows x 128 bytes, 128-byte swizzle.
 int encode_operand(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows,
                    const char* what);
 // The repacked weight scales of `g` (see launch_prep), one 128-byte K block per box.
 struct GemmShape;
 int encode_scales(CUtensorMap* m, void* base, const GemmShape& g);
+
+// N tiles per band of the GEMM's tile order.
+int band_tiles(const GemmShape& g);
 
 }  // namespace qkvcte

@@ -77,4 +77,16 @@ cudaError_t launch_rope_apply(const RopeArgs& a, int dtype, bool rotate_half, cu
 // cos_t, sin_t: fp32 [batch * seq, d], 8-byte aligned for interleaved pairs.
 cudaError_t launch_rope_tables(const RopeArgs& a, float* cos_t, float* sin_t, bool rotate_half, cudaStream_t s);
 
+// The product's epilogue beyond scale and bias (see linear_epilogue.cuh).
+struct LinearEpilogue {
+  int act;                // QKV_CTE_ACT_*
+  int dtype;              // of the residual and the output
+  const uint16_t* gate;   // [N] bf16, or null
+  const void* residual;   // or null
+  long long ldr;
+  void* out;
+  long long ldo;
+  int wide;               // residual and output rows start on 32-byte boundaries
+};
+
 }  // namespace qkvcte

@@ -32,14 +32,8 @@ struct Rows {
   size_t extent() const { return rows > 0 ? (size_t)((rows - 1) * stride + row_bytes) : 0; }
 };
 
-// Whether two row blocks share a byte. Blocks of one stride whose rows lie side by side
-// (two column ranges of one wide tensor) do not.
 bool rows_overlap(const Rows& a, const Rows& b) {
-  if (!overlaps(a.p, a.extent(), b.p, b.extent())) return false;
-  if (a.stride != b.stride || a.stride <= 0) return true;
-  const intptr_t d = (intptr_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
-  const int64_t m = ((d % a.stride) + a.stride) % a.stride;  // b's offset within a's row pitch
-  return m < a.row_bytes || a.stride - m < b.row_bytes;
+  return strided_rows_overlap(a.p, a.stride, b.p, b.stride, a.rows, a.row_bytes, b.row_bytes);
 }
 
 bool same_rows(const Rows& a, const Rows& b) { return a.p == b.p && (a.stride == b.stride || a.rows <= 1); }

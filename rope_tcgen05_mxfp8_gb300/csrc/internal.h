@@ -7,6 +7,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "block_ops.h"
+
 namespace qkvcte {
 
 // Device status word bits (workspace word 0): which bounded wait ran out.
@@ -192,6 +194,7 @@ struct GemmArgs {
   int stats_kind;
   float* head_stats;
   int stat_parts;
+  LinearEpilogue lin;        // the product's epilogue (kEpiLinear only; O is unused then)
 };
 
 // Element (row t, column c) of O in either layout (c and the 16 columns after it
@@ -265,6 +268,9 @@ cudaError_t launch_gemm(const GemmShape& g, const CUtensorMap& tmA, const CUtens
 // (qkv_gemm_mxf8_head.cu); launch_gemm calls it when a.head_norm or a.stats_kind is set.
 cudaError_t launch_gemm_head(const GemmShape& g, const CUtensorMap& tmA, const CUtensorMap& tmW,
                              const CUtensorMap& tmSF, const GemmArgs& a, cudaStream_t s, int num_sms);
+// K1 (CTA-pair form) with the product's epilogue (qkv_gemm_mxf8_linear.cu).
+cudaError_t launch_gemm_linear(const GemmShape& g, const CUtensorMap& tmA, const CUtensorMap& tmW,
+                               const CUtensorMap& tmSF, const GemmArgs& a, cudaStream_t s, int num_sms);
 // K1 (CTA-pair form) with the norm/RoPE tasks run by its epilogue warps
 // (qkv_gemm_mxf8_fused.cu); launch_gemm calls it when given `fused`.
 cudaError_t launch_gemm_fused(const GemmShape& g, const CUtensorMap& tmA, const CUtensorMap& tmW,

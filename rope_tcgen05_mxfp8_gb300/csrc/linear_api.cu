@@ -1,0 +1,202 @@
+// C-ABI front end of the product with bias, activation, gate and residual
+// (qkv_cte_linear_*, documented in qkv_cte.h): plan, workspace, tensor maps, launches.
+#include <climits>
+#include <new>
+
+#include "api_common.h"
+#include "internal.h"
+#include "qkv_cte.h"
+
+using namespace qkvcte;
+
+namespace {
+
+// Workspace (256-byte aligned offsets): [0, 256) the status word and the GEMM's counters
+// and stamps at the offsets of internal.h, and a word the scale repack clears in the
+// status word's place (a run leaves the status of earlier runs alone); then W's repacked
+// scales, the counters K1 expects, and the producer step's codes and row scales.
+constexpr size_t kSpareWordOffset = 136;
+
+struct LinearLayout {
+  size_t sf_off, ready_off, sm_busy_off, act_off, act_scale_off, total;
+};
+
+}  // namespace
+
+struct qkv_cte_linear_plan_s {
+  qkv_cte_linear_desc d;
+  GemmShape g;
+  LinearLayout ws;
+};
+
+namespace {
+
+size_t out_size(const qkv_cte_linear_desc& d) { return d.out_dtype == QKV_CTE_DTYPE_FP32 ? 4 : 2; }
+
+}  // namespace
+
+extern "C" {
+
+int qkv_cte_linear_plan(qkv_cte_linear_plan_t* out, const qkv_cte_linear_desc* desc, size_t* workspace_bytes) {
+  const char* who = "qkv_cte_linear_plan";
+  if (out == nullptr || desc == nullptr || workspace_bytes == nullptr)
+    return fail(QKV_CTE_ERR_INVALID, "%s: null argument", who);
+  *out = nullptr;
+  const qkv_cte_linear_desc& d = *desc;
+  if (d.tokens < 0) return fail(QKV_CTE_ERR_INVALID, "%s: tokens must be >= 0 (got %lld)", who, (long long)d.tokens);
+  if (d.tokens > INT32_MAX) return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: tokens > INT32_MAX", who);
+  if (d.in_features <= 0 || d.out_features <= 0)
+    return fail(QKV_CTE_ERR_INVALID, "%s: in_features and out_features must be > 0", who);
+  if (d.in_features % 32 != 0)
+    return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: in_features %d is not a multiple of 32", who, d.in_features);
+  if (d.out_features > INT32_MAX / 2) return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: out_features too large", who);
+  if (d.act < QKV_CTE_ACT_NONE || d.act > QKV_CTE_ACT_SILU)
+    return fail(QKV_CTE_ERR_INVALID, "%s: unknown activation %d", who, d.act);
+  if (d.out_dtype < QKV_CTE_DTYPE_BF16 || d.out_dtype > QKV_CTE_DTYPE_FP32)
+    return fail(QKV_CTE_ERR_INVALID, "%s: unknown output type %d", who, d.out_dtype);
+  if (d.input_layout != QKV_CTE_INPUT_ROW_FP8 && d.input_layout != QKV_CTE_INPUT_PACKED &&
+      d.input_layout != QKV_CTE_INPUT_BF16)
+    return fail(QKV_CTE_ERR_INVALID, "%s: unknown input layout %d", who, d.input_layout);
+  if ((d.flags & ~QKV_CTE_FLAG_TEST_STALL) != 0) return fail(QKV_CTE_ERR_INVALID, "%s: unknown flags 0x%x", who, d.flags);
+  qkv_cte_linear_plan_s* p = new (std::nothrow) qkv_cte_linear_plan_s();
+  if (p == nullptr) return fail(QKV_CTE_ERR_INVALID, "out of host memory");
+  p->d = d;
+  GemmShape& g = p->g;
+  g.T = (int)d.tokens;
+  g.H = d.in_features;
+  g.I = d.out_features;
+  g.tile_n = 240;
+  g.cta_pair = 1;
+  g.blocks128 = (g.T + 127) / 128;
+  g.m_tiles = (g.T + 255) / 256;
+  g.n_tiles = (g.I + g.tile_n - 1) / g.tile_n;
+  g.k_stages = (g.H + 127) / 128;  // a short last K block reads zeros past the row's end
+  if ((long long)g.m_tiles * g.n_tiles > INT32_MAX) {
+    delete p;
+    return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: too many output tiles", who);
+  }
+  g.sf_chunks = gemm_sf_chunks(g.tile_n);
+  g.n_qk_tiles = 0;
+  make_bands(g, band_tiles(g));
+  LinearLayout& w = p->ws;
+  w.sf_off = 256;
+  w.ready_off = w.sf_off + align_up((size_t)g.n_tiles * g.k_stages * g.sf_chunks * kSfBlockBytesPerChunk, 256);
+  w.sm_busy_off = w.ready_off + align_up((size_t)g.blocks128 * sizeof(uint32_t), 256);
+  w.act_off = w.sm_busy_off + align_up((size_t)kSmTable * sizeof(uint32_t), 256);
+  const bool produced = d.input_layout != QKV_CTE_INPUT_ROW_FP8;
+  w.act_scale_off = w.act_off + (produced ? align_up((size_t)g.T * g.H, 256) : 0);
+  w.total = w.act_scale_off + (produced ? align_up((size_t)g.T * sizeof(float), 256) : 0);
+  *workspace_bytes = w.total;
+  *out = p;
+  return ok();
+}
+
+void qkv_cte_linear_destroy(qkv_cte_linear_plan_t plan) { delete plan; }
+
+int qkv_cte_linear_run(qkv_cte_linear_plan_t plan, const void* A, const float* a_scale, const uint8_t* W,
+                       const uint8_t* w_sf, const float* w_col_scale, const uint16_t* bias, const uint16_t* gate,
+                       const void* residual, int64_t residual_row_stride, void* O, int64_t out_row_stride,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "qkv_cte_linear_run";
+  if (plan == nullptr) return fail(QKV_CTE_ERR_INVALID, "%s: null plan", who);
+  const qkv_cte_linear_desc& d = plan->d;
+  const GemmShape& g = plan->g;
+  if (g.T == 0) return ok();
+  const bool produced = d.input_layout != QKV_CTE_INPUT_ROW_FP8;
+  if (!A || !W || !w_sf || !O || !workspace)
+    return fail(QKV_CTE_ERR_INVALID, "%s: A, W, w_sf, O and workspace are required", who);
+  if (!produced && !a_scale) return fail(QKV_CTE_ERR_INVALID, "%s: a_scale is required with separate FP8 rows", who);
+  if (produced && a_scale)
+    return fail(QKV_CTE_ERR_INVALID, "%s: a_scale must be NULL with a packed or bf16 input", who);
+  const int64_t T = g.T, N = g.I, e = (int64_t)out_size(d);
+  if (T > 1 && (out_row_stride < N || (residual && residual_row_stride < N && residual_row_stride != 0)))
+    return fail(QKV_CTE_ERR_INVALID, "%s: a row stride is smaller than out_features", who);
+  if (out_row_stride > INT64_MAX / 8 / T || (residual && residual_row_stride > INT64_MAX / 8 / T))
+    return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: a row stride overflows", who);
+  if (!aligned(A, d.input_layout == QKV_CTE_INPUT_PACKED ? 4 : 16) || !aligned(W, 16))
+    return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: A (but for packed rows: 4) and W must be 16-byte aligned", who);
+  if (!aligned(a_scale, 4) || !aligned(w_sf, 4) || !aligned(O, e) || !aligned(residual, e))
+    return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: a_scale and w_sf must be 4-byte aligned, O and residual to their elements",
+                who);
+  if (!aligned(w_col_scale, 16) || !aligned(bias, 16) || !aligned(gate, 16))
+    return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: w_col_scale, bias and gate must be 16-byte aligned", who);
+  if (!aligned(workspace, 256)) return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: workspace must be 256-byte aligned", who);
+  if (workspace_bytes < plan->ws.total)
+    return fail(QKV_CTE_ERR_INVALID, "%s: workspace of %zu bytes is smaller than the planned %zu", who, workspace_bytes,
+                plan->ws.total);
+  // O may be the residual itself; it shares no byte with anything else that is read or written.
+  const size_t row_bytes = (size_t)(N * e);
+  const size_t o_bytes = (size_t)((T - 1) * (T > 1 ? out_row_stride : 0) * e) + row_bytes;
+  const size_t r_bytes = residual ? (size_t)((T - 1) * (T > 1 ? residual_row_stride : 0) * e) + row_bytes : 0;
+  const size_t a_row = (size_t)g.H * (d.input_layout == QKV_CTE_INPUT_BF16 ? 2 : 1) +
+                       (d.input_layout == QKV_CTE_INPUT_PACKED ? 4 : 0);
+  const struct {
+    const void* p;
+    size_t n;
+  } in[] = {{A, a_row * (size_t)T},  {a_scale, 4 * (size_t)T},      {W, (size_t)N * g.H},
+            {w_sf, (size_t)N * (g.H / 32)}, {w_col_scale, 4 * (size_t)N}, {bias, 2 * (size_t)N},
+            {gate, 2 * (size_t)N}};
+  for (const auto& b : in)
+    if (overlaps(b.p, b.n, O, o_bytes) || overlaps(b.p, b.n, workspace, plan->ws.total))
+      return fail(QKV_CTE_ERR_INVALID, "%s: O or the workspace overlaps an input", who);
+  if (overlaps(O, o_bytes, workspace, plan->ws.total) || overlaps(residual, r_bytes, workspace, plan->ws.total))
+    return fail(QKV_CTE_ERR_INVALID, "%s: the workspace overlaps O or the residual", who);
+  const bool in_place = residual == O && (T == 1 || residual_row_stride == out_row_stride);
+  if (residual && !in_place &&
+      strided_rows_overlap(residual, residual_row_stride * e, O, out_row_stride * e, T, (int64_t)row_bytes))
+    return fail(QKV_CTE_ERR_INVALID, "%s: O overlaps the residual without being the same rows", who);
+
+  DeviceInfo dev;
+  int rc = check_device(&dev);
+  if (rc != QKV_CTE_OK) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const uint8_t* codes = produced ? ws + plan->ws.act_off : static_cast<const uint8_t*>(A);
+  const float* scales = produced ? reinterpret_cast<const float*>(ws + plan->ws.act_scale_off) : a_scale;
+  uint8_t* sf_packed = ws + plan->ws.sf_off;
+  CUtensorMap tmA, tmW, tmSF;
+  if ((rc = encode_operand(&tmA, codes, (uint64_t)g.T, (uint64_t)g.H, 128u, "A")) != QKV_CTE_OK) return rc;
+  if ((rc = encode_operand(&tmW, W, (uint64_t)g.I, (uint64_t)g.H, (uint32_t)g.tile_n / 2, "W")) != QKV_CTE_OK) return rc;
+  if ((rc = encode_scales(&tmSF, sf_packed, g)) != QKV_CTE_OK) return rc;
+
+  cudaError_t err = cudaSuccess;
+  if (d.input_layout == QKV_CTE_INPUT_PACKED)
+    err = launch_unpack_rows(static_cast<const uint8_t*>(A), g.T, g.H, ws + plan->ws.act_off,
+                             reinterpret_cast<float*>(ws + plan->ws.act_scale_off), s, dev.sms);
+  else if (d.input_layout == QKV_CTE_INPUT_BF16)
+    err = launch_row_quantize(static_cast<const uint16_t*>(A), g.T, g.H, ws + plan->ws.act_off,
+                              reinterpret_cast<float*>(ws + plan->ws.act_scale_off), nullptr, s, dev.sms);
+  if (err != cudaSuccess) return fail(QKV_CTE_ERR_CUDA, "%s: producer launch: %s", who, cudaGetErrorString(err));
+  unsigned long long* stamps = reinterpret_cast<unsigned long long*>(ws + kStampOffset);
+  uint32_t* ready = reinterpret_cast<uint32_t*>(ws + plan->ws.ready_off);
+  uint32_t* sm_busy = reinterpret_cast<uint32_t*>(ws + plan->ws.sm_busy_off);
+  err = launch_prep(g, w_sf, sf_packed, nullptr, 0, ready, sm_busy, reinterpret_cast<uint32_t*>(ws + kSpareWordOffset),
+                    stamps, reinterpret_cast<uint32_t*>(ws + kTaskCounterOffset), nullptr, 0, s, dev.sms, produced);
+  if (err != cudaSuccess) return fail(QKV_CTE_ERR_CUDA, "%s: scale repack launch: %s", who, cudaGetErrorString(err));
+  GemmArgs a{};
+  a.a_scale = scales;
+  a.w_col_scale = w_col_scale;
+  a.bias = bias;
+  a.sf_packed = sf_packed;
+  a.ready = ready;
+  a.sm_busy = sm_busy;
+  a.stamps = stamps;
+  a.tile_next = reinterpret_cast<uint32_t*>(ws + kTileCounterOffset);
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.flags = d.flags;
+  a.d_head = 16;
+  a.lin.act = d.act;
+  a.lin.dtype = d.out_dtype;
+  a.lin.gate = gate;
+  a.lin.residual = residual;
+  a.lin.ldr = T > 1 ? residual_row_stride : 0;
+  a.lin.out = O;
+  a.lin.ldo = T > 1 ? out_row_stride : 0;
+  a.lin.wide = aligned(O, 32) && (a.lin.ldo * e) % 32 == 0 &&
+               (!residual || (aligned(residual, 32) && (a.lin.ldr * e) % 32 == 0));
+  err = launch_gemm_linear(g, tmA, tmW, tmSF, a, s, dev.sms);
+  if (err != cudaSuccess) return fail(QKV_CTE_ERR_CUDA, "%s: GEMM launch: %s", who, cudaGetErrorString(err));
+  return ok();
+}
+
+}  // extern "C"

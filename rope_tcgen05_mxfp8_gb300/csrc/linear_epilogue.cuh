@@ -1,0 +1,163 @@
+// The product's epilogue: O = residual + gate * act(z), z = acc * scale + bias, on 16
+// columns of one row at a time.
+#pragma once
+
+#include "block_ops.h"
+#include "ptx.cuh"
+#include "qkv_cte.h"
+#include "vec_io.cuh"
+
+namespace qkvcte {
+
+// act(z). The exponentials are ex2.approx of a rounded product: their relative error is
+// about 2^-22 plus 2^-24 |argument|, and z / (1 + e) inherits it only in so far as e
+// counts beside 1, so act is within 2^-20 |z| for any argument that does not vanish.
+// e = inf gives the limit -0.
+__device__ __forceinline__ float apply_act(float z, int act) {
+  switch (act) {
+    case QKV_CTE_ACT_GELU_TANH: {
+      // 0.5 z (1 + tanh u) = z / (1 + exp(-2 u)), u = sqrt(2/pi) (z + 0.044715 z^3)
+      const float u2 = -1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.0f);
+      return __fdividef(z, 1.0f + __expf(u2));
+    }
+    case QKV_CTE_ACT_GELU_ERF: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    case QKV_CTE_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
+    default: return z;
+  }
+}
+
+__device__ __forceinline__ float load_any(const void* p, long long i, int dtype) {
+  switch (dtype) {
+    case QKV_CTE_DTYPE_BF16: return to_f32(static_cast<const __nv_bfloat16*>(p)[i]);
+    case QKV_CTE_DTYPE_FP16: return to_f32(static_cast<const __half*>(p)[i]);
+    default: return static_cast<const float*>(p)[i];
+  }
+}
+
+__device__ __forceinline__ void store_any(void* p, long long i, int dtype, float v) {
+  switch (dtype) {
+    case QKV_CTE_DTYPE_BF16: static_cast<__nv_bfloat16*>(p)[i] = from_f32<__nv_bfloat16>(v); break;
+    case QKV_CTE_DTYPE_FP16: static_cast<__half*>(p)[i] = from_f32<__half>(v); break;
+    default: static_cast<float*>(p)[i] = v;
+  }
+}
+
+// 32-byte global load. Not the read-only path: the residual may be the output itself.
+__device__ __forceinline__ void ld_global_v8_b32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+
+// 16 residual elements of a row as raw words (8 for 2-byte types, 16 for fp32).
+__device__ __forceinline__ void load_residual16(const LinearEpilogue& e, long long row, int col0, uint32_t* r) {
+  if (e.dtype == QKV_CTE_DTYPE_FP32) {
+    const float* p = static_cast<const float*>(e.residual) + row * e.ldr + col0;
+    ld_global_v8_b32(p, r);
+    ld_global_v8_b32(p + 8, r + 8);
+  } else {
+    ld_global_v8_b32(static_cast<const uint16_t*>(e.residual) + row * e.ldr + col0, r);
+  }
+}
+
+__device__ __forceinline__ float2 unpack2(uint32_t w, int dtype) {
+  if (dtype == QKV_CTE_DTYPE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int dtype) {
+  if (dtype == QKV_CTE_DTYPE_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 16 bf16 parameters of consecutive columns as fp32 (16-byte aligned, all in range).
+__device__ __forceinline__ void load_bf16x16(const uint16_t* p, float* out) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    out[2 * j] = __uint_as_float(w[j] << 16);
+    out[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+
+// The 16 columns at col0, whole and 32-byte aligned: v = acc * ascale (* col) + bias,
+// activation, gate, the residual's raw words r, one rounding, 32-byte stores.
+__device__ __forceinline__ void finish16(const LinearEpilogue& e, long long row, int col0, const uint32_t* acc,
+                                         float ascale, const float* col, const uint16_t* bias, const uint32_t* r,
+                                         uint64_t pol) {
+  float v[16], p[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(acc[j]) * ascale;
+  if (col != nullptr) {
+    ld_params<float, 16>(col + col0, p);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] *= p[j];
+  }
+  if (bias != nullptr) {
+    load_bf16x16(bias + col0, p);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] += p[j];
+  }
+  switch (e.act) {  // one uniform branch for the 16 columns
+    case QKV_CTE_ACT_GELU_TANH:
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = apply_act(v[j], QKV_CTE_ACT_GELU_TANH);
+      break;
+    case QKV_CTE_ACT_GELU_ERF:
+#pragma unroll 4
+      for (int j = 0; j < 16; ++j) v[j] = apply_act(v[j], QKV_CTE_ACT_GELU_ERF);
+      break;
+    case QKV_CTE_ACT_SILU:
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = apply_act(v[j], QKV_CTE_ACT_SILU);
+      break;
+    default: break;
+  }
+  if (e.gate != nullptr) {
+    load_bf16x16(e.gate + col0, p);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] *= p[j];
+  }
+  if (e.dtype == QKV_CTE_DTYPE_FP32) {
+    if (e.residual != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
+    }
+    float* dst = static_cast<float*>(e.out) + row * e.ldo + col0;
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(v[j]);
+    st_global_v8_b32_hint(dst, w, pol);
+    st_global_v8_b32_hint(dst + 8, w + 8, pol);
+    return;
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float lo = v[2 * j], hi = v[2 * j + 1];
+    if (e.residual != nullptr) {
+      const float2 q = unpack2(r[j], e.dtype);
+      lo += q.x;
+      hi += q.y;
+    }
+    w[j] = pack2(lo, hi, e.dtype);
+  }
+  st_global_v8_b32_hint(static_cast<uint16_t*>(e.out) + row * e.ldo + col0, w, pol);
+}
+
+// One element, any alignment: the few-token form and ragged chunks.
+__device__ __forceinline__ void finish_one(const LinearEpilogue& e, long long row, int c, float acc, float scale,
+                                           float bias, float gate) {
+  float v = apply_act(fmaf(acc, scale, bias), e.act);
+  if (e.gate != nullptr) v *= gate;
+  if (e.residual != nullptr) v += load_any(e.residual, row * e.ldr + c, e.dtype);
+  store_any(e.out, row * e.ldo + c, e.dtype, v);
+}
+
+}  // namespace qkvcte

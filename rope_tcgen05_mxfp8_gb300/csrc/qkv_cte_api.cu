@@ -140,24 +140,6 @@ int encode_scales(CUtensorMap* m, void* base, const GemmShape& g) {
   return QKV_CTE_OK;
 }
 
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
-
-int check_device(DeviceInfo* dev) {
-  int rc = device_info(dev);
-  if (rc != QKV_CTE_OK) return rc;
-  if (!(dev->major == 10 && dev->minor == 3))
-    return fail(QKV_CTE_ERR_ARCH, "device is sm_%d%d; this library is built for sm_103a", dev->major, dev->minor);
-  return QKV_CTE_OK;
-}
-
-}  // namespace qkvcte
-
-namespace {
-
 // N tiles per band: the band's W slab (tile_n * H bytes per N tile) is kept to about
 // 28 MB so that it stays resident in the 129 MB L2 beside the streaming traffic
 // (measured at the Wan 480p shape: 28 MB bands beat 56 MB, 110 MB and one band).
@@ -172,6 +154,35 @@ int band_tiles(const GemmShape& g) {
   int n = (int)(mb * 1048576.0 / per_tile);
   return n < 1 ? 1 : n;
 }
+
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+bool strided_rows_overlap(const void* a, int64_t a_stride, const void* b, int64_t b_stride, int64_t rows,
+                          int64_t a_row, int64_t b_row) {
+  if (b_row == 0) b_row = a_row;
+  if (rows <= 0) return false;
+  if (!overlaps(a, (size_t)((rows - 1) * a_stride + a_row), b, (size_t)((rows - 1) * b_stride + b_row))) return false;
+  if (a_stride != b_stride || a_stride <= 0) return true;
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  const int64_t m = ((d % a_stride) + a_stride) % a_stride;  // b's offset within a's row pitch
+  return m < a_row || a_stride - m < b_row;
+}
+
+int check_device(DeviceInfo* dev) {
+  int rc = device_info(dev);
+  if (rc != QKV_CTE_OK) return rc;
+  if (!(dev->major == 10 && dev->minor == 3))
+    return fail(QKV_CTE_ERR_ARCH, "device is sm_%d%d; this library is built for sm_103a", dev->major, dev->minor);
+  return QKV_CTE_OK;
+}
+
+}  // namespace qkvcte
+
+namespace {
 
 // Row-panel ranges the Q/K bands take turns over (1: each Q/K band over all panels).
 // QKV_CTE_M_CHUNKS overrides it (for tuning sweeps).

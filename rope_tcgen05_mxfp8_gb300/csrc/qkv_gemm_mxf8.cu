@@ -42,9 +42,20 @@ __global__ void __launch_bounds__(kPrepThreads) qkv_prep_kernel(
     const int i = threadIdx.x;  // tile_n <= 256 = kPrepThreads
     const int n = nt * tile_n + i;
     const bool live = i < tile_n && n < I;
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(w_sf + static_cast<size_t>(live ? n : 0) * k_blocks) + kst0;
+    const uint8_t* src = w_sf + static_cast<size_t>(live ? n : 0) * k_blocks + 4 * kst0;
+    if ((k_blocks & 3) == 0) {
 #pragma unroll
-    for (int k = 0; k < kPrepStages; ++k) rows[i][k] = (live && k < n_st) ? __ldg(src + k) : 0x7F7F7F7Fu;
+      for (int k = 0; k < kPrepStages; ++k)
+        rows[i][k] = (live && k < n_st) ? __ldg(reinterpret_cast<const uint32_t*>(src) + k) : 0x7F7F7F7Fu;
+    } else {  // the last K stage is short (products only): rows off word boundaries, 127 past the end
+      for (int k = 0; k < kPrepStages; ++k) {
+        uint32_t w = 0x7F7F7F7Fu;
+        for (int j = 0; live && k < n_st && j < 4; ++j)
+          if (4 * (kst0 + k) + j < k_blocks)
+            w = (w & ~(0xFFu << (8 * j))) | static_cast<uint32_t>(__ldg(src + 4 * k + j)) << (8 * j);
+        rows[i][k] = w;
+      }
+    }
     __syncthreads();
     // The image's four lane quarters are the same 32-row block (sf_chunks * 512 bytes):
     // each thread builds one 16-byte row of a core matrix of that block and stores it

@@ -46,6 +46,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "fp32x2.cuh"
+#include "linear_epilogue.cuh"
 #include "qk_norm_rope.cuh"
 
 namespace qkvcte {
@@ -466,6 +467,58 @@ __device__ __forceinline__ void epilogue_drain_plain(const GemmShape& g, const G
   }
 }
 
+// Epilogue of the product (kEpiLinear): 32 columns per TMEM load; the residual's words of
+// the next 32 columns are requested before this chunk is finished, so that the epilogue
+// does not wait out the memory latency chunk by chunk. Rows off 32-byte boundaries and
+// the ragged last 16 columns go element by element.
+template <int BN>
+__device__ __forceinline__ void epilogue_drain_linear(const GemmShape& g, const GemmArgs& a, uint32_t t_acc,
+                                                      int block128, int row_in_block, int col_base, uint64_t pol_out) {
+  const LinearEpilogue& e = a.lin;
+  const long long row = static_cast<long long>(block128) * 128 + row_in_block;
+  const bool row_ok = row < g.T;
+  const float ascale = row_ok ? a.a_scale[row] : 0.0f;
+  const bool fetch = e.residual != nullptr && e.wide && row_ok;
+  uint32_t res[2][16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (fetch && col_base + 16 * (h + 1) <= g.I) load_residual16(e, row, col_base + 16 * h, res[h]);
+#pragma unroll 1
+  for (int c0 = 0; c0 < BN; c0 += 32) {
+    if (col_base + c0 >= g.I) break;  // uniform across the warp
+    uint32_t r[32];
+    if (c0 + 32 <= BN)
+      tmem_ld_32x32b_x32(t_acc + static_cast<uint32_t>(c0), r);
+    else
+      tmem_ld_32x32b_x16(t_acc + static_cast<uint32_t>(c0), r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int cc = c0 + 16 * h;
+      const int col0 = col_base + cc;
+      if (cc >= BN || col0 >= g.I) break;  // uniform across the warp
+      uint32_t now[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) now[j] = res[h][j];
+      if (fetch && cc + 32 < BN && col0 + 48 <= g.I) load_residual16(e, row, col0 + 32, res[h]);
+      if (!row_ok) continue;
+      if (e.wide && col0 + 16 <= g.I) {
+        finish16(e, row, col0, r + 16 * h, ascale, a.w_col_scale, a.bias, now, pol_out);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int c = col0 + j;
+          if (c < g.I)
+            finish_one(e, row, c, __uint_as_float(r[16 * h + j]),
+                       a.w_col_scale != nullptr ? ascale * a.w_col_scale[c] : ascale,
+                       a.bias != nullptr ? bf16_bits_to_float(a.bias[c]) : 0.0f,
+                       e.gate != nullptr ? bf16_bits_to_float(e.gate[c]) : 1.0f);
+        }
+      }
+    }
+  }
+}
+
 // Epilogue kinds, each a separate instantiation of the kernels (the per-head ones need
 // more registers per thread, which would otherwise leave no room on an SM
 // sub-partition for a norm/RoPE warp beside the GEMM's two warps there):
@@ -474,7 +527,8 @@ __device__ __forceinline__ void epilogue_drain_plain(const GemmShape& g, const G
 //   kEpiStatsRms / kEpiStatsLayer : as plain, plus the per-head statistics (RMS: sums of
 //               squares; LayerNorm: each part's mean and centred M2, values handed over
 //               centred) the norm/RoPE pass finishes from
-constexpr int kEpiPlain = 0, kEpiHead = 1, kEpiStatsRms = 2, kEpiStatsLayer = 3;
+//   kEpiLinear: bias, activation, gate and residual to a strided output (qkv_cte_linear_run)
+constexpr int kEpiPlain = 0, kEpiHead = 1, kEpiStatsRms = 2, kEpiStatsLayer = 3, kEpiLinear = 4;
 
 template <int BN, int kEpi>
 __device__ __forceinline__ void epilogue_drain(const GemmShape& g, const GemmArgs& a, uint32_t t_acc, int block128,
@@ -482,6 +536,8 @@ __device__ __forceinline__ void epilogue_drain(const GemmShape& g, const GemmArg
                                                float& ss_k) {
   if constexpr (kEpi == kEpiHead)
     epilogue_drain_head<BN>(g, a, t_acc, block128, row_in_block, col_base, pol_out, ss_q, ss_k);
+  else if constexpr (kEpi == kEpiLinear)
+    epilogue_drain_linear<BN>(g, a, t_acc, block128, row_in_block, col_base, pol_out);
   else
     epilogue_drain_plain<BN, kEpi == kEpiStatsRms ? 2 : (kEpi == kEpiStatsLayer ? 3 : 0)>(
         g, a, t_acc, block128, row_in_block, col_base, pol_out, ss_q, ss_k);

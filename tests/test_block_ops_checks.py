@@ -175,3 +175,67 @@ def test_new_entry_points_are_exported():
     for name in ("qkv_cte_layer_norm", "qkv_cte_layer_norm_backward", "qkv_cte_layer_norm_backward_workspace",
                  "qkv_cte_rope_plan", "qkv_cte_rope_destroy", "qkv_cte_rope_tables", "qkv_cte_rope_apply"):
         assert hasattr(lib, name)
+
+
+# --- the product ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(), 0), (dict(tokens=0), 0), (dict(tokens=1), 0), (dict(tokens=-1), -1), (dict(tokens=2 ** 31), -2),
+    (dict(in_features=0), -1), (dict(in_features=48), -2), (dict(in_features=32), 0), (dict(in_features=-32), -1),
+    (dict(out_features=0), -1), (dict(out_features=1), 0), (dict(out_features=2 ** 31 - 1), -2),
+    (dict(act=4), -1), (dict(act=-1), -1), (dict(act=3), 0), (dict(out_dtype=3), -1), (dict(out_dtype=2), 0),
+    (dict(input_layout=3), -1), (dict(flags=2), -1), (dict(flags=1), 0),
+])
+def test_linear_plan_validation(kw, code):
+    a = dict(tokens=300, in_features=256, out_features=500, act=0, out_dtype=0, input_layout=0, flags=0)
+    a.update(kw)
+    plan, n = ctypes.c_void_p(), ctypes.c_size_t()
+    lib = bo._lib()
+    desc = bo.qkv_cte_linear_desc(*[a[k] for k, _ in bo.qkv_cte_linear_desc._fields_])
+    assert lib.qkv_cte_linear_plan(ctypes.byref(plan), ctypes.byref(desc), ctypes.byref(n)) == code
+    assert (plan.value is not None) == (code == 0)
+    lib.qkv_cte_linear_destroy(plan)
+    assert lib.qkv_cte_linear_plan(None, ctypes.byref(desc), ctypes.byref(n)) == -1
+
+
+LIN = dict(A=16 * MB, a_scale=1 * MB, W=32 * MB, w_sf=48 * MB, col=2 * MB, bias=3 * MB, gate=4 * MB, res=64 * MB,
+           ldr=512, O=80 * MB, ldo=512, ws=128 * MB, wsn=None)
+
+
+@pytest.mark.parametrize("tokens", [3, 300])
+@pytest.mark.parametrize("kw,code", [
+    (dict(A=None), -1), (dict(W=None), -1), (dict(w_sf=None), -1), (dict(O=None), -1), (dict(ws=None), -1),
+    (dict(a_scale=None), -1), (dict(wsn=255), -1),
+    (dict(ldo=511), -1), (dict(ldr=511), -1), (dict(ldr=-1), -1), (dict(ldo=2 ** 61), -2),
+    (dict(A=16 * MB + 8), -2), (dict(W=32 * MB + 8), -2), (dict(w_sf=48 * MB + 2), -2), (dict(O=80 * MB + 1), -2),
+    (dict(res=64 * MB + 1), -2), (dict(bias=3 * MB + 8), -2), (dict(gate=4 * MB + 2), -2), (dict(col=2 * MB + 4), -2),
+    (dict(a_scale=MB + 2), -2), (dict(ws=128 * MB + 128), -2),
+    (dict(O=16 * MB), -1), (dict(O=32 * MB), -1), (dict(O=3 * MB), -1), (dict(O=128 * MB), -1), (dict(ws=16 * MB), -1),
+    (dict(ws=64 * MB), -1), (dict(O=64 * MB + 2), -1), (dict(O=64 * MB, ldo=1024), -1),
+    (dict(O=64 * MB + 1000, ldo=1024, ldr=1024), -1),
+])
+def test_linear_run_refusals(tokens, kw, code):
+    plan, n = ctypes.c_void_p(), ctypes.c_size_t()
+    lib = bo._lib()
+    desc = bo.qkv_cte_linear_desc(tokens, 256, 512, 0, 0, 0, 0)
+    assert lib.qkv_cte_linear_plan(ctypes.byref(plan), ctypes.byref(desc), ctypes.byref(n)) == 0
+    a = dict(LIN, wsn=n.value)
+    a.update(kw)
+    got = lib.qkv_cte_linear_run(plan, a["A"], a["a_scale"], a["W"], a["w_sf"], a["col"], a["bias"], a["gate"], a["res"],
+                                 a["ldr"], a["O"], a["ldo"], a["ws"], a["wsn"], None)
+    lib.qkv_cte_linear_destroy(plan)
+    assert got == code
+    assert lib.qkv_cte_linear_run(None, *[None] * 8, 0, None, 0, None, 0, None) == -1
+
+
+def test_linear_produced_inputs_take_no_scale():
+    lib = bo._lib()
+    for layout in (1, 2):
+        plan, n = ctypes.c_void_p(), ctypes.c_size_t()
+        desc = bo.qkv_cte_linear_desc(3, 256, 512, 0, 0, layout, 0)
+        assert lib.qkv_cte_linear_plan(ctypes.byref(plan), ctypes.byref(desc), ctypes.byref(n)) == 0
+        a = dict(LIN, wsn=n.value)
+        got = lib.qkv_cte_linear_run(plan, a["A"], a["a_scale"], a["W"], a["w_sf"], None, None, None, None, 0, a["O"],
+                                     512, a["ws"], a["wsn"], None)
+        lib.qkv_cte_linear_destroy(plan)
+        assert got == -1
