@@ -84,24 +84,30 @@ def _lib() -> ctypes.CDLL:
     return lib
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
+_current_device = torch._C._cuda_getDevice
+
+
 def _launch(fn, device, stream, *args):
     """fn(*args, stream) with `device` current."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if device.index == torch.cuda.current_device():
-        return _check(fn(*args, handle))
-    with torch.cuda.device(device):
-        return _check(fn(*args, handle))
+        handle = _raw_stream(device.index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if device.index == _current_device():
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, handle)
+    if rc:
+        _check(rc)
 
 
 def _kept(stream, device, *tensors):
     """Tensors allocated here for work on another stream than the one the allocator knows
     of: their memory is not handed out again before that work is done."""
-    if stream is None:
-        return
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if handle == torch.cuda.current_stream(device).cuda_stream:
+    if handle == _raw_stream(device.index):
         return
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=device)
     for t in tensors:
@@ -127,7 +133,7 @@ def _vector(name: str, t, dtypes, device, n: int) -> Optional[int]:
     if t is None:
         return None
     _tensor(name, t, dtypes, device)
-    if not t.is_contiguous() or t.numel() != n:
+    if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous with {n} elements, got shape {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -135,15 +141,18 @@ def _vector(name: str, t, dtypes, device, n: int) -> Optional[int]:
 def _rows(name: str, t, dtypes, device=None, shape=None):
     """(address, row stride) of [..., cols] as rows; the elements of a row are contiguous."""
     _tensor(name, t, dtypes, device)
-    if t.dim() < 1:
-        raise ValueError(f"{name}: needs at least one dimension")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} is not {tuple(shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    strides = t.stride()
+    if len(strides) == 2 and strides[1] == 1:
+        return t.data_ptr(), strides[0]
+    if not strides:
+        raise ValueError(f"{name}: needs at least one dimension")
+    if t.shape[-1] > 1 and strides[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    if t.dim() == 1:
+    if len(strides) == 1:
         return t.data_ptr(), t.shape[0]
-    if t.dim() != 2:
+    if len(strides) > 2:
         try:
             t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(-1, max(t.shape[-1], 1))
         except RuntimeError:
@@ -167,7 +176,7 @@ def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None,
     pb = _vector("bias", bias, (pdt,), dev, cols)
     made = []
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = x.new_empty(x.shape)
         made.append(out)
     if stats:
         if mean is None:
@@ -179,7 +188,8 @@ def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None,
     py, ldy = _rows("out", out, (x.dtype,), dev, x.shape)
     pm = _vector("mean", mean, (torch.float32,), dev, rows)
     pr = _vector("rstd", rstd, (torch.float32,), dev, rows)
-    _kept(stream, dev, *made)
+    if stream is not None:
+        _kept(stream, dev, *made)
     _launch(_lib().qkv_cte_layer_norm, dev, stream, px, ldx, pw, pb, py, ldy, pm, pr, rows, cols, eps, _DTYPE[x.dtype],
             _DTYPE[pdt])
     return out, mean, rstd
@@ -206,7 +216,7 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
         raise TypeError(f"weight, dweight and dbias: dtype {pdt} is neither {x.dtype} nor torch.float32")
     made = []
     if dx is None and dweight is None and dbias is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dx = x.new_empty(x.shape)
         dweight = torch.empty(cols, dtype=pdt, device=dev)
         dbias = torch.empty(cols, dtype=pdt, device=dev)
         made += [dx, dweight, dbias]
@@ -223,7 +233,8 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
             made.append(workspace)
         ws_bytes = workspace.numel()
         pws = _vector("workspace", workspace, (torch.uint8,), dev, ws_bytes)
-    _kept(stream, dev, *made)
+    if stream is not None:
+        _kept(stream, dev, *made)
     _launch(_lib().qkv_cte_layer_norm_backward, dev, stream, pg, ldg, px, ldx, pw, pm, pr, pd, ldd, pdw, pdb, rows,
             cols, _DTYPE[x.dtype], _DTYPE[pdt], pws, ws_bytes)
     return dx, dweight, dbias
@@ -278,7 +289,8 @@ class QkvCteRopeAxes:
             made.append(sin)
         n = batch * seq * self.d_head
         pc, ps = _vector("cos", cos, (torch.float32,), dev, n), _vector("sin", sin, (torch.float32,), dev, n)
-        _kept(stream, dev, *made)
+        if stream is not None:
+            _kept(stream, dev, *made)
         _launch(_lib().qkv_cte_rope_tables, dev, stream, self.plan, batch, seq, p, stride, g, pc, ps)
         return cos, sin
 
@@ -292,7 +304,7 @@ class QkvCteRopeAxes:
         dev = x.device
         made = out is None
         if made:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            out = x.new_empty(x.shape)
         _tensor("out", out, (x.dtype,), dev)
         if out.shape != x.shape:
             raise ValueError(f"out: shape {tuple(out.shape)} is not {tuple(x.shape)}")
@@ -304,7 +316,7 @@ class QkvCteRopeAxes:
         p, stride, g = self._where(batch, seq, positions, grids, dev)
         sx, sy = x.stride(), out.stride()
         bx, by = (sx[0], sy[0]) if x.dim() == 4 else (0, 0)
-        if made:
+        if made and stream is not None:
             _kept(stream, dev, out)
         _launch(_lib().qkv_cte_rope_apply, dev, stream, self.plan, x.data_ptr(), bx, sx[-3], sx[-2], out.data_ptr(),
                 by, sy[-3], sy[-2], batch, seq, heads, p, stride, g, _DTYPE[x.dtype], 1 if inverse else 0)
@@ -369,8 +381,9 @@ class QkvCteLinear:
         pg = _vector("gate", gate, _BF16_BITS, dev, N)
         pr, ldr = _rows("residual", residual, (self.out_dtype,), dev, (T, N)) if residual is not None else (None, 0)
         if out is None:
-            out = torch.empty(T, N, dtype=self.out_dtype, device=dev)
-            _kept(stream, dev, out)
+            out = torch.empty(self.shape, dtype=self.out_dtype, device=dev)
+            if stream is not None:
+                _kept(stream, dev, out)
         po, ldo = _rows("out", out, (self.out_dtype,), dev, (T, N))
         _launch(_lib().qkv_cte_linear_run, dev, stream, self.plan, pa, ps, pw, pf, pc, pb, pg, pr, ldr, po, ldo,
                 self.workspace.data_ptr(), self.workspace.numel())

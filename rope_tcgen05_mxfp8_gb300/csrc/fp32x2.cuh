@@ -1,6 +1,6 @@
-// Two fp32 fma / mul in one instruction (fma.rn.f32x2 / mul.rn.f32x2, sm_100 family).
+// Two fp32 fma / mul / add in one instruction (fma.rn.f32x2 and so on, sm_100 family).
 // Each lane rounds exactly as the scalar instruction does, so results are
-// bit-identical to two fmaf / __fmul_rn.
+// bit-identical to two fmaf / __fmul_rn / __fadd_rn.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -22,6 +22,16 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
       "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
       "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;

@@ -4,17 +4,25 @@
 //   y  = xh * w + b
 //   g  = dy * w,  dx = r (g - mean(g) - xh mean(g xh)),  dw = sum_rows dy xh,  db = sum_rows dy
 //
-// Both passes are bound by memory (2 and 3 times the tensor). A row is held in the
-// registers of one group of threads (a warp for short rows, a block for long ones), so
-// it is read once; the variance is taken about the mean in a second sweep over the
-// registers, never as a difference of large sums. The backward pass keeps its column
-// sums dw and db in the registers of the same threads over all rows of the block, one
-// partial row per block goes to the workspace, and a second kernel adds those in a
-// fixed order (no atomics: the result does not depend on the schedule). Sums,
-// statistics and gradients are fp32; x and the outputs are rounded once.
+// Both passes are bound by memory (2 and 3 times the tensor). A row belongs to one group
+// of threads (a warp for short rows, a block for long ones) and is read once; the
+// variance is taken about the mean in a second sweep over the registers, never as a
+// difference of large sums. Rows come through a ring in shared memory that each thread
+// fills for itself with 16-byte asynchronous copies, kRing rows ahead, so that loads
+// stay in flight across the reductions; parameters stay in registers over all the rows
+// of a block. The backward pass keeps its column sums dw and db in the registers of the
+// same threads; one partial row per block goes to the workspace, and a second kernel
+// adds those in a fixed order (no atomics: the result does not depend on the schedule).
+// Sums, statistics and gradients are fp32; outputs are rounded once.
+//
+// Arithmetic counts: a first form that converted each element in each sweep, read the
+// parameters from L1 and prefetched one row into registers ran 24 instructions per
+// element and took 204 us for 32760 x 5120 in bf16, twice the floor. Elements are
+// converted once, worked on in pairs (fma.rn.f32x2 and so on) and kept as x - mu.
 #include <algorithm>
 
 #include "block_ops.h"
+#include "fp32x2.cuh"
 #include "qkv_cte.h"
 #include "vec_io.cuh"
 
@@ -24,89 +32,280 @@ namespace {
 
 constexpr int kWarpRows = 4;  // rows (warps) per block of the warp-per-row form
 
-// Sum over the group of threads that holds a row: a warp (blockDim.x == 32, no
-// barrier) or the whole block. `slot` alternates between consecutive calls: a thread
-// writes a slot again only after the barrier of the call in between, which every
-// reader of the slot has reached.
-__device__ __forceinline__ float group_sum(float v, float (*red)[32], int slot) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (blockDim.x == 32) return v;
-  const int warps = blockDim.x >> 5;
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) red[slot][threadIdx.x >> 5] = v;
+constexpr int kRing = 3;      // rows in flight per group of threads
+
+// Sums of N values over the group of threads that holds a row: a warp (blockDim.x ==
+// 32, no barrier) or the whole block of at most 4 * kQuads warps. `slot` alternates
+// between consecutive calls: a thread writes a slot again only after the barrier of the
+// call in between, which every reader of the slot has reached. The entries of absent
+// warps must hold zeros (clear_sums). Per thread: its terms, five levels in the warp,
+// then kQuads additions in four lanes and two more.
+template <int N, int kQuads>
+struct GroupSums {
+  float4 v[2][N][kQuads];
+};
+
+template <int N, int kQuads>
+__device__ __forceinline__ void clear_sums(GroupSums<N, kQuads>& red) {
+  if (blockDim.x == 32) return;
+  float* p = reinterpret_cast<float*>(&red);
+  for (int i = threadIdx.x; i < 2 * N * 4 * kQuads; i += blockDim.x) p[i] = 0.0f;
   __syncthreads();
-  v = lane < warps ? red[slot][lane] : 0.0f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
 }
 
-// VEC elements per access, CH accesses per thread: rows of up to CH * VEC * blockDim.x.
-template <typename T, typename P, int VEC, int CH>
-__global__ void __launch_bounds__(1024) layer_norm_kernel(LayerNormArgs a) {
-  __shared__ float red[2][32];
-  const float inv = 1.0f / static_cast<float>(a.cols);
-  const P* w = static_cast<const P*>(a.weight);
-  const P* b = static_cast<const P*>(a.bias);
-  for (long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y; row < a.rows;
-       row += static_cast<long long>(gridDim.x) * blockDim.y) {
-    const T* xr = static_cast<const T*>(a.x) + row * a.ldx;
-    T* yr = static_cast<T*>(a.y) + row * a.ldy;
-    Vec<T, VEC> v[CH];
-    float s = 0.0f;
+template <int N, int kQuads>
+__device__ __forceinline__ void group_sum(float* v, GroupSums<N, kQuads>& red, int slot) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if (blockDim.x == 32) return;
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) reinterpret_cast<float*>(red.v[slot][k])[threadIdx.x >> 5] = v[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    float4 t = red.v[slot][k][0];
+#pragma unroll
+    for (int q = 1; q < kQuads; ++q) {
+      const float4 r = red.v[slot][k][q];
+      t = make_float4(t.x + r.x, t.y + r.y, t.z + r.z, t.w + r.w);
+    }
+    v[k] = (t.x + t.y) + (t.z + t.w);
+  }
+}
+
+// What a thread computes on: pairs where an access holds several elements, else single
+// elements.
+__device__ __forceinline__ float2 vfma(float2 a, float2 b, float2 c) { return ffma2(a, b, c); }
+__device__ __forceinline__ float2 vmul(float2 a, float2 b) { return fmul2(a, b); }
+__device__ __forceinline__ float2 vadd(float2 a, float2 b) { return fadd2(a, b); }
+__device__ __forceinline__ float vfma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float vmul(float a, float b) { return a * b; }
+__device__ __forceinline__ float vadd(float a, float b) { return a + b; }
+__device__ __forceinline__ float hsum(float2 a) { return a.x + a.y; }
+__device__ __forceinline__ float hsum(float a) { return a; }
+
+template <int VEC>
+struct Lanes {
+  static_assert(VEC % 2 == 0, "pairs");
+  using F = float2;
+  static constexpr int N = VEC / 2;
+  static __device__ __forceinline__ F all(float x) { return make_float2(x, x); }
+  template <typename V>
+  static __device__ __forceinline__ F get(const V& v, int j) {
+    return v.pair(j);
+  }
+  template <typename V>
+  static __device__ __forceinline__ void put(V& v, int j, F x) {
+    v.set_pair(j, x);
+  }
+};
+template <>
+struct Lanes<1> {
+  using F = float;
+  static constexpr int N = 1;
+  static __device__ __forceinline__ F all(float x) { return x; }
+  template <typename V>
+  static __device__ __forceinline__ F get(const V& v, int) {
+    return v.one();
+  }
+  template <typename V>
+  static __device__ __forceinline__ void put(V& v, int, F x) {
+    v.set_one(x);
+  }
+};
+
+// A thread's part of a row: CH accesses of VEC elements, blockDim.x accesses apart (kFull:
+// the row fills them all). The next rows are on their way: whole 16-byte accesses go
+// through the ring, single elements wait in registers, one row ahead.
+template <typename T, int VEC, int CH, bool kFull>
+struct RowStream {
+  static constexpr bool kAsync = VEC > 1;
+  // rows kept requested: as many as shared memory takes for long rows
+  static constexpr int kAhead = !kAsync ? 1 : (CH > 2 ? 2 : kRing);
+  static constexpr int kBytes = kAsync ? kAhead * CH * 16 : 0;  // of the ring, per thread
+
+  const T* next;   // this thread's first element of the next row to request
+  long long pitch; // elements to the one after
+  int left;        // rows still to request
+  uint32_t ring;   // shared address of this thread's first access; a row's are `stride` apart
+  uint32_t stride;
+  Vec<T, VEC> ahead[kAsync ? 1 : CH];
+
+  static __device__ __forceinline__ bool inside(int i, int cols) {
+    return kFull || static_cast<int>(i * blockDim.x + threadIdx.x) * VEC < cols;
+  }
+  // `base`: this tensor's part of shared memory, kBytes per thread; the group takes rows
+  // first, first + step, ... below rows.
+  __device__ __forceinline__ void init(uint8_t* base, const void* p, long long ld, int first, int step, int rows) {
+    next = static_cast<const T*>(p) + first * ld + threadIdx.x * VEC;
+    pitch = step * ld;
+    left = first < rows ? (rows - 1 - first) / step + 1 : 0;
+    stride = 16 * blockDim.x * blockDim.y;
+    ring = static_cast<uint32_t>(__cvta_generic_to_shared(base)) + 16 * (threadIdx.y * blockDim.x + threadIdx.x);
+  }
+  // Request the next row, if there is one, into ring slot `slot`.
+  __device__ __forceinline__ void request(int cols, int slot) {
+    if (left > 0) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        if (inside(i, cols)) {
+          if constexpr (kAsync)
+            cp_async16(ring + (slot * CH + i) * stride, next + i * blockDim.x * VEC);
+          else
+            ahead[i] = ld_once<T, VEC>(next + i * blockDim.x * VEC);
+        }
+      }
+      next += pitch;
+      --left;
+    }
+  }
+  __device__ __forceinline__ Vec<T, VEC> take(int i, int slot) const {
+    if constexpr (kAsync) {
+      Vec<T, VEC> r;
+      ld_shared16(ring + (slot * CH + i) * stride, r.w);
+      return r;
+    } else {
+      return ahead[i];
+    }
+  }
+};
+
+// A thread's part of the parameters, packed (`absent` without a tensor).
+template <typename P, int VEC, int CH>
+struct ParamPart {
+  using L = Lanes<VEC>;
+  static constexpr int N = 16 / sizeof(P) < VEC ? 16 / sizeof(P) : VEC;  // per access
+  static constexpr int kPer = VEC == 1 ? 1 : N / 2;                       // lanes per access
+  Vec<P, N> v[CH][VEC / N];
+
+  __device__ __forceinline__ void load(const void* p, int cols, float absent) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * VEC;
-      if (c < a.cols) v[i] = ld_once<T, VEC>(xr + c);
-    }
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      if ((i * blockDim.x + threadIdx.x) * VEC < a.cols) {
+      for (int k = 0; k < VEC / N; ++k) {
+        if (p != nullptr && c < cols) {
+          v[i][k] = *reinterpret_cast<const Vec<P, N>*>(static_cast<const P*>(p) + c + k * N);
+        } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) s += to_f32(v[i].v[j]);
-      }
-    }
-    const float mean = group_sum(s, red, 0) * inv;
-    float ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      if ((i * blockDim.x + threadIdx.x) * VEC < a.cols) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float d = to_f32(v[i].v[j]) - mean;
-          ss = fmaf(d, d, ss);
+          for (int j = 0; j < kPer; ++j) L::put(v[i][k], j, L::all(absent));
         }
       }
     }
-    const float rstd = 1.0f / sqrtf(group_sum(ss, red, 1) * inv + a.eps);
+  }
+  __device__ __forceinline__ typename L::F get(int i, int j) const { return L::get(v[i][j / kPer], j % kPer); }
+};
+
+// Forms of the kernels: kKeep holds the parameters in registers over all rows (blocks of
+// 256 threads at most), else they are read for every row (512 threads); kFull rows fill
+// every access of every thread.
+template <typename T_, typename P_, int VEC_, int CH_, bool kKeep_, bool kFull_>
+struct Form {
+  using T = T_;
+  using P = P_;
+  static constexpr int VEC = VEC_, CH = CH_;
+  static constexpr bool kKeep = kKeep_, kFull = kFull_;
+  static constexpr int kQuads = kKeep ? 2 : 4;
+  using L = Lanes<VEC>;
+  using Stream = RowStream<T, VEC, CH, kFull>;
+};
+
+template <typename Fm>
+__global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_kernel(LayerNormArgs a) {
+  using T = typename Fm::T;
+  using L = typename Fm::L;
+  using F = typename L::F;
+  using Stream = typename Fm::Stream;
+  constexpr int VEC = Fm::VEC, CH = Fm::CH, kAhead = Stream::kAhead;
+  extern __shared__ __align__(16) uint8_t ring_mem[];
+  __shared__ GroupSums<1, Fm::kQuads> red;
+  const float inv = 1.0f / static_cast<float>(a.cols);
+  const int step = gridDim.x * blockDim.y;
+  const int first = blockIdx.x * blockDim.y + threadIdx.y;
+  Stream in;
+  in.init(ring_mem, a.x, a.ldx, first, step, static_cast<int>(a.rows));
+  const int n = in.left;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    in.request(a.cols, k);
+    cp_async_commit();
+  }
+  ParamPart<typename Fm::P, VEC, CH> wp, bp;
+  if (Fm::kKeep) {
+    wp.load(a.weight, a.cols, 1.0f);
+    bp.load(a.bias, a.cols, 0.0f);
+  }
+  clear_sums(red);
+  T* out = static_cast<T*>(a.y) + first * a.ldy + threadIdx.x * VEC;
+  int slot = 0;
+  for (int k = 0; k < n; ++k) {
+    cp_async_wait<kAhead - 1>();
+    F d[CH][L::N];
+    F s = L::all(0.0f);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (Stream::inside(i, a.cols)) {
+        const Vec<T, VEC> v = in.take(i, slot);
+#pragma unroll
+        for (int j = 0; j < L::N; ++j) {
+          d[i][j] = L::get(v, j);
+          s = vadd(s, d[i][j]);
+        }
+      }
+    }
+    // the slot is free: this thread alone filled and read it
+    in.request(a.cols, slot);
+    cp_async_commit();
+    slot = slot + 1 == kAhead ? 0 : slot + 1;
+    float sum = hsum(s);
+    group_sum(&sum, red, 0);
+    const float mean = sum * inv;
+    F ss = L::all(0.0f);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (Stream::inside(i, a.cols)) {
+#pragma unroll
+        for (int j = 0; j < L::N; ++j) {
+          d[i][j] = vadd(d[i][j], L::all(-mean));
+          ss = vfma(d[i][j], d[i][j], ss);
+        }
+      }
+    }
+    sum = hsum(ss);
+    group_sum(&sum, red, 1);
+    const float rstd = rsqrtf(fmaf(sum, inv, a.eps));
     if (threadIdx.x == 0) {
+      const long long row = first + static_cast<long long>(k) * step;
       if (a.mean != nullptr) a.mean[row] = mean;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
+    if (!Fm::kKeep) {
+      wp.load(a.weight, a.cols, 1.0f);
+      bp.load(a.bias, a.cols, 0.0f);
+    }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * VEC;
-      if (c < a.cols) {
-        float wv[VEC], bv[VEC];
-        if (w != nullptr) ld_params<P, VEC>(w + c, wv);
-        if (b != nullptr) ld_params<P, VEC>(b + c, bv);
+      if (Stream::inside(i, a.cols)) {
         Vec<T, VEC> o;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float xh = (to_f32(v[i].v[j]) - mean) * rstd;
-          o.v[j] = from_f32<T>(fmaf(xh, w != nullptr ? wv[j] : 1.0f, b != nullptr ? bv[j] : 0.0f));
-        }
-        st_vec(yr + c, o);
+        for (int j = 0; j < L::N; ++j)
+          L::put(o, j, vfma(vmul(d[i][j], L::all(rstd)), wp.get(i, j), bp.get(i, j)));
+        st_vec(out + i * blockDim.x * VEC, o);
       }
     }
+    out += step * a.ldy;
   }
 }
 
 // Rows longer than the registers of a block: read three times (from L2 after the first).
 template <typename T, typename P>
 __global__ void __launch_bounds__(1024) layer_norm_long_kernel(LayerNormArgs a) {
-  __shared__ float red[2][32];
+  __shared__ GroupSums<1, 8> red;
+  clear_sums(red);
   const float inv = 1.0f / static_cast<float>(a.cols);
   const P* w = static_cast<const P*>(a.weight);
   const P* b = static_cast<const P*>(a.bias);
@@ -115,13 +314,15 @@ __global__ void __launch_bounds__(1024) layer_norm_long_kernel(LayerNormArgs a) 
     T* yr = static_cast<T*>(a.y) + row * a.ldy;
     float s = 0.0f;
     for (int c = threadIdx.x; c < a.cols; c += blockDim.x) s += to_f32(xr[c]);
-    const float mean = group_sum(s, red, 0) * inv;
+    group_sum(&s, red, 0);
+    const float mean = s * inv;
     float ss = 0.0f;
     for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
       const float d = to_f32(xr[c]) - mean;
       ss = fmaf(d, d, ss);
     }
-    const float rstd = 1.0f / sqrtf(group_sum(ss, red, 1) * inv + a.eps);
+    group_sum(&ss, red, 1);
+    const float rstd = rsqrtf(fmaf(ss, inv, a.eps));
     if (threadIdx.x == 0) {
       if (a.mean != nullptr) a.mean[row] = mean;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
@@ -133,96 +334,122 @@ __global__ void __launch_bounds__(1024) layer_norm_long_kernel(LayerNormArgs a) 
   }
 }
 
-// Rows held in registers, columns fixed to threads; the block's column sums leave as one
-// row of the workspace.
-template <typename T, typename P, int VEC, int CH>
-__global__ void __launch_bounds__(512) layer_norm_backward_kernel(LayerNormGradArgs a) {
-  __shared__ float red[2][2][32];
-  extern __shared__ float cols_sum[];  // [2][cols], only with several rows per block
+// Columns fixed to threads; the block's column sums leave as one row of the workspace.
+// The second sweep takes the row from the ring again: keeping xh and g instead cost 64
+// registers at four accesses per thread, and with them the second block on an SM.
+template <typename Fm>
+__global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_backward_kernel(LayerNormGradArgs a) {
+  using T = typename Fm::T;
+  using L = typename Fm::L;
+  using F = typename L::F;
+  using Stream = typename Fm::Stream;
+  constexpr int VEC = Fm::VEC, CH = Fm::CH, kAhead = Stream::kAhead;
+  // the ring; after the last row, with several rows per block, [2][cols] column sums
+  extern __shared__ __align__(16) uint8_t ring_mem[];
+  __shared__ GroupSums<2, Fm::kQuads> red;
   const float inv = 1.0f / static_cast<float>(a.cols);
-  const P* w = static_cast<const P*>(a.weight);
-  float dw[CH][VEC], db[CH][VEC];
+  const int step = gridDim.x * blockDim.y;
+  const int first = blockIdx.x * blockDim.y + threadIdx.y;
+  const int rows = static_cast<int>(a.rows);
+  Stream xin, gin;
+  xin.init(ring_mem, a.x, a.ldx, first, step, rows);
+  gin.init(ring_mem + Stream::kBytes * blockDim.x * blockDim.y, a.dy, a.lddy, first, step, rows);
+  const int n = xin.left;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    xin.request(a.cols, k);
+    gin.request(a.cols, k);
+    cp_async_commit();
+  }
+  const float* mean_p = a.mean + first;
+  const float* rstd_p = a.rstd + first;
+  float mean = n > 0 ? *mean_p : 0.0f, rstd = n > 0 ? *rstd_p : 0.0f;
+  ParamPart<typename Fm::P, VEC, CH> wp;
+  if (Fm::kKeep) wp.load(a.weight, a.cols, 1.0f);
+  clear_sums(red);
+  F dw[CH][L::N], db[CH][L::N];
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) dw[i][j] = db[i][j] = 0.0f;
-  int parity = 0;
-  for (long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y; row < a.rows;
-       row += static_cast<long long>(gridDim.x) * blockDim.y, parity ^= 1) {
-    const T* xr = static_cast<const T*>(a.x) + row * a.ldx;
-    const T* gr = static_cast<const T*>(a.dy) + row * a.lddy;
-    Vec<T, VEC> xv[CH], gv[CH];
+    for (int j = 0; j < L::N; ++j) dw[i][j] = db[i][j] = L::all(0.0f);
+  T* out_row = a.dx != nullptr ? static_cast<T*>(a.dx) + first * a.lddx + threadIdx.x * VEC : nullptr;
+  int slot = 0;
+  for (int k = 0; k < n; ++k) {
+    cp_async_wait<kAhead - 1>();
+    if (!Fm::kKeep) wp.load(a.weight, a.cols, 1.0f);
+    F s1 = L::all(0.0f), s2 = L::all(0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * VEC;
-      if (c < a.cols) {
-        xv[i] = ld_once<T, VEC>(xr + c);
-        gv[i] = ld_once<T, VEC>(gr + c);
-      }
-    }
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    float s1 = 0.0f, s2 = 0.0f;
+      if (Stream::inside(i, a.cols)) {
+        const Vec<T, VEC> xv = xin.take(i, slot), gv = gin.take(i, slot);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * VEC;
-      if (c < a.cols) {
-        float wv[VEC];
-        if (w != nullptr) ld_params<P, VEC>(w + c, wv);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float dy = to_f32(gv[i].v[j]);
-          const float xh = (to_f32(xv[i].v[j]) - mean) * rstd;
-          const float g = w != nullptr ? dy * wv[j] : dy;
-          s1 += g;
-          s2 = fmaf(g, xh, s2);
-          dw[i][j] = fmaf(dy, xh, dw[i][j]);
-          db[i][j] += dy;
+        for (int j = 0; j < L::N; ++j) {
+          const F d = L::get(gv, j);
+          const F xh = vmul(vadd(L::get(xv, j), L::all(-mean)), L::all(rstd));
+          const F g = vmul(d, wp.get(i, j));
+          s1 = vadd(s1, g);
+          s2 = vfma(g, xh, s2);
+          dw[i][j] = vfma(d, xh, dw[i][j]);
+          db[i][j] = vadd(db[i][j], d);
         }
       }
     }
-    if (a.dx == nullptr) continue;  // uniform over the grid
-    const float c1 = group_sum(s1, red[0], parity) * inv;
-    const float c2 = group_sum(s2, red[1], parity) * inv;
-    T* dr = static_cast<T*>(a.dx) + row * a.lddx;
+    if (a.dx != nullptr) {  // uniform over the grid
+      float c[2] = {hsum(s1), hsum(s2)};
+      group_sum(c, red, k & 1);
+      // dx = r (g - c1 - xh c2) with xh = (x - mean) r
+      const F c1 = L::all(-c[0] * inv), c2 = L::all(-c[1] * inv);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * VEC;
-      if (c < a.cols) {
-        float wv[VEC];
-        if (w != nullptr) ld_params<P, VEC>(w + c, wv);
-        Vec<T, VEC> o;
+      for (int i = 0; i < CH; ++i) {
+        if (Stream::inside(i, a.cols)) {
+          const Vec<T, VEC> xv = xin.take(i, slot), gv = gin.take(i, slot);
+          Vec<T, VEC> o;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float dy = to_f32(gv[i].v[j]);
-          const float xh = (to_f32(xv[i].v[j]) - mean) * rstd;
-          const float g = w != nullptr ? dy * wv[j] : dy;
-          o.v[j] = from_f32<T>(rstd * (g - c1 - xh * c2));
+          for (int j = 0; j < L::N; ++j) {
+            const F xh = vmul(vadd(L::get(xv, j), L::all(-mean)), L::all(rstd));
+            const F g = vmul(L::get(gv, j), wp.get(i, j));
+            L::put(o, j, vmul(vadd(vfma(xh, c2, g), c1), L::all(rstd)));
+          }
+          st_vec(out_row + i * blockDim.x * VEC, o);
         }
-        st_vec(dr + c, o);
       }
+      out_row += step * a.lddx;
+    }
+    // the slot is free: this thread alone filled and read it
+    xin.request(a.cols, slot);
+    gin.request(a.cols, slot);
+    cp_async_commit();
+    slot = slot + 1 == kAhead ? 0 : slot + 1;
+    if (k + 1 < n) {
+      mean = *(mean_p += step);
+      rstd = *(rstd_p += step);
     }
   }
   if (a.partial == nullptr) return;
   float* out = a.partial + static_cast<size_t>(blockIdx.x) * 2 * a.cols;
   if (blockDim.y > 1) {  // the block's rows (warps) one after the other, in order
+    float* sums = reinterpret_cast<float*>(ring_mem);
+    cp_async_wait<0>();
+    __syncthreads();  // no warp reads the ring any more
     for (int r = 0; r < static_cast<int>(blockDim.y); ++r) {
       if (static_cast<int>(threadIdx.y) == r) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
           const int c = (i * blockDim.x + threadIdx.x) * VEC;
-          if (c < a.cols) {
+          if (Stream::inside(i, a.cols)) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-              cols_sum[c + j] = r == 0 ? dw[i][j] : cols_sum[c + j] + dw[i][j];
-              cols_sum[a.cols + c + j] = r == 0 ? db[i][j] : cols_sum[a.cols + c + j] + db[i][j];
+            for (int j = 0; j < L::N; ++j) {
+              F* p = reinterpret_cast<F*>(sums + c) + j;  // [cols] then [cols]: cols is even where F is a pair
+              *p = r == 0 ? dw[i][j] : vadd(*p, dw[i][j]);
+              p = reinterpret_cast<F*>(sums + a.cols + c) + j;
+              *p = r == 0 ? db[i][j] : vadd(*p, db[i][j]);
             }
           }
         }
       }
       __syncthreads();
     }
-    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < 2 * a.cols; c += blockDim.x * blockDim.y)
-      out[c] = cols_sum[c];
+    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < 2 * a.cols; c += blockDim.x * blockDim.y) out[c] = sums[c];
     return;
   }
 #pragma unroll
@@ -230,9 +457,9 @@ __global__ void __launch_bounds__(512) layer_norm_backward_kernel(LayerNormGradA
     const int c = (i * blockDim.x + threadIdx.x) * VEC;
     if (c < a.cols) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        out[c + j] = dw[i][j];
-        out[a.cols + c + j] = db[i][j];
+      for (int j = 0; j < L::N; ++j) {
+        reinterpret_cast<F*>(out + c)[j] = dw[i][j];
+        reinterpret_cast<F*>(out + a.cols + c)[j] = db[i][j];
       }
     }
   }
@@ -241,7 +468,8 @@ __global__ void __launch_bounds__(512) layer_norm_backward_kernel(LayerNormGradA
 // Rows longer than the registers: dx with two sweeps over the row ...
 template <typename T, typename P>
 __global__ void __launch_bounds__(1024) layer_norm_backward_long_kernel(LayerNormGradArgs a) {
-  __shared__ float red[2][2][32];
+  __shared__ GroupSums<2, 8> red;
+  clear_sums(red);
   const float inv = 1.0f / static_cast<float>(a.cols);
   const P* w = static_cast<const P*>(a.weight);
   int parity = 0;
@@ -256,8 +484,9 @@ __global__ void __launch_bounds__(1024) layer_norm_backward_long_kernel(LayerNor
       s1 += g;
       s2 = fmaf(g, (to_f32(xr[c]) - mean) * rstd, s2);
     }
-    const float c1 = group_sum(s1, red[0], parity) * inv;
-    const float c2 = group_sum(s2, red[1], parity) * inv;
+    float sums[2] = {s1, s2};
+    group_sum(sums, red, parity);
+    const float c1 = sums[0] * inv, c2 = sums[1] * inv;
     for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
       const float g = to_f32(gr[c]) * (w != nullptr ? to_f32(w[c]) : 1.0f);
       dr[c] = from_f32<T>(rstd * (g - c1 - (to_f32(xr[c]) - mean) * rstd * c2));
@@ -308,29 +537,24 @@ __global__ void __launch_bounds__(32 * kJoinRows) layer_norm_join_kernel(const f
   if (out != nullptr) out[c < cols ? c : c - cols] = from_f32<P>(s);
 }
 
-// Threads and accesses per thread for a row of `chunks` accesses: a warp when a warp
-// holds it, else the fewest accesses per thread (a power of two from `ch0`) with which
-// `max_threads` threads hold it. 0: it does not fit.
-int pick_accesses(int chunks, int ch0, int ch_max, int max_threads, dim3* block) {
-  if (chunks <= 32 * ch0) {
-    int ch = 1;
-    while (32 * ch < chunks) ch *= 2;
-    *block = dim3(32, kWarpRows);
-    return ch;
-  }
-  for (int ch = ch0; ch <= ch_max; ch *= 2) {
-    const int threads = (chunks + ch * 32 - 1) / (ch * 32) * 32;
-    if (threads <= max_threads) {
-      *block = dim3(threads, 1);
-      return ch;
-    }
-  }
-  return 0;
+// The block for rows of `chunks` accesses with `ch` accesses per thread: false when more
+// than max_threads threads would be needed.
+bool pick_block(int chunks, int ch, int max_threads, dim3* block) {
+  const int threads = (chunks + ch * 32 - 1) / (ch * 32) * 32;
+  *block = threads == 32 ? dim3(32, kWarpRows) : dim3(threads, 1);
+  return threads <= max_threads;
 }
 
 bool vec_ok(const void* p, long long ld, int cols, size_t elem, long long rows) {
   const int n = static_cast<int>(16 / elem);
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && cols % n == 0 && (rows <= 1 || ld % n == 0);
+}
+
+// What exceeds the 48 KB that every kernel may use is asked for.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t smem) {
+  if (smem <= 40 * 1024) return cudaSuccess;  // with the static part, within the 48 KB
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
 }
 
 template <typename K>
@@ -343,25 +567,40 @@ int resident_grid(K kernel, dim3 block, size_t smem, int num_sms, long long work
   return static_cast<int>(std::min<long long>(static_cast<long long>(per_sm) * num_sms, work));
 }
 
-template <typename T, typename P, int VEC, int CH>
-cudaError_t forward_go(const LayerNormArgs& a, dim3 block, cudaStream_t s, int num_sms) {
-  auto k = layer_norm_kernel<T, P, VEC, CH>;
+template <typename Fm>
+cudaError_t forward_launch(const LayerNormArgs& a, dim3 block, cudaStream_t s, int num_sms) {
+  auto k = layer_norm_kernel<Fm>;
   const long long groups = (a.rows + block.y - 1) / block.y;
-  k<<<resident_grid(k, block, 0, num_sms, groups), block, 0, s>>>(a);
+  const size_t smem = static_cast<size_t>(Fm::Stream::kBytes) * block.x * block.y;
+  const cudaError_t e = allow_smem(k, smem);
+  if (e != cudaSuccess) return e;
+  k<<<resident_grid(k, block, smem, num_sms, groups), block, smem, s>>>(a);
   return cudaGetLastError();
 }
 
+template <typename T, typename P, int VEC, int CH, bool kKeep>
+cudaError_t forward_go(const LayerNormArgs& a, dim3 block, cudaStream_t s, int num_sms) {
+  if constexpr (VEC > 1) {
+    if (a.cols == static_cast<int>(block.x) * CH * VEC)
+      return forward_launch<Form<T, P, VEC, CH, kKeep, true>>(a, block, s, num_sms);
+  }
+  return forward_launch<Form<T, P, VEC, CH, kKeep, false>>(a, block, s, num_sms);
+}
+
+// Accesses per thread: one or two for rows of up to 64 (a warp) or 256 accesses, then
+// four. More accesses per thread mean fewer warps per row, each of which pays for the
+// reductions and addresses: 5120 bf16 columns on 160 threads take 105 us for 32760 rows,
+// on 320 threads 150 us.
 template <typename T, typename P, int VEC>
 cudaError_t forward_vec(const LayerNormArgs& a, cudaStream_t s, int num_sms) {
   dim3 block;
-  switch (pick_accesses(a.cols / VEC, 4, VEC == 1 ? 16 : 8, 1024, &block)) {
-    case 1: return forward_go<T, P, VEC, 1>(a, block, s, num_sms);
-    case 2: return forward_go<T, P, VEC, 2>(a, block, s, num_sms);
-    case 4: return forward_go<T, P, VEC, 4>(a, block, s, num_sms);
-    case 8: return forward_go<T, P, VEC, 8>(a, block, s, num_sms);
-    case 16:
-      if constexpr (VEC == 1) return forward_go<T, P, VEC, 16>(a, block, s, num_sms);
-    default: break;
+  const int chunks = a.cols / VEC;
+  if (chunks <= 32 && pick_block(chunks, 1, 32, &block)) return forward_go<T, P, VEC, 1, true>(a, block, s, num_sms);
+  if (chunks <= 256 && pick_block(chunks, 2, 256, &block)) return forward_go<T, P, VEC, 2, true>(a, block, s, num_sms);
+  if (pick_block(chunks, 4, 256, &block)) return forward_go<T, P, VEC, 4, true>(a, block, s, num_sms);
+  if (pick_block(chunks, 4, 512, &block)) return forward_go<T, P, VEC, 4, false>(a, block, s, num_sms);
+  if constexpr (VEC == 1) {
+    if (pick_block(chunks, 16, 512, &block)) return forward_go<T, P, VEC, 16, false>(a, block, s, num_sms);
   }
   auto k = layer_norm_long_kernel<T, P>;
   k<<<resident_grid(k, dim3(1024), 0, num_sms, a.rows), 1024, 0, s>>>(a);
@@ -392,32 +631,40 @@ cudaError_t join(const LayerNormGradArgs& a, int parts, cudaStream_t s) {
                             static_cast<P*>(a.dweight), static_cast<P*>(a.dbias));
 }
 
-template <typename T, typename P, int VEC, int CH>
-cudaError_t backward_go(const LayerNormGradArgs& a, dim3 block, cudaStream_t s, int num_sms) {
-  auto k = layer_norm_backward_kernel<T, P, VEC, CH>;
-  const size_t smem = block.y > 1 && a.partial != nullptr ? 2 * sizeof(float) * static_cast<size_t>(a.cols) : 0;
+template <typename Fm>
+cudaError_t backward_launch(const LayerNormGradArgs& a, dim3 block, cudaStream_t s, int num_sms) {
+  auto k = layer_norm_backward_kernel<Fm>;
+  size_t smem = 2 * static_cast<size_t>(Fm::Stream::kBytes) * block.x * block.y;
+  if (block.y > 1) smem = std::max(smem, 2 * sizeof(float) * static_cast<size_t>(a.cols));
+  cudaError_t e = allow_smem(k, smem);
+  if (e != cudaSuccess) return e;
   long long groups = (a.rows + block.y - 1) / block.y;
   if (a.partial != nullptr) groups = std::min<long long>(groups, a.max_parts);
   const int grid = resident_grid(k, block, smem, num_sms, groups);
   k<<<grid, block, smem, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess || a.partial == nullptr ? e : join<P>(a, grid, s);
+  e = cudaGetLastError();
+  return e != cudaSuccess || a.partial == nullptr ? e : join<typename Fm::P>(a, grid, s);
+}
+
+template <typename T, typename P, int VEC, int CH, bool kKeep>
+cudaError_t backward_go(const LayerNormGradArgs& a, dim3 block, cudaStream_t s, int num_sms) {
+  if constexpr (VEC > 1) {
+    if (a.cols == static_cast<int>(block.x) * CH * VEC)
+      return backward_launch<Form<T, P, VEC, CH, kKeep, true>>(a, block, s, num_sms);
+  }
+  return backward_launch<Form<T, P, VEC, CH, kKeep, false>>(a, block, s, num_sms);
 }
 
 template <typename T, typename P, int VEC>
 cudaError_t backward_vec(const LayerNormGradArgs& a, cudaStream_t s, int num_sms) {
   dim3 block;
-  // two 16-byte accesses per thread and tensor keep dw and db (32 fp32) in registers
-  // without spilling; four where the row needs them
-  switch (pick_accesses(a.cols / VEC, VEC == 1 ? 4 : 2, VEC == 1 ? 16 : 4, 512, &block)) {
-    case 1: return backward_go<T, P, VEC, 1>(a, block, s, num_sms);
-    case 2: return backward_go<T, P, VEC, 2>(a, block, s, num_sms);
-    case 4: return backward_go<T, P, VEC, 4>(a, block, s, num_sms);
-    case 8:
-      if constexpr (VEC == 1) return backward_go<T, P, VEC, 8>(a, block, s, num_sms);
-    case 16:
-      if constexpr (VEC == 1) return backward_go<T, P, VEC, 16>(a, block, s, num_sms);
-    default: break;
+  const int chunks = a.cols / VEC;
+  if (chunks <= 32 && pick_block(chunks, 1, 32, &block)) return backward_go<T, P, VEC, 1, true>(a, block, s, num_sms);
+  if (chunks <= 256 && pick_block(chunks, 2, 256, &block)) return backward_go<T, P, VEC, 2, true>(a, block, s, num_sms);
+  if (pick_block(chunks, 4, 256, &block)) return backward_go<T, P, VEC, 4, true>(a, block, s, num_sms);
+  if (pick_block(chunks, 4, 512, &block)) return backward_go<T, P, VEC, 4, false>(a, block, s, num_sms);
+  if constexpr (VEC == 1) {
+    if (pick_block(chunks, 16, 512, &block)) return backward_go<T, P, VEC, 16, false>(a, block, s, num_sms);
   }
   cudaError_t e = cudaSuccess;
   if (a.dx != nullptr) {

@@ -62,47 +62,34 @@ __device__ __forceinline__ void load_residual16(const LinearEpilogue& e, long lo
 }
 
 __device__ __forceinline__ float2 unpack2(uint32_t w, int dtype) {
-  if (dtype == QKV_CTE_DTYPE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return dtype == QKV_CTE_DTYPE_BF16 ? unpack_pair<__nv_bfloat16>(w) : unpack_pair<__half>(w);
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi, int dtype) {
-  if (dtype == QKV_CTE_DTYPE_BF16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// 16 bf16 parameters of consecutive columns as fp32 (16-byte aligned, all in range).
-__device__ __forceinline__ void load_bf16x16(const uint16_t* p, float* out) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    out[2 * j] = __uint_as_float(w[j] << 16);
-    out[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-  }
+  const float2 v = make_float2(lo, hi);
+  return dtype == QKV_CTE_DTYPE_BF16 ? pack_pair<__nv_bfloat16>(v) : pack_pair<__half>(v);
 }
 
 // The 16 columns at col0, whole and 32-byte aligned: v = acc * ascale (* col) + bias,
-// activation, gate, the residual's raw words r, one rounding, 32-byte stores.
+// activation, gate, the residual's raw words r, one rounding, 32-byte stores. col, bias
+// and gate are the columns' values in shared memory (16-byte aligned; read by every lane
+// alike), or null.
 __device__ __forceinline__ void finish16(const LinearEpilogue& e, long long row, int col0, const uint32_t* acc,
-                                         float ascale, const float* col, const uint16_t* bias, const uint32_t* r,
-                                         uint64_t pol) {
-  float v[16], p[16];
+                                         float ascale, const float* col, const float* bias, const float* gate,
+                                         const uint32_t* r, uint64_t pol) {
+  float v[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(acc[j]) * ascale;
-  if (col != nullptr) {
-    ld_params<float, 16>(col + col0, p);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] *= p[j];
-  }
-  if (bias != nullptr) {
-    load_bf16x16(bias + col0, p);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] += p[j];
+  for (int q = 0; q < 4; ++q) {
+    float4 c = make_float4(ascale, ascale, ascale, ascale), b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (col != nullptr) {
+      c = reinterpret_cast<const float4*>(col)[q];
+      c = make_float4(c.x * ascale, c.y * ascale, c.z * ascale, c.w * ascale);
+    }
+    if (bias != nullptr) b = reinterpret_cast<const float4*>(bias)[q];
+    v[4 * q + 0] = fmaf(__uint_as_float(acc[4 * q + 0]), c.x, b.x);
+    v[4 * q + 1] = fmaf(__uint_as_float(acc[4 * q + 1]), c.y, b.y);
+    v[4 * q + 2] = fmaf(__uint_as_float(acc[4 * q + 2]), c.z, b.z);
+    v[4 * q + 3] = fmaf(__uint_as_float(acc[4 * q + 3]), c.w, b.w);
   }
   switch (e.act) {  // one uniform branch for the 16 columns
     case QKV_CTE_ACT_GELU_TANH:
@@ -110,7 +97,7 @@ __device__ __forceinline__ void finish16(const LinearEpilogue& e, long long row,
       for (int j = 0; j < 16; ++j) v[j] = apply_act(v[j], QKV_CTE_ACT_GELU_TANH);
       break;
     case QKV_CTE_ACT_GELU_ERF:
-#pragma unroll 4
+#pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = apply_act(v[j], QKV_CTE_ACT_GELU_ERF);
       break;
     case QKV_CTE_ACT_SILU:
@@ -119,10 +106,15 @@ __device__ __forceinline__ void finish16(const LinearEpilogue& e, long long row,
       break;
     default: break;
   }
-  if (e.gate != nullptr) {
-    load_bf16x16(e.gate + col0, p);
+  if (gate != nullptr) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] *= p[j];
+    for (int q = 0; q < 4; ++q) {
+      const float4 p = reinterpret_cast<const float4*>(gate)[q];
+      v[4 * q + 0] *= p.x;
+      v[4 * q + 1] *= p.y;
+      v[4 * q + 2] *= p.z;
+      v[4 * q + 3] *= p.w;
+    }
   }
   if (e.dtype == QKV_CTE_DTYPE_FP32) {
     if (e.residual != nullptr) {

@@ -467,57 +467,90 @@ __device__ __forceinline__ void epilogue_drain_plain(const GemmShape& g, const G
   }
 }
 
-// Epilogue of the product (kEpiLinear): 32 columns per TMEM load; the residual's words of
-// the next 32 columns are requested before this chunk is finished, so that the epilogue
-// does not wait out the memory latency chunk by chunk. Rows off 32-byte boundaries and
+// Epilogue of the product (kEpiLinear). What a tile needs beside its accumulator is
+// requested while the MMAs still run: each epilogue warp copies the tile's column scales,
+// biases and gates into shared memory of its own (read back as broadcasts; loading them
+// from global memory 16 columns at a time exposed three L2 latencies per 16 columns and
+// took 1.6 times the MMAs' time at K = 5120), and each thread holds the residual words
+// of its row's next kLinearAhead columns in registers. Rows off 32-byte boundaries and
 // the ragged last 16 columns go element by element.
+constexpr int kLinearAhead = 64;  // columns
+
 template <int BN>
-__device__ __forceinline__ void epilogue_drain_linear(const GemmShape& g, const GemmArgs& a, uint32_t t_acc,
-                                                      int block128, int row_in_block, int col_base, uint64_t pol_out) {
-  const LinearEpilogue& e = a.lin;
-  const long long row = static_cast<long long>(block128) * 128 + row_in_block;
-  const bool row_ok = row < g.T;
-  const float ascale = row_ok ? a.a_scale[row] : 0.0f;
-  const bool fetch = e.residual != nullptr && e.wide && row_ok;
-  uint32_t res[2][16];
+struct LinearTile {
+  static constexpr int kParamBytes = 4 * 3 * BN * 4;  // 4 warps x (scale, bias, gate) x BN fp32
+
+  uint32_t res[kLinearAhead / 16][16];
+
+  static __device__ __forceinline__ bool fetches(const GemmShape& g, const LinearEpilogue& e, long long row) {
+    return e.residual != nullptr && e.wide && row < g.T;
+  }
+
+  // Before the wait for the accumulator. `params`: this warp's 3 * BN floats.
+  __device__ __forceinline__ void begin(const GemmShape& g, const GemmArgs& a, float* params, int block128,
+                                        int row_in_block, int col_base) {
+    const long long row = static_cast<long long>(block128) * 128 + row_in_block;
+    if (fetches(g, a.lin, row)) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (fetch && col_base + 16 * (h + 1) <= g.I) load_residual16(e, row, col_base + 16 * h, res[h]);
+      for (int i = 0; i < kLinearAhead / 16; ++i)
+        if (col_base + 16 * (i + 1) <= g.I) load_residual16(a.lin, row, col_base + 16 * i, res[i]);
+    }
+    __syncwarp();  // every lane has read the previous tile's
+#pragma unroll
+    for (int i = 0; i < (BN + 31) / 32; ++i) {
+      const int j = 32 * i + (threadIdx.x & 31);
+      const int c = col_base + j;
+      if (j < BN && c < g.I) {
+        if (a.w_col_scale != nullptr) params[j] = __ldg(a.w_col_scale + c);
+        if (a.bias != nullptr) params[BN + j] = bf16_bits_to_float(__ldg(a.bias + c));
+        if (a.lin.gate != nullptr) params[2 * BN + j] = bf16_bits_to_float(__ldg(a.lin.gate + c));
+      }
+    }
+    __syncwarp();
+  }
+
+  // 64 columns per turn, so that the window of residual words is indexed statically.
+  __device__ __forceinline__ void drain(const GemmShape& g, const GemmArgs& a, uint32_t t_acc, const float* params,
+                                        int block128, int row_in_block, int col_base, uint64_t pol_out) {
+    const LinearEpilogue& e = a.lin;
+    const long long row = static_cast<long long>(block128) * 128 + row_in_block;
+    const bool row_ok = row < g.T;
+    const float ascale = row_ok ? a.a_scale[row] : 0.0f;
+    const bool fetch = fetches(g, e, row);
 #pragma unroll 1
-  for (int c0 = 0; c0 < BN; c0 += 32) {
-    if (col_base + c0 >= g.I) break;  // uniform across the warp
-    uint32_t r[32];
-    if (c0 + 32 <= BN)
-      tmem_ld_32x32b_x32(t_acc + static_cast<uint32_t>(c0), r);
-    else
-      tmem_ld_32x32b_x16(t_acc + static_cast<uint32_t>(c0), r);
-    tmem_ld_wait();
+    for (int c0 = 0; c0 < BN; c0 += kLinearAhead) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int cc = c0 + 16 * h;
-      const int col0 = col_base + cc;
-      if (cc >= BN || col0 >= g.I) break;  // uniform across the warp
-      uint32_t now[16];
+      for (int i = 0; i < kLinearAhead / 16; ++i) {
+        const int cc = c0 + 16 * i;
+        const int col0 = col_base + cc;
+        if (cc >= BN || col0 >= g.I) break;  // uniform across the warp
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(t_acc + static_cast<uint32_t>(cc), r);
+        tmem_ld_wait();
+        if (row_ok) {
+          if (e.wide && col0 + 16 <= g.I) {
+            finish16(e, row, col0, r, ascale, a.w_col_scale != nullptr ? params + cc : nullptr,
+                     a.bias != nullptr ? params + BN + cc : nullptr, e.gate != nullptr ? params + 2 * BN + cc : nullptr,
+                     res[i], pol_out);
+          } else {
+            for (int j = 0; j < 16; ++j) {
+              const int c = col0 + j;
+              float acc = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) now[j] = res[h][j];
-      if (fetch && cc + 32 < BN && col0 + 48 <= g.I) load_residual16(e, row, col0 + 32, res[h]);
-      if (!row_ok) continue;
-      if (e.wide && col0 + 16 <= g.I) {
-        finish16(e, row, col0, r + 16 * h, ascale, a.w_col_scale, a.bias, now, pol_out);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int c = col0 + j;
-          if (c < g.I)
-            finish_one(e, row, c, __uint_as_float(r[16 * h + j]),
-                       a.w_col_scale != nullptr ? ascale * a.w_col_scale[c] : ascale,
-                       a.bias != nullptr ? bf16_bits_to_float(a.bias[c]) : 0.0f,
-                       e.gate != nullptr ? bf16_bits_to_float(e.gate[c]) : 1.0f);
+              for (int k = 0; k < 16; ++k) acc = j == k ? __uint_as_float(r[k]) : acc;
+              if (c < g.I)
+                finish_one(e, row, c, acc, a.w_col_scale != nullptr ? ascale * params[cc + j] : ascale,
+                           a.bias != nullptr ? params[BN + cc + j] : 0.0f,
+                           e.gate != nullptr ? params[2 * BN + cc + j] : 1.0f);
+            }
+          }
         }
+        if (fetch && cc + kLinearAhead < BN && col0 + kLinearAhead + 16 <= g.I)
+          load_residual16(e, row, col0 + kLinearAhead, res[i]);
       }
     }
   }
-}
+};
 
 // Epilogue kinds, each a separate instantiation of the kernels (the per-head ones need
 // more registers per thread, which would otherwise leave no room on an SM
@@ -536,8 +569,6 @@ __device__ __forceinline__ void epilogue_drain(const GemmShape& g, const GemmArg
                                                float& ss_k) {
   if constexpr (kEpi == kEpiHead)
     epilogue_drain_head<BN>(g, a, t_acc, block128, row_in_block, col_base, pol_out, ss_q, ss_k);
-  else if constexpr (kEpi == kEpiLinear)
-    epilogue_drain_linear<BN>(g, a, t_acc, block128, row_in_block, col_base, pol_out);
   else
     epilogue_drain_plain<BN, kEpi == kEpiStatsRms ? 2 : (kEpi == kEpiStatsLayer ? 3 : 0)>(
         g, a, t_acc, block128, row_in_block, col_base, pol_out, ss_q, ss_k);
@@ -1228,6 +1259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     FusedWork fw;
+    [[maybe_unused]] LinearTile<BN> lin;
+    [[maybe_unused]] float* lin_params = reinterpret_cast<float*>(sSFA + 768) + quarter * 3 * BN;
     const long long n_tasks = kFused ? nrp::task_count(nr, kFusedHeadGroup) : 0;
     const uint64_t once = kFused ? nrp::evict_first_policy() : 0;
     for (int seq = 0;; ++seq) {
@@ -1246,6 +1279,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tile < 0) break;
       int m_blk, n_blk;
       tile_coords(g, tile, m_blk, n_blk);
+      const int block128 = m_blk * 2 + static_cast<int>(rank);
+      // A 128-row half wholly past T (T mod 256 in (0, 128]) has nothing to store.
+      const bool live = block128 * kBM < g.T;
+      if constexpr (kEpi == kEpiLinear) {
+        if (live) lin.begin(g, a, lin_params, block128, row_in_block, n_blk * BN);
+      }
       bool ok;
       if constexpr (kFused)
         ok = fused_wait_acc(smem_u32(&tfull[acc]), acc_phase, abort_flag, nr, n_tasks, fw, once);
@@ -1257,13 +1296,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const int block128 = m_blk * 2 + static_cast<int>(rank);
-      // A 128-row half wholly past T (T mod 256 in (0, 128]) has nothing to store.
-      const bool live = block128 * kBM < g.T;
       float ss_q = 0.0f, ss_k = 0.0f;
-      if (live)
-        epilogue_drain<BN, kEpi>(g, a, t_lane + static_cast<uint32_t>(acc * BN), block128, row_in_block, n_blk * BN,
-                           pol_out, ss_q, ss_k);
+      if (live) {
+        if constexpr (kEpi == kEpiLinear)
+          lin.drain(g, a, t_lane + static_cast<uint32_t>(acc * BN), lin_params, block128, row_in_block, n_blk * BN,
+                    pol_out);
+        else
+          epilogue_drain<BN, kEpi>(g, a, t_lane + static_cast<uint32_t>(acc * BN), block128, row_in_block, n_blk * BN,
+                             pol_out, ss_q, ss_k);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), lead));
@@ -1323,8 +1364,9 @@ cudaError_t launch_gemm_pair_t(const GemmShape& g, const CUtensorMap& tmA, const
                                int num_sms) {
   using C = K1PairCfg<BN>;
   auto kern = qkv_gemm_mxf8_pair_kernel<BN, kEpi, kFused>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(C::SMEM));
+  constexpr size_t smem = C::SMEM + (kEpi == kEpiLinear ? LinearTile<BN>::kParamBytes : 0);
+  static_assert(smem <= C::SMEM_LIMIT, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int tiles = g.m_tiles * g.n_tiles;
   const int pairs = num_sms / 2;
@@ -1332,7 +1374,7 @@ cudaError_t launch_gemm_pair_t(const GemmShape& g, const CUtensorMap& tmA, const
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

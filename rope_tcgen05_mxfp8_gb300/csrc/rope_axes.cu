@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "block_ops.h"
+#include "fp32x2.cuh"
 #include "qkv_cte.h"
 #include "vec_io.cuh"
 
@@ -29,6 +30,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kHeadsPerThread = 8;  // heads a thread walks with one set of cos and sin
+constexpr int kHeadsAtOnce = 4;     // of which so many are requested ahead
 
 // cos and sin of pos * step turns (step: a binary fraction of a turn).
 __device__ __forceinline__ void turn(int pos, unsigned long long step, float& c, float& s) {
@@ -76,9 +78,72 @@ __device__ __forceinline__ int pair_axis_position(const RopeArgs& a, int pair, c
   return v;
 }
 
-// PV pairs per thread. T[PV] vectors at lo and at lo + d/2 (rotate-half), or 2 PV
-// elements at 2 lo (interleaved).
-template <typename T, int PV, bool kHalf>
+// PV pairs per thread: vectors of PV elements at lane p0 and at p0 + d/2 (rotate-half), or
+// one of 2 PV elements at 2 p0 (interleaved). cos and sin are computed while the first heads' loads are in flight.
+template <typename T, int PV>
+struct HalfPairs {
+  using V = Vec<T, PV>;
+  V lo, hi;
+  __device__ __forceinline__ void load(const T* x, int p0, int half) {
+    lo = ld_once<T, PV>(x + p0);
+    hi = ld_once<T, PV>(x + p0 + half);
+  }
+  __device__ __forceinline__ void store(T* y, int p0, int half) const {
+    st_vec(y + p0, lo);
+    st_vec(y + p0 + half, hi);
+  }
+  __device__ __forceinline__ void rotate(const float* c, const float* s) {
+    if constexpr (PV == 1) {
+      const float a = lo.one(), b = hi.one();
+      lo.set_one(a * c[0] - b * s[0]);
+      hi.set_one(b * c[0] + a * s[0]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < PV / 2; ++j) {
+        const float2 a = lo.pair(j), b = hi.pair(j);
+        const float2 cc = make_float2(c[2 * j], c[2 * j + 1]), ss = make_float2(s[2 * j], s[2 * j + 1]);
+        lo.set_pair(j, ffma2(a, cc, fmul2(b, make_float2(-ss.x, -ss.y))));
+        hi.set_pair(j, ffma2(b, cc, fmul2(a, ss)));
+      }
+    }
+  }
+};
+
+template <typename T, int PV>
+struct NeighbourPairs {
+  using V = Vec<T, 2 * PV>;
+  V v;
+  __device__ __forceinline__ void load(const T* x, int p0, int) { v = ld_once<T, 2 * PV>(x + 2 * p0); }
+  __device__ __forceinline__ void store(T* y, int p0, int) const { st_vec(y + 2 * p0, v); }
+  __device__ __forceinline__ void rotate(const float* c, const float* s) {
+#pragma unroll
+    for (int j = 0; j < PV; ++j) {
+      const float2 a = v.pair(j);
+      v.set_pair(j, make_float2(a.x * c[j] - a.y * s[j], a.y * c[j] + a.x * s[j]));
+    }
+  }
+};
+
+// Neighbouring lanes at an address that keeps no pair together (2-byte aligned only).
+template <typename T>
+struct ScatteredPair {
+  Vec<T, 1> lo, hi;
+  __device__ __forceinline__ void load(const T* x, int p0, int) {
+    lo = ld_once<T, 1>(x + 2 * p0);
+    hi = ld_once<T, 1>(x + 2 * p0 + 1);
+  }
+  __device__ __forceinline__ void store(T* y, int p0, int) const {
+    st_vec(y + 2 * p0, lo);
+    st_vec(y + 2 * p0 + 1, hi);
+  }
+  __device__ __forceinline__ void rotate(const float* c, const float* s) {
+    const float a = lo.one(), b = hi.one();
+    lo.set_one(a * c[0] - b * s[0]);
+    hi.set_one(b * c[0] + a * s[0]);
+  }
+};
+
+template <typename T, int PV, typename Pairs>
 __global__ void __launch_bounds__(kRopeThreads) rope_apply_kernel(const __grid_constant__ RopeArgs a) {
   const int half = a.d >> 1;
   const int per_row = half / PV;
@@ -88,45 +153,48 @@ __global__ void __launch_bounds__(kRopeThreads) rope_apply_kernel(const __grid_c
   const int p0 = static_cast<int>(idx - row * per_row) * PV;
   const int b = static_cast<int>(row / a.seq);
   const int s = static_cast<int>(row - static_cast<long long>(b) * a.seq);
+  const int h0 = blockIdx.y * kHeadsPerThread;
+  const T* x = static_cast<const T*>(a.x) + b * a.xb + s * a.xs + h0 * a.xh;
+  T* y = static_cast<T*>(a.y) + b * a.yb + s * a.ys + h0 * a.yh;
+  const int n = min(a.heads - h0, kHeadsPerThread);
+  Pairs v[kHeadsAtOnce];
+#pragma unroll
+  for (int k = 0; k < kHeadsAtOnce; ++k)
+    if (k < n) v[k].load(x + k * a.xh, p0, half);
   int pos[kRopeMaxAxes];
   const bool live = row_position(a, b, s, pos);
-  const T* x = static_cast<const T*>(a.x) + b * a.xb + s * a.xs;
-  T* y = static_cast<T*>(a.y) + b * a.yb + s * a.ys;
-  if (!live && x == y) return;
+  if (!live && a.x == a.y) return;  // padding in place
   float cs[PV], sn[PV];
 #pragma unroll
   for (int j = 0; j < PV; ++j) {
     turn(pair_axis_position(a, p0 + j, pos), a.step[p0 + j], cs[j], sn[j]);
     if (a.inverse) sn[j] = -sn[j];
   }
-  const int h1 = min(a.heads, static_cast<int>(blockIdx.y + 1) * kHeadsPerThread);
-  const int off0 = kHalf ? p0 : 2 * p0;
-  const int off1 = kHalf ? p0 + half : 2 * p0 + PV;
-#pragma unroll 4
-  for (int h = blockIdx.y * kHeadsPerThread; h < h1; ++h) {
-    const Vec<T, PV> v0 = ld_once<T, PV>(x + h * a.xh + off0);
-    const Vec<T, PV> v1 = ld_once<T, PV>(x + h * a.xh + off1);
-    Vec<T, PV> o0 = v0, o1 = v1;
-    if (live) {
+  for (int h = 0; h < n; h += kHeadsAtOnce) {
 #pragma unroll
-      for (int j = 0; j < PV; ++j) {
-        // interleaved: element 2j of the 2 PV (v0 then v1) and its neighbour
-        const float lo = to_f32(kHalf ? v0.v[j] : (2 * j < PV ? v0.v[2 * j % PV] : v1.v[2 * j % PV]));
-        const float hi = to_f32(kHalf ? v1.v[j] : (2 * j + 1 < PV ? v0.v[(2 * j + 1) % PV] : v1.v[(2 * j + 1) % PV]));
-        const T ylo = from_f32<T>(lo * cs[j] - hi * sn[j]);
-        const T yhi = from_f32<T>(hi * cs[j] + lo * sn[j]);
-        if (kHalf) {
-          o0.v[j] = ylo;
-          o1.v[j] = yhi;
-        } else {
-          if (2 * j < PV) o0.v[2 * j % PV] = ylo; else o1.v[2 * j % PV] = ylo;
-          if (2 * j + 1 < PV) o0.v[(2 * j + 1) % PV] = yhi; else o1.v[(2 * j + 1) % PV] = yhi;
-        }
+    for (int k = 0; k < kHeadsAtOnce; ++k) {
+      if (h + k < n) {
+        Pairs o = v[k];
+        if (h + k + kHeadsAtOnce < n) v[k].load(x + (h + k + kHeadsAtOnce) * a.xh, p0, half);
+        if (live) o.rotate(cs, sn);  // padding rows keep their values, whatever they are
+        o.store(y + (h + k) * a.yh, p0, half);
       }
     }
-    st_vec(y + h * a.yh + off0, o0);
-    st_vec(y + h * a.yh + off1, o1);
   }
+}
+
+// The same PV values at two places of a table row.
+template <int PV>
+__device__ __forceinline__ void store_table(float* p, float* q, const float* v) {
+  Vec<float, PV> o;
+  if constexpr (PV == 1) {
+    o.set_one(v[0]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < PV / 2; ++j) o.set_pair(j, make_float2(v[2 * j], v[2 * j + 1]));
+  }
+  st_vec(p, o);
+  st_vec(q, o);
 }
 
 // Tables: fp32 [batch * seq, d], each pair's value at both of its lanes.
@@ -142,51 +210,59 @@ __global__ void __launch_bounds__(kRopeThreads) rope_tables_kernel(const __grid_
   const int b = static_cast<int>(row / a.seq);
   int pos[kRopeMaxAxes];
   const bool live = row_position(a, b, static_cast<int>(row - static_cast<long long>(b) * a.seq), pos);
-  Vec<float, PV> c, s;
+  float c[PV], s[PV];
 #pragma unroll
   for (int j = 0; j < PV; ++j) {
-    c.v[j] = 1.0f;
-    s.v[j] = 0.0f;
-    if (live) turn(pair_axis_position(a, p0 + j, pos), a.step[p0 + j], c.v[j], s.v[j]);
+    c[j] = 1.0f;
+    s[j] = 0.0f;
+    if (live) turn(pair_axis_position(a, p0 + j, pos), a.step[p0 + j], c[j], s[j]);
   }
   float* cr = cos_t + row * a.d;
   float* sr = sin_t + row * a.d;
   if constexpr (kHalf) {
-    st_vec(cr + p0, c);
-    st_vec(cr + p0 + half, c);
-    st_vec(sr + p0, s);
-    st_vec(sr + p0 + half, s);
+    store_table<PV>(cr + p0, cr + p0 + half, c);
+    store_table<PV>(sr + p0, sr + p0 + half, s);
   } else {
 #pragma unroll
     for (int j = 0; j < PV; ++j) {
-      st_vec(cr + 2 * (p0 + j), Vec<float, 2>{{c.v[j], c.v[j]}});
-      st_vec(sr + 2 * (p0 + j), Vec<float, 2>{{s.v[j], s.v[j]}});
+      reinterpret_cast<float2*>(cr)[p0 + j] = make_float2(c[j], c[j]);
+      reinterpret_cast<float2*>(sr)[p0 + j] = make_float2(s[j], s[j]);
     }
   }
 }
 
-template <typename T, int PV, bool kHalf>
+template <typename T, int PV, typename Pairs>
 cudaError_t apply_go(const RopeArgs& a, cudaStream_t s) {
   const long long threads = static_cast<long long>(a.batch) * a.seq * ((a.d >> 1) / PV);
   const long long blocks = (threads + kRopeThreads - 1) / kRopeThreads;
   const dim3 grid(static_cast<unsigned>(blocks), (a.heads + kHeadsPerThread - 1) / kHeadsPerThread);
-  rope_apply_kernel<T, PV, kHalf><<<grid, kRopeThreads, 0, s>>>(a);
+  rope_apply_kernel<T, PV, Pairs><<<grid, kRopeThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, bool kHalf>
-cudaError_t apply_t(const RopeArgs& a, cudaStream_t s) {
-  // the widest access that divides a head's pairs and that pointers and strides allow
-  int pv = 16 / static_cast<int>(sizeof(T));
+// The widest access that divides a head's pairs and that pointers and strides allow.
+template <typename T>
+cudaError_t apply_t(const RopeArgs& a, bool rotate_half, cudaStream_t s) {
+  const int half = a.d >> 1;
   const uintptr_t where = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y);
   const long long strides = a.xb | a.xs | a.xh | a.yb | a.ys | a.yh;
-  while (pv > 1 && ((a.d >> 1) % pv != 0 || where % (pv * sizeof(T)) != 0 || strides % pv != 0)) pv >>= 1;
-  switch (pv) {
+  int n = 16 / static_cast<int>(sizeof(T));  // elements per access
+  while (n > 1 && ((rotate_half ? half % n : a.d % n) != 0 || where % (n * sizeof(T)) != 0 || strides % n != 0)) n >>= 1;
+  if (rotate_half) {
+    switch (n) {
+      case 8:
+        if constexpr (sizeof(T) == 2) return apply_go<T, 8, HalfPairs<T, 8>>(a, s);
+      case 4: return apply_go<T, 4, HalfPairs<T, 4>>(a, s);
+      case 2: return apply_go<T, 2, HalfPairs<T, 2>>(a, s);
+      default: return apply_go<T, 1, HalfPairs<T, 1>>(a, s);
+    }
+  }
+  switch (n) {
     case 8:
-      if constexpr (sizeof(T) == 2) return apply_go<T, 8, kHalf>(a, s);
-    case 4: return apply_go<T, 4, kHalf>(a, s);
-    case 2: return apply_go<T, 2, kHalf>(a, s);
-    default: return apply_go<T, 1, kHalf>(a, s);
+      if constexpr (sizeof(T) == 2) return apply_go<T, 4, NeighbourPairs<T, 4>>(a, s);
+    case 4: return apply_go<T, 2, NeighbourPairs<T, 2>>(a, s);
+    case 2: return apply_go<T, 1, NeighbourPairs<T, 1>>(a, s);
+    default: return apply_go<T, 1, ScatteredPair<T>>(a, s);
   }
 }
 
@@ -203,10 +279,9 @@ cudaError_t tables_go(const RopeArgs& a, float* cos_t, float* sin_t, cudaStream_
 cudaError_t launch_rope_apply(const RopeArgs& a, int dtype, bool rotate_half, cudaStream_t s) {
   if (static_cast<long long>(a.batch) * a.seq * a.heads == 0) return cudaSuccess;
   switch (dtype) {
-    case QKV_CTE_DTYPE_BF16:
-      return rotate_half ? apply_t<__nv_bfloat16, true>(a, s) : apply_t<__nv_bfloat16, false>(a, s);
-    case QKV_CTE_DTYPE_FP16: return rotate_half ? apply_t<__half, true>(a, s) : apply_t<__half, false>(a, s);
-    default: return rotate_half ? apply_t<float, true>(a, s) : apply_t<float, false>(a, s);
+    case QKV_CTE_DTYPE_BF16: return apply_t<__nv_bfloat16>(a, rotate_half, s);
+    case QKV_CTE_DTYPE_FP16: return apply_t<__half>(a, rotate_half, s);
+    default: return apply_t<float>(a, rotate_half, s);
   }
 }
 
