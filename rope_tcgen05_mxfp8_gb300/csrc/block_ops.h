@@ -37,14 +37,14 @@ struct LayerNormGradArgs {
   long long lddx;
   void* dweight;  // [cols] or null
   void* dbias;    // [cols] or null
-  float* partial;  // [parts][2][cols] column sums of each block, or null: no dweight or dbias
+  float* partial;  // [parts][2][cols] partial column sums, or null: no dweight or dbias
   int max_parts;
   long long rows;
   int cols;
 };
 
-// Blocks whose column sums the backward pass keeps apart (bounds its workspace).
-constexpr int kLayerNormMaxParts = 608;
+// Partial rows of column sums the backward pass keeps apart (bounds its workspace).
+constexpr int kLayerNormMaxParts = 128;
 
 cudaError_t launch_layer_norm(const LayerNormArgs& a, int dtype, int param_dtype, cudaStream_t s, int num_sms);
 // `sums`: dweight and/or dbias are wanted (with no rows they are zeros).

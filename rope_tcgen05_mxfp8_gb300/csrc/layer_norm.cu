@@ -23,6 +23,7 @@
 
 #include "block_ops.h"
 #include "fp32x2.cuh"
+#include "ptx.cuh"
 #include "qkv_cte.h"
 #include "vec_io.cuh"
 
@@ -32,6 +33,7 @@ namespace {
 
 constexpr int kWarpRows = 4;  // rows (warps) per block of the warp-per-row form
 
+constexpr int kGradCluster = 4;  // blocks whose column sums are joined on chip
 constexpr int kRing = 3;      // rows in flight per group of threads
 
 // Sums of N values over the group of threads that holds a row: a warp (blockDim.x ==
@@ -124,7 +126,7 @@ struct Lanes<1> {
 template <typename T, int VEC, int CH, bool kFull>
 struct RowStream {
   static constexpr bool kAsync = VEC > 1;
-  // rows kept requested: as many as shared memory takes for long rows
+  // rows kept requested
   static constexpr int kAhead = !kAsync ? 1 : (CH > 2 ? 2 : kRing);
   static constexpr int kBytes = kAsync ? kAhead * CH * 16 : 0;  // of the ring, per thread
 
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(1024) layer_norm_long_kernel(LayerNormArgs a) 
   }
 }
 
-// Columns fixed to threads; the block's column sums leave as one row of the workspace.
+// Columns fixed to threads; a cluster's column sums leave as one row of the workspace.
 // The second sweep takes the row from the ring again: keeping xh and g instead cost 64
 // registers at four accesses per thread, and with them the second block on an SM.
 template <typename Fm>
@@ -375,6 +377,11 @@ __global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_backward_ker
   T* out_row = a.dx != nullptr ? static_cast<T*>(a.dx) + first * a.lddx + threadIdx.x * VEC : nullptr;
   int slot = 0;
   for (int k = 0; k < n; ++k) {
+    float mean_next = 0.0f, rstd_next = 0.0f;  // requested a whole row before their use
+    if (k + 1 < n) {
+      mean_next = *(mean_p += step);
+      rstd_next = *(rstd_p += step);
+    }
     cp_async_wait<kAhead - 1>();
     if (!Fm::kKeep) wp.load(a.weight, a.cols, 1.0f);
     F s1 = L::all(0.0f), s2 = L::all(0.0f);
@@ -420,49 +427,49 @@ __global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_backward_ker
     gin.request(a.cols, slot);
     cp_async_commit();
     slot = slot + 1 == kAhead ? 0 : slot + 1;
-    if (k + 1 < n) {
-      mean = *(mean_p += step);
-      rstd = *(rstd_p += step);
-    }
+    mean = mean_next;
+    rstd = rstd_next;
   }
   if (a.partial == nullptr) return;
-  float* out = a.partial + static_cast<size_t>(blockIdx.x) * 2 * a.cols;
-  if (blockDim.y > 1) {  // the block's rows (warps) one after the other, in order
-    float* sums = reinterpret_cast<float*>(ring_mem);
-    cp_async_wait<0>();
-    __syncthreads();  // no warp reads the ring any more
-    for (int r = 0; r < static_cast<int>(blockDim.y); ++r) {
-      if (static_cast<int>(threadIdx.y) == r) {
+  // The block's column sums [2][cols] to shared memory (several rows per block: the warps
+  // one after the other), then the cluster's blocks added in order, each block taking a
+  // share of the columns: one partial row per cluster goes to the workspace.
+  float* sums = reinterpret_cast<float*>(ring_mem);
+  cp_async_wait<0>();
+  __syncthreads();  // no thread reads the ring any more
+  for (int r = 0; r < static_cast<int>(blockDim.y); ++r) {
+    if (static_cast<int>(threadIdx.y) == r) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int c = (i * blockDim.x + threadIdx.x) * VEC;
-          if (Stream::inside(i, a.cols)) {
+      for (int i = 0; i < CH; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * VEC;
+        if (Stream::inside(i, a.cols)) {
 #pragma unroll
-            for (int j = 0; j < L::N; ++j) {
-              F* p = reinterpret_cast<F*>(sums + c) + j;  // [cols] then [cols]: cols is even where F is a pair
-              *p = r == 0 ? dw[i][j] : vadd(*p, dw[i][j]);
-              p = reinterpret_cast<F*>(sums + a.cols + c) + j;
-              *p = r == 0 ? db[i][j] : vadd(*p, db[i][j]);
-            }
+          for (int j = 0; j < L::N; ++j) {
+            F* p = reinterpret_cast<F*>(sums + c) + j;  // cols is even where F is a pair
+            *p = r == 0 ? dw[i][j] : vadd(*p, dw[i][j]);
+            p = reinterpret_cast<F*>(sums + a.cols + c) + j;
+            *p = r == 0 ? db[i][j] : vadd(*p, db[i][j]);
           }
         }
       }
-      __syncthreads();
     }
-    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < 2 * a.cols; c += blockDim.x * blockDim.y) out[c] = sums[c];
-    return;
+    if (blockDim.y > 1) __syncthreads();
   }
+  cluster_sync();
+  const uint32_t base = smem_u32(sums);
+  const int threads = blockDim.x * blockDim.y;
+  float* out = a.partial + static_cast<size_t>(blockIdx.x / kGradCluster) * 2 * a.cols;
+  for (int c = cluster_ctarank() * threads + threadIdx.y * blockDim.x + threadIdx.x; c < 2 * a.cols;
+       c += kGradCluster * threads) {
+    float v[kGradCluster];
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * VEC;
-    if (c < a.cols) {
+    for (int r = 0; r < kGradCluster; ++r) v[r] = ld_shared_cluster_f32(mapa_shared(base + 4 * c, r));
+    float t = v[0];
 #pragma unroll
-      for (int j = 0; j < L::N; ++j) {
-        reinterpret_cast<F*>(out + c)[j] = dw[i][j];
-        reinterpret_cast<F*>(out + a.cols + c)[j] = db[i][j];
-      }
-    }
+    for (int r = 1; r < kGradCluster; ++r) t += v[r];
+    out[c] = t;
   }
+  cluster_sync();  // no block leaves while another reads its sums
 }
 
 // Rows longer than the registers: dx with two sweeps over the row ...
@@ -635,15 +642,32 @@ template <typename Fm>
 cudaError_t backward_launch(const LayerNormGradArgs& a, dim3 block, cudaStream_t s, int num_sms) {
   auto k = layer_norm_backward_kernel<Fm>;
   size_t smem = 2 * static_cast<size_t>(Fm::Stream::kBytes) * block.x * block.y;
-  if (block.y > 1) smem = std::max(smem, 2 * sizeof(float) * static_cast<size_t>(a.cols));
+  const bool sums = a.partial != nullptr;
+  if (sums) smem = std::max(smem, 2 * sizeof(float) * static_cast<size_t>(a.cols));
   cudaError_t e = allow_smem(k, smem);
   if (e != cudaSuccess) return e;
-  long long groups = (a.rows + block.y - 1) / block.y;
-  if (a.partial != nullptr) groups = std::min<long long>(groups, a.max_parts);
-  const int grid = resident_grid(k, block, smem, num_sms, groups);
-  k<<<grid, block, smem, s>>>(a);
-  e = cudaGetLastError();
-  return e != cudaSuccess || a.partial == nullptr ? e : join<typename Fm::P>(a, grid, s);
+  const long long groups = (a.rows + block.y - 1) / block.y;
+  const int cluster = sums ? kGradCluster : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // one wave: a cluster stays within a GPC, so fewer blocks of clusters than of single
+  // blocks are resident at once
+  int resident = 0;
+  if (cudaOccupancyMaxActiveClusters(&resident, k, &cfg) != cudaSuccess || resident < 1) resident = num_sms / cluster;
+  if (sums) resident = std::min(resident, a.max_parts);
+  const int grid = static_cast<int>(std::min<long long>((groups + cluster - 1) / cluster, resident)) * cluster;
+  cfg.gridDim = dim3(grid);
+  e = cudaLaunchKernelEx(&cfg, k, a);
+  return e != cudaSuccess || !sums ? e : join<typename Fm::P>(a, grid / cluster, s);
 }
 
 template <typename T, typename P, int VEC, int CH, bool kKeep>

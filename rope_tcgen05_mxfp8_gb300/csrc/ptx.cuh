@@ -307,6 +307,12 @@ __device__ __forceinline__ void st_shared_cluster_s32(uint32_t cluster_addr, int
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
 // try_wait with acquire at cluster scope: for a phase completed by a release arrive of
 // the other CTA of the cluster, so that its earlier stores into this CTA's shared
 // memory are visible afterwards.
