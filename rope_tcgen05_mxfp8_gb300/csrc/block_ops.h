@@ -87,6 +87,22 @@ struct LinearEpilogue {
   void* out;
   long long ldo;
   int wide;               // residual and output rows start on 32-byte boundaries
+  int pairs;              // ... on boundaries of two elements
+};
+
+// The product's channel-major form (linear_few.cu).
+struct LinearFewArgs {
+  const float* a_scale;
+  const float* w_col_scale;  // or null
+  const uint16_t* bias;      // or null
+  const uint8_t* w_sf;       // [N, k_blocks]
+  int T, N;
+  int k_blocks;              // K / 32
+  int k_stages;              // ceil(K / 128)
+  int split;                 // CTAs of a cluster that share a tile's K blocks: 1, 2, 4 or 8, <= k_stages
+  uint32_t flags;
+  uint32_t* status;
+  LinearEpilogue lin;
 };
 
 }  // namespace qkvcte

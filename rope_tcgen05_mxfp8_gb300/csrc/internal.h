@@ -271,6 +271,11 @@ cudaError_t launch_gemm_head(const GemmShape& g, const CUtensorMap& tmA, const C
 // K1 (CTA-pair form) with the product's epilogue (qkv_gemm_mxf8_linear.cu).
 cudaError_t launch_gemm_linear(const GemmShape& g, const CUtensorMap& tmA, const CUtensorMap& tmW,
                                const CUtensorMap& tmSF, const GemmArgs& a, cudaStream_t s, int num_sms);
+// The product's channel-major form: token tiles of 16, 32, 64 or 128; tmA boxes
+// of token_tile rows, tmW boxes of 128. After a producer step it is launched as its
+// programmatic dependent.
+cudaError_t launch_linear_few(const CUtensorMap& tmA, const CUtensorMap& tmW, int token_tile, const LinearFewArgs& a,
+                              bool after_producer, cudaStream_t s);
 // K1 (CTA-pair form) with the norm/RoPE tasks run by its epilogue warps
 // (qkv_gemm_mxf8_fused.cu); launch_gemm calls it when given `fused`.
 cudaError_t launch_gemm_fused(const GemmShape& g, const CUtensorMap& tmA, const CUtensorMap& tmW,

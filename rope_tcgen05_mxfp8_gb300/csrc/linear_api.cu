@@ -27,9 +27,38 @@ struct qkv_cte_linear_plan_s {
   qkv_cte_linear_desc d;
   GemmShape g;
   LinearLayout ws;
+  bool few;        // the channel-major form; else K1, but for rows it would store element by element
+  int token_tile;  // of the channel-major form
+  int split;
 };
 
 namespace {
+
+// Token tile and K split of the channel-major form, and whether it is the form for a
+// problem (its rows' alignment aside). Measured on GB300, us a call, K1 against it:
+//   T, K, N            K1     token tile / split
+//   1, 5120, 5120      51     12.4 (16/4)
+//   16, 5120, 20480    107    27.4 (16/1)
+//   128, 1024, 5120    22.7   12.5 (64/2)
+//   256, 5120, 5120    31.0   24.7 (128/2)
+//   128, 5120, 20480   54     36.7 (128/1)
+//   512, 1024, 5120    24.2   20.6 (128/1)
+//   512, 5120, 5120    32.9   34.9 (128/1)
+//   256, 5120, 20480   54     65.7 (128/1, 320 tiles)
+// It wins while its tiles fit the SMs about once (two CTAs share an SM, at the expense of
+// each other's loads); smaller token tiles add CTAs while there are few.
+bool choose_few(const GemmShape& g, int* token_tile, int* split) {
+  const long long channel_tiles = (g.I + 127) / 128;
+  int nt = 16;
+  while (nt < 64 && nt < g.T) nt *= 2;
+  if (channel_tiles * ((g.T + nt - 1) / nt) > 80 && g.T > 64) nt = 128;
+  const long long tiles = channel_tiles * ((g.T + nt - 1) / nt);
+  int s = 1;
+  while (s < 8 && 2 * s <= g.k_stages && tiles * 2 * s <= 192) s *= 2;
+  *token_tile = nt;
+  *split = s;
+  return g.T <= 64 || (g.T <= 512 && tiles <= 160);
+}
 
 size_t out_size(const qkv_cte_linear_desc& d) { return d.out_dtype == QKV_CTE_DTYPE_FP32 ? 4 : 2; }
 
@@ -78,11 +107,17 @@ int qkv_cte_linear_plan(qkv_cte_linear_plan_t* out, const qkv_cte_linear_desc* d
   g.sf_chunks = gemm_sf_chunks(g.tile_n);
   g.n_qk_tiles = 0;
   make_bands(g, band_tiles(g));
+  p->few = choose_few(g, &p->token_tile, &p->split);
   LinearLayout& w = p->ws;
   w.sf_off = 256;
-  w.ready_off = w.sf_off + align_up((size_t)g.n_tiles * g.k_stages * g.sf_chunks * kSfBlockBytesPerChunk, 256);
-  w.sm_busy_off = w.ready_off + align_up((size_t)g.blocks128 * sizeof(uint32_t), 256);
-  w.act_off = w.sm_busy_off + align_up((size_t)kSmTable * sizeof(uint32_t), 256);
+  w.ready_off = w.sf_off;
+  w.sm_busy_off = w.ready_off;
+  w.act_off = w.sm_busy_off;
+  if (!p->few) {
+    w.ready_off = w.sf_off + align_up((size_t)g.n_tiles * g.k_stages * g.sf_chunks * kSfBlockBytesPerChunk, 256);
+    w.sm_busy_off = w.ready_off + align_up((size_t)g.blocks128 * sizeof(uint32_t), 256);
+    w.act_off = w.sm_busy_off + align_up((size_t)kSmTable * sizeof(uint32_t), 256);
+  }
   const bool produced = d.input_layout != QKV_CTE_INPUT_ROW_FP8;
   w.act_scale_off = w.act_off + (produced ? align_up((size_t)g.T * g.H, 256) : 0);
   w.total = w.act_scale_off + (produced ? align_up((size_t)g.T * sizeof(float), 256) : 0);
@@ -153,11 +188,26 @@ int qkv_cte_linear_run(qkv_cte_linear_plan_t plan, const void* A, const float* a
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const uint8_t* codes = produced ? ws + plan->ws.act_off : static_cast<const uint8_t*>(A);
   const float* scales = produced ? reinterpret_cast<const float*>(ws + plan->ws.act_scale_off) : a_scale;
+  LinearEpilogue lin{};
+  lin.act = d.act;
+  lin.dtype = d.out_dtype;
+  lin.gate = gate;
+  lin.residual = residual;
+  lin.ldr = T > 1 ? residual_row_stride : 0;
+  lin.out = O;
+  lin.ldo = T > 1 ? out_row_stride : 0;
+  lin.wide = aligned(O, 32) && (lin.ldo * e) % 32 == 0 &&
+             (!residual || (aligned(residual, 32) && (lin.ldr * e) % 32 == 0));
+  lin.pairs = aligned(O, 2 * e) && lin.ldo % 2 == 0 && (!residual || (aligned(residual, 2 * e) && lin.ldr % 2 == 0));
+  // K1 would store rows off 32-byte boundaries element by element
+  const bool few = plan->few || (!lin.wide && (g.T + plan->token_tile - 1) / plan->token_tile <= 65535);
   uint8_t* sf_packed = ws + plan->ws.sf_off;
   CUtensorMap tmA, tmW, tmSF;
-  if ((rc = encode_operand(&tmA, codes, (uint64_t)g.T, (uint64_t)g.H, 128u, "A")) != QKV_CTE_OK) return rc;
-  if ((rc = encode_operand(&tmW, W, (uint64_t)g.I, (uint64_t)g.H, (uint32_t)g.tile_n / 2, "W")) != QKV_CTE_OK) return rc;
-  if ((rc = encode_scales(&tmSF, sf_packed, g)) != QKV_CTE_OK) return rc;
+  rc = encode_operand(&tmA, codes, (uint64_t)g.T, (uint64_t)g.H, few ? (uint32_t)plan->token_tile : 128u, "A");
+  if (rc != QKV_CTE_OK) return rc;
+  rc = encode_operand(&tmW, W, (uint64_t)g.I, (uint64_t)g.H, few ? 128u : (uint32_t)g.tile_n / 2, "W");
+  if (rc != QKV_CTE_OK) return rc;
+  if (!few && (rc = encode_scales(&tmSF, sf_packed, g)) != QKV_CTE_OK) return rc;
 
   cudaError_t err = cudaSuccess;
   if (d.input_layout == QKV_CTE_INPUT_PACKED)
@@ -167,6 +217,13 @@ int qkv_cte_linear_run(qkv_cte_linear_plan_t plan, const void* A, const float* a
     err = launch_row_quantize(static_cast<const uint16_t*>(A), g.T, g.H, ws + plan->ws.act_off,
                               reinterpret_cast<float*>(ws + plan->ws.act_scale_off), nullptr, s, dev.sms);
   if (err != cudaSuccess) return fail(QKV_CTE_ERR_CUDA, "%s: producer launch: %s", who, cudaGetErrorString(err));
+  if (few) {
+    const LinearFewArgs fa{scales,     w_col_scale, bias,    w_sf,                            g.T, g.I, g.H / 32, g.k_stages,
+                           plan->split, d.flags,     reinterpret_cast<uint32_t*>(ws), lin};
+    err = launch_linear_few(tmA, tmW, plan->token_tile, fa, produced, s);
+    if (err != cudaSuccess) return fail(QKV_CTE_ERR_CUDA, "%s: GEMM launch: %s", who, cudaGetErrorString(err));
+    return ok();
+  }
   unsigned long long* stamps = reinterpret_cast<unsigned long long*>(ws + kStampOffset);
   uint32_t* ready = reinterpret_cast<uint32_t*>(ws + plan->ws.ready_off);
   uint32_t* sm_busy = reinterpret_cast<uint32_t*>(ws + plan->ws.sm_busy_off);
@@ -185,15 +242,7 @@ int qkv_cte_linear_run(qkv_cte_linear_plan_t plan, const void* A, const float* a
   a.status = reinterpret_cast<uint32_t*>(ws);
   a.flags = d.flags;
   a.d_head = 16;
-  a.lin.act = d.act;
-  a.lin.dtype = d.out_dtype;
-  a.lin.gate = gate;
-  a.lin.residual = residual;
-  a.lin.ldr = T > 1 ? residual_row_stride : 0;
-  a.lin.out = O;
-  a.lin.ldo = T > 1 ? out_row_stride : 0;
-  a.lin.wide = aligned(O, 32) && (a.lin.ldo * e) % 32 == 0 &&
-               (!residual || (aligned(residual, 32) && (a.lin.ldr * e) % 32 == 0));
+  a.lin = lin;
   err = launch_gemm_linear(g, tmA, tmW, tmSF, a, s, dev.sms);
   if (err != cudaSuccess) return fail(QKV_CTE_ERR_CUDA, "%s: GEMM launch: %s", who, cudaGetErrorString(err));
   return ok();

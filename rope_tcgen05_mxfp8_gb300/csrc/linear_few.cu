@@ -1,0 +1,420 @@
+// The product in its channel-major form: 128 output channels take the MMA's M side, a
+// tile of tokens its N side, and a cluster splits K and joins its sums on chip.
+//
+// With few tokens the product reads W once and is bound by that read (and, for the
+// smallest calls, by latency). K1's 256-token tiles would leave most SMs idle there: 40
+// tiles of 128 channels cover N = 5120. So each tile's K blocks are divided among the 1
+// to 8 CTAs of a cluster, every CTA streams its share of W once through a ring of
+// 128-byte K blocks, and the partial sums [token][channel] meet in shared memory: CTA r
+// of the cluster finishes tokens r, r + S, ... by reading all S parts in order through
+// distributed shared memory. There is no workspace and no second launch, and the result
+// does not depend on the schedule. W's block scales go straight from w_sf to the layout
+// tcgen05.cp wants (a warp gathers one word per channel and K block), so no repack
+// kernel runs either. Lanes of the epilogue own channels: consecutive lanes store
+// consecutive elements, whatever the alignment of O's rows, which is why rows off 32-byte
+// boundaries take this form at any token count.
+//
+// The tokens carry no block scales (their scale is the fp32 row scale): their side's
+// scale factors are the constant 2^0. Every wait is bounded as in K1.
+#include <algorithm>
+
+#include "internal.h"
+#include "linear_epilogue.cuh"
+#include "ptx.cuh"
+
+namespace qkvcte {
+
+namespace {
+
+constexpr int kFewThreads = 256;  // load, MMA and scale warps, one idle; four epilogue warps
+constexpr int kChannels = 128;
+constexpr int kFewK = 128;  // K elements (bytes) per ring stage
+constexpr int kFewScaleBytes = 512;  // 32 rows x 16 bytes: word c of row r is channel 32 c + r
+constexpr uint64_t kFewWaitNs = 2000000000ull;
+constexpr uint32_t kFewStall = 0x1u;  // QKV_CTE_FLAG_TEST_STALL
+
+template <int NT>
+struct FewCfg {
+  static constexpr int W_BYTES = kChannels * kFewK;
+  static constexpr int A_BYTES = NT * kFewK;
+  static constexpr int STAGE_BYTES = W_BYTES + A_BYTES;
+  // alignment slack, the tokens' block scales, barriers, the tokens' row scales
+  static constexpr int FIXED = 1024 + kFewScaleBytes + 256 + NT * 4;
+  static constexpr int BUDGET = 113 * 1024;  // two CTAs share an SM: one's tail overlaps the other's loads
+  static constexpr int FIT = (BUDGET - FIXED) / (STAGE_BYTES + kFewScaleBytes);
+  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+  static constexpr size_t SMEM = FIXED + static_cast<size_t>(STAGES) * (STAGE_BYTES + kFewScaleBytes);
+  static constexpr int SFA_COL = NT, SFB_COL = NT + 4;
+  static constexpr uint32_t TMEM_COLS = NT <= 16 ? 32 : 2 * NT;
+  static_assert(SFB_COL + 4 <= static_cast<int>(TMEM_COLS) && TMEM_COLS <= 256, "TMEM columns, of two CTAs");
+  static_assert(STAGES * STAGE_BYTES >= NT * kChannels * 4, "the partial sums reuse the ring");
+  static_assert(STAGES >= 3, "pipeline depth");
+};
+
+__device__ __forceinline__ void few_failure(uint32_t* status, volatile int* abort_flag, uint32_t code) {
+  atomicOr(status, code);
+  *abort_flag = 1;
+}
+
+// One word of block scales: K blocks 4 kb .. 4 kb + 3 of a channel (127 past K or N).
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, bool live, int kb, int k_blocks) {
+  if (!live) return 0x7F7F7F7Fu;
+  if ((k_blocks & 3) == 0) return __ldg(reinterpret_cast<const uint32_t*>(row) + kb);
+  uint32_t w = 0x7F7F7F7Fu;
+  for (int j = 0; j < 4; ++j)
+    if (4 * kb + j < k_blocks)
+      w = (w & ~(0xFFu << (8 * j))) | static_cast<uint32_t>(__ldg(row + 4 * kb + j)) << (8 * j);
+  return w;
+}
+
+// A thread's two channels.
+struct ChannelParams {
+  float col[2], bias[2], gate[2];
+
+  __device__ __forceinline__ ChannelParams(const LinearFewArgs& a, int n) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const bool in = n + k < a.N;
+      col[k] = a.w_col_scale != nullptr && in ? __ldg(a.w_col_scale + n + k) : 1.0f;
+      bias[k] = a.bias != nullptr && in ? to_f32(reinterpret_cast<const __nv_bfloat16*>(a.bias)[n + k]) : 0.0f;
+      gate[k] = a.lin.gate != nullptr && in ? to_f32(reinterpret_cast<const __nv_bfloat16*>(a.lin.gate)[n + k]) : 1.0f;
+    }
+  }
+};
+
+// Tokens t, t + step, ... (kBatch of them, those below `live`) of the tile: the sum of
+// the cluster's parts in rank order, the epilogue, two elements stored. kMaxParts: the
+// cluster's size where it is known, else its largest.
+template <int kBatch, int kMaxParts>
+__device__ __forceinline__ void finish_tokens(const LinearFewArgs& a, const ChannelParams& cp, uint32_t base,
+                                              const float* row_scale, int t0, int t, int step, int live, int n) {
+  const LinearEpilogue& e = a.lin;
+  float2 v[kBatch], res[kBatch];
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    const int tu = t + u * step;
+    res[u] = make_float2(0.0f, 0.0f);
+    if (tu < live) {
+      if (e.residual != nullptr) {
+        const long long i = static_cast<long long>(t0 + tu) * e.ldr + n;
+        if (e.pairs && n + 1 < a.N) {
+          res[u] = load_pair(e.residual, i, e.dtype);
+        } else {
+          res[u].x = load_any(e.residual, i, e.dtype);
+          if (n + 1 < a.N) res[u].y = load_any(e.residual, i + 1, e.dtype);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    const int tu = t + u * step;
+    if (tu < live) {
+      const uint32_t addr = base + 4 * kChannels * tu;
+      if constexpr (kMaxParts == 1) {
+        v[u] = ld_shared_f32x2(addr);
+      } else {
+        float2 p[kMaxParts];
+#pragma unroll
+        for (int r = 0; r < kMaxParts; ++r)
+          p[r] = kMaxParts == 2 || r < a.split ? ld_shared_cluster_f32x2(mapa_shared(addr, r)) : make_float2(0.0f, 0.0f);
+        v[u] = p[0];
+#pragma unroll
+        for (int r = 1; r < kMaxParts; ++r) {
+          v[u].x += p[r].x;
+          v[u].y += p[r].y;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    const int tu = t + u * step;
+    if (tu < live) {
+      const float s = row_scale[tu];
+      float2 o;
+      o.x = fmaf(cp.gate[0], apply_act(fmaf(v[u].x, s * cp.col[0], cp.bias[0]), e.act), res[u].x);
+      o.y = fmaf(cp.gate[1], apply_act(fmaf(v[u].y, s * cp.col[1], cp.bias[1]), e.act), res[u].y);
+      const long long i = static_cast<long long>(t0 + tu) * e.ldo + n;
+      if (e.pairs && n + 1 < a.N) {
+        store_pair(e.out, i, e.dtype, o);
+      } else {
+        store_any(e.out, i, e.dtype, o.x);
+        if (n + 1 < a.N) store_any(e.out, i + 1, e.dtype, o.y);
+      }
+    }
+  }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kFewThreads)
+    linear_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
+                      const LinearFewArgs a) {
+  using C = FewCfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sW = smem;
+  uint8_t* sA = sW + C::STAGES * C::W_BYTES;
+  uint8_t* sSF = sA + C::STAGES * C::A_BYTES;
+  uint8_t* sOne = sSF + C::STAGES * kFewScaleBytes;  // the tokens' scales
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOne + kFewScaleBytes);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((2 * C::STAGES + 1) * 8 + 8 <= 256, "barrier area");
+  float* row_scale = reinterpret_cast<float*>(sOne + kFewScaleBytes + 256);  // [NT]
+  float* part = reinterpret_cast<float*>(smem);  // [NT][128] once the ring is done
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = a.split;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int n0 = (static_cast<int>(blockIdx.x) / split) * kChannels;
+  const int t0 = static_cast<int>(blockIdx.y) * NT;
+  const int kb0 = static_cast<int>(static_cast<long long>(a.k_stages) * rank / split);
+  const int kb1 = static_cast<int>(static_cast<long long>(a.k_stages) * (rank + 1) / split);
+  const int n_kb = kb1 - kb0;  // at least one: split <= k_stages
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(smem_u32(&full[s]), 2);  // the loads, and the scale warp
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(tfull), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp >= 4) {
+    reinterpret_cast<uint32_t*>(sOne)[threadIdx.x - 128] = 0x7F7F7F7Fu;
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  // What the end needs of each thread's two channels is requested now.
+  const int live_tokens = a.T - t0 < NT ? a.T - t0 : NT;
+  const int ch = 2 * (static_cast<int>(threadIdx.x) & 63);
+  const ChannelParams cp(a, n0 + ch);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // W is read once per token tile; with several tiles the others find it in L2
+      const uint64_t pol_w = gridDim.y > 1 ? policy_evict_normal() : policy_evict_first();
+      const uint64_t pol_a = policy_evict_last();
+      int issued = 0;
+      auto load_w = [&](int i, int stage) {
+        const uint32_t fb = smem_u32(&full[stage]);
+        mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
+        tma_load_2d(smem_u32(sW + stage * C::W_BYTES), &tmW, (kb0 + i) * kFewK, n0, fb, pol_w);
+      };
+      auto load_a = [&](int i, int stage) {
+        tma_load_2d(smem_u32(sA + stage * C::A_BYTES), &tmA, (kb0 + i) * kFewK, t0, smem_u32(&full[stage]), pol_a);
+      };
+      const bool stall = (a.flags & kFewStall) != 0;  // test hook: load nothing
+      // W does not depend on the producer step (bf16 or packed rows) this kernel may
+      // have been launched beside: the first stages' W goes out before the wait for it.
+      const int first = stall ? 0 : (n_kb < C::STAGES ? n_kb : C::STAGES);
+      for (int i = 0; i < first; ++i) load_w(i, i);
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      for (int i = 0; i < first; ++i) load_a(i, i);
+      issued = first;
+      int stage = first == C::STAGES ? 0 : first;
+      uint32_t phase = first == C::STAGES ? 1 : 0;
+      for (int i = first; !stall && i < n_kb; ++i) {
+        if (!mbar_wait_bounded(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, kFewWaitNs)) {
+          few_failure(a.status, abort_flag, kErrProducerEmptyWait);
+          break;
+        }
+        load_w(i, stage);
+        load_a(i, stage);
+        ++issued;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      // Without a failure the epilogue's wait covers every copy (the MMAs have read them).
+      // After one, stay until the last copies have landed; their barriers also count the
+      // scale warp, which may have left: then the limit ends the wait.
+      if (*abort_flag) {
+        const int pending = issued < C::STAGES ? issued : C::STAGES;
+        for (int i = 0; i < pending; ++i) {
+          if (stage == 0) {
+            stage = C::STAGES - 1;
+            phase ^= 1u;
+          } else {
+            --stage;
+          }
+          if (!mbar_wait_bounded(smem_u32(&full[stage]), phase, nullptr, kFewWaitNs)) {
+            few_failure(a.status, abort_flag, kErrDrainWait);
+            break;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_mxf8_e4m3(kChannels, NT);
+      const uint32_t sfa = tmem_base + C::SFA_COL, sfb = tmem_base + C::SFB_COL;
+      tc_copy_32x128b_x4(sfb, smem_desc_plain(smem_u32(sOne)));
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int i = 0; i < n_kb; ++i) {
+        if (!mbar_wait_bounded(smem_u32(&full[stage]), phase, abort_flag, kFewWaitNs)) {
+          few_failure(a.status, abort_flag, kErrMmaFullWait);
+          break;
+        }
+        tc_fence_after();
+        tc_copy_32x128b_x4(sfa, smem_desc_plain(smem_u32(sSF + stage * kFewScaleBytes)));
+        const uint64_t wd = smem_desc_sw128(smem_u32(sW + stage * C::W_BYTES));
+        const uint64_t ad = smem_desc_sw128(smem_u32(sA + stage * C::A_BYTES));
+#pragma unroll
+        for (int k = 0; k < kFewK / 32; ++k)
+          mma_mxf8(tmem_base, wd + 2 * k, ad + 2 * k, idesc_with_sf_id(idesc, k, 0), sfa, sfb, (i | k) != 0 ? 1u : 0u);
+        tc_commit(smem_u32(&empty[stage]));
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      tc_commit(smem_u32(tfull));  // also on failure: every operation issued above has completed
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // Block scales: lane r gathers the words of channels r, 32 + r, 64 + r, 96 + r of each
+    // K block, four K blocks ahead of the one it writes.
+    constexpr int kAhead = 4;
+    uint32_t w[kAhead][4];
+    const uint8_t* row[4];
+    bool live[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int n = n0 + 32 * c + lane;
+      live[c] = n < a.N;
+      row[c] = a.w_sf + static_cast<size_t>(live[c] ? n : 0) * a.k_blocks;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) w[j][c] = scale_word(row[c], live[c] && j < n_kb, kb0 + j, a.k_blocks);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int i0 = 0; ok && i0 < n_kb; i0 += kAhead) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (ok && i0 + j < n_kb) {
+          ok = mbar_wait_bounded(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, kFewWaitNs);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            *reinterpret_cast<uint4*>(sSF + stage * kFewScaleBytes + 16 * lane) =
+                make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&full[stage]));
+            if (++stage == C::STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          const int next = i0 + j + kAhead;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) w[j][c] = scale_word(row[c], live[c] && next < n_kb, kb0 + next, a.k_blocks);
+        }
+      }
+    }
+    if (!ok && lane == 0) few_failure(a.status, abort_flag, kErrProducerEmptyWait);
+    __syncwarp();
+  } else if (warp >= 4) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the row scales of a producer step
+    for (int t = static_cast<int>(threadIdx.x) - 128; t < live_tokens; t += 128) row_scale[t] = a.a_scale[t0 + t];
+  }
+  // ---------------- partial sums to shared memory: all warps, two per lane quarter ----------------
+  bool ok = mbar_wait_bounded(smem_u32(tfull), 0, abort_flag, kFewWaitNs);
+  ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+  if (ok) {
+    tc_fence_after();
+    const int quarter = warp & 3;
+    const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    for (int c = 16 * (warp >> 2); c < live_tokens; c += 32) {
+      uint32_t r[16];
+      tmem_ld_32x32b_x16(t_lane + c, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) part[(c + j) * kChannels + quarter * 32 + lane] = __uint_as_float(r[j]);
+    }
+  } else if (lane == 0) {
+    few_failure(a.status, abort_flag, kErrEpilogueTmemFullWait);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (split > 1) cluster_sync();  // every CTA's partial sums are in place
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!*abort_flag && n0 + ch < a.N) {
+    // tokens rank + split * (group, group + 4, ...) with two channels per thread, kBatch at
+    // a time so that their loads overlap
+    const uint32_t base = smem_u32(part) + 4 * ch;
+    const int step = split * 4;
+    int t = rank + split * (static_cast<int>(threadIdx.x) >> 6);
+    if (split == 1) {
+      for (; t < live_tokens; t += 8 * step) finish_tokens<8, 1>(a, cp, base, row_scale, t0, t, step, live_tokens, n0 + ch);
+    } else if (split == 2) {
+      for (; t < live_tokens; t += 8 * step) finish_tokens<8, 2>(a, cp, base, row_scale, t0, t, step, live_tokens, n0 + ch);
+    } else {
+      for (; t < live_tokens; t += 2 * step) finish_tokens<2, 8>(a, cp, base, row_scale, t0, t, step, live_tokens, n0 + ch);
+    }
+  }
+  if (split > 1) cluster_sync();  // no CTA leaves while another reads its sums
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+template <int NT>
+cudaError_t launch_few(const CUtensorMap& tmA, const CUtensorMap& tmW, const LinearFewArgs& a, bool after_producer,
+                       cudaStream_t s) {
+  using C = FewCfg<NT>;
+  auto k = linear_few_kernel<NT>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.N + kChannels - 1) / kChannels * a.split, (a.T + NT - 1) / NT);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after_producer ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k, tmA, tmW, a);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_few(const CUtensorMap& tmA, const CUtensorMap& tmW, int token_tile, const LinearFewArgs& a,
+                              bool after_producer, cudaStream_t s) {
+  switch (token_tile) {
+    case 16: return launch_few<16>(tmA, tmW, a, after_producer, s);
+    case 32: return launch_few<32>(tmA, tmW, a, after_producer, s);
+    case 64: return launch_few<64>(tmA, tmW, a, after_producer, s);
+    case 128: return launch_few<128>(tmA, tmW, a, after_producer, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace qkvcte
