@@ -128,24 +128,29 @@ def _tensor(name: str, t, dtypes, device=None):
     return t
 
 
+# The checks below test what is right first, with as few calls into torch as will do (a
+# small kernel's call is bound by the host), and look for what is wrong afterwards.
+
 def _vector(name: str, t, dtypes, device, n: int) -> Optional[int]:
     """Address of a contiguous tensor of n elements, or None."""
     if t is None:
         return None
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == device and t.numel() == n
+            and t.is_contiguous()):
+        return t.data_ptr()
     _tensor(name, t, dtypes, device)
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous with {n} elements, got shape {tuple(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: must be contiguous with {n} elements, got shape {tuple(t.shape)}")
 
 
 def _rows(name: str, t, dtypes, device=None, shape=None):
     """(address, row stride) of [..., cols] as rows; the elements of a row are contiguous."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and (t.is_cuda if device is None else t.device == device):
+        strides = t.stride()
+        if len(strides) == 2 and strides[1] == 1 and (shape is None or t.shape == shape):
+            return t.data_ptr(), strides[0]
     _tensor(name, t, dtypes, device)
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} is not {tuple(shape)}")
-    strides = t.stride()
-    if len(strides) == 2 and strides[1] == 1:
-        return t.data_ptr(), strides[0]
     if not strides:
         raise ValueError(f"{name}: needs at least one dimension")
     if t.shape[-1] > 1 and strides[-1] != 1:
@@ -166,31 +171,34 @@ def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None,
     the fp32 statistics [...] are written when given or asked for with `stats`, else None.
     `out` may be x."""
     px, ldx = _rows("x", x, _DTYPE)
-    dev, cols = x.device, x.shape[-1]
+    dev, shape, dt = x.device, x.shape, x.dtype
+    cols = shape[-1]
     rows = x.numel() // cols if cols else 0
     param = weight if weight is not None else bias
-    pdt = param.dtype if isinstance(param, torch.Tensor) else x.dtype
-    if pdt not in (x.dtype, torch.float32):
-        raise TypeError(f"weight and bias: dtype {pdt} is neither {x.dtype} nor torch.float32")
+    pdt = param.dtype if isinstance(param, torch.Tensor) else dt
+    if pdt is not dt and pdt is not torch.float32:
+        raise TypeError(f"weight and bias: dtype {pdt} is neither {dt} nor torch.float32")
     pw = _vector("weight", weight, (pdt,), dev, cols)
     pb = _vector("bias", bias, (pdt,), dev, cols)
     made = []
     if out is None:
-        out = x.new_empty(x.shape)
+        out = torch.empty(shape, dtype=dt, device=dev)
         made.append(out)
+        py, ldy = out.data_ptr(), cols
+    else:
+        py, ldy = _rows("out", out, (dt,), dev, shape)
     if stats:
         if mean is None:
-            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+            mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
             made.append(mean)
         if rstd is None:
-            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+            rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
             made.append(rstd)
-    py, ldy = _rows("out", out, (x.dtype,), dev, x.shape)
     pm = _vector("mean", mean, (torch.float32,), dev, rows)
     pr = _vector("rstd", rstd, (torch.float32,), dev, rows)
     if stream is not None:
         _kept(stream, dev, *made)
-    _launch(_lib().qkv_cte_layer_norm, dev, stream, px, ldx, pw, pb, py, ldy, pm, pr, rows, cols, eps, _DTYPE[x.dtype],
+    _launch(_lib().qkv_cte_layer_norm, dev, stream, px, ldx, pw, pb, py, ldy, pm, pr, rows, cols, eps, _DTYPE[dt],
             _DTYPE[pdt])
     return out, mean, rstd
 
@@ -216,14 +224,18 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
         raise TypeError(f"weight, dweight and dbias: dtype {pdt} is neither {x.dtype} nor torch.float32")
     made = []
     if dx is None and dweight is None and dbias is None:
-        dx = x.new_empty(x.shape)
-        dweight = torch.empty(cols, dtype=pdt, device=dev)
-        dbias = torch.empty(cols, dtype=pdt, device=dev)
-        made += [dx, dweight, dbias]
-    pd, ldd = _rows("dx", dx, (x.dtype,), dev, x.shape) if dx is not None else (None, 0)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        sums = torch.empty(2, cols, dtype=pdt, device=dev)
+        dweight, dbias = sums[0], sums[1]
+        made += [dx, sums]
+        pd, ldd = dx.data_ptr(), cols
+        pdw = sums.data_ptr()
+        pdb = pdw + cols * sums.element_size()
+    else:
+        pd, ldd = _rows("dx", dx, (x.dtype,), dev, x.shape) if dx is not None else (None, 0)
+        pdw = _vector("dweight", dweight, (pdt,), dev, cols)
+        pdb = _vector("dbias", dbias, (pdt,), dev, cols)
     pw = _vector("weight", weight, (pdt,), dev, cols)
-    pdw = _vector("dweight", dweight, (pdt,), dev, cols)
-    pdb = _vector("dbias", dbias, (pdt,), dev, cols)
     pm = _vector("mean", mean, (torch.float32,), dev, rows)
     pr = _vector("rstd", rstd, (torch.float32,), dev, rows)
     ws_bytes, pws = 0, None
@@ -298,28 +310,28 @@ class QkvCteRopeAxes:
         """x [B, S, heads, d_head] or [S, heads, d_head] rotated (turned back with
         `inverse`: the rotation's gradient); any strides with contiguous lanes. `out` may be x."""
         _tensor("x", x, _DTYPE)
-        if x.dim() not in (3, 4) or x.shape[-1] != self.d_head:
+        dev, shape, dt, sx = x.device, x.shape, x.dtype, x.stride()
+        if len(shape) not in (3, 4) or shape[-1] != self.d_head:
             raise ValueError(f"x: expected [B, S, heads, {self.d_head}] or [S, heads, {self.d_head}], "
-                             f"got {tuple(x.shape)}")
-        dev = x.device
-        made = out is None
-        if made:
-            out = x.new_empty(x.shape)
-        _tensor("out", out, (x.dtype,), dev)
-        if out.shape != x.shape:
-            raise ValueError(f"out: shape {tuple(out.shape)} is not {tuple(x.shape)}")
-        for name, t in (("x", x), ("out", out)):
-            if t.stride(-1) != 1:
-                raise ValueError(f"{name}: the last dimension must be contiguous")
-        batch = x.shape[0] if x.dim() == 4 else 1
-        seq, heads = x.shape[-3], x.shape[-2]
+                             f"got {tuple(shape)}")
+        if sx[-1] != 1:
+            raise ValueError("x: the last dimension must be contiguous")
+        if out is None:
+            out = torch.empty(shape, dtype=dt, device=dev)
+            if stream is not None:
+                _kept(stream, dev, out)
+        else:
+            _tensor("out", out, (dt,), dev)
+            if out.shape != shape:
+                raise ValueError(f"out: shape {tuple(out.shape)} is not {tuple(shape)}")
+        sy = out.stride()
+        if sy[-1] != 1:
+            raise ValueError("out: the last dimension must be contiguous")
+        batch, bx, by = (shape[0], sx[0], sy[0]) if len(shape) == 4 else (1, 0, 0)
+        seq, heads = shape[-3], shape[-2]
         p, stride, g = self._where(batch, seq, positions, grids, dev)
-        sx, sy = x.stride(), out.stride()
-        bx, by = (sx[0], sy[0]) if x.dim() == 4 else (0, 0)
-        if made and stream is not None:
-            _kept(stream, dev, out)
         _launch(_lib().qkv_cte_rope_apply, dev, stream, self.plan, x.data_ptr(), bx, sx[-3], sx[-2], out.data_ptr(),
-                by, sy[-3], sy[-2], batch, seq, heads, p, stride, g, _DTYPE[x.dtype], 1 if inverse else 0)
+                by, sy[-3], sy[-2], batch, seq, heads, p, stride, g, _DTYPE[dt], 1 if inverse else 0)
         return out
 
     def close(self):

@@ -557,31 +557,72 @@ bool vec_ok(const void* p, long long ld, int cols, size_t elem, long long rows) 
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && cols % n == 0 && (rows <= 1 || ld % n == 0);
 }
 
-// What exceeds the 48 KB that every kernel may use is asked for.
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t smem) {
-  if (smem <= 40 * 1024) return cudaSuccess;  // with the static part, within the 48 KB
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-}
+// Blocks (or clusters) of a kernel that the current device holds at once. Asking costs
+// more than the launch, so each thread keeps the last answer per kernel; the first use of
+// a shape also raises the kernel's shared memory limit where it exceeds the 48 KB (static
+// part included) that every kernel may use.
+struct Residency {
+  int device = -1, threads = 0, cluster = 0;
+  size_t smem = 0;
+  int count = 0;
+};
 
 template <typename K>
-int resident_grid(K kernel, dim3 block, size_t smem, int num_sms, long long work) {
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, static_cast<int>(block.x * block.y), smem) !=
-          cudaSuccess ||
-      per_sm < 1)
-    per_sm = 1;
-  return static_cast<int>(std::min<long long>(static_cast<long long>(per_sm) * num_sms, work));
+cudaError_t residency(K kernel, Residency& last, dim3 block, size_t smem, int cluster, int num_sms, int* count) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const int threads = static_cast<int>(block.x * block.y);
+  if (device != last.device || threads != last.threads || smem != last.smem || cluster != last.cluster) {
+    if (smem > 40 * 1024) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+    }
+    int n = 0;
+    if (cluster > 1) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(cluster);
+      cfg.blockDim = block;
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = cluster;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      // a cluster stays within a GPC: fewer blocks fit than of single ones
+      e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    } else {
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+      n *= num_sms;
+    }
+    if (e != cudaSuccess) return e;
+    last.device = device;
+    last.threads = threads;
+    last.smem = smem;
+    last.cluster = cluster;
+    last.count = n > 0 ? n : 1;
+  }
+  *count = last.count;
+  return cudaSuccess;
 }
+
+// (one call site per kernel, so that each has its own record)
+#define QKVCTE_RESIDENT(kernel, block, smem, cluster, num_sms, count)          \
+  ([&] {                                                                       \
+    static thread_local Residency last;                                        \
+    return residency(kernel, last, block, smem, cluster, num_sms, count);      \
+  }())
 
 template <typename Fm>
 cudaError_t forward_launch(const LayerNormArgs& a, dim3 block, cudaStream_t s, int num_sms) {
   auto k = layer_norm_kernel<Fm>;
   const long long groups = (a.rows + block.y - 1) / block.y;
   const size_t smem = static_cast<size_t>(Fm::Stream::kBytes) * block.x * block.y;
-  const cudaError_t e = allow_smem(k, smem);
+  int resident = 0;
+  const cudaError_t e = QKVCTE_RESIDENT(k, block, smem, 1, num_sms, &resident);
   if (e != cudaSuccess) return e;
-  k<<<resident_grid(k, block, smem, num_sms, groups), block, smem, s>>>(a);
+  k<<<static_cast<int>(std::min<long long>(groups, resident)), block, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -610,7 +651,7 @@ cudaError_t forward_vec(const LayerNormArgs& a, cudaStream_t s, int num_sms) {
     if (pick_block(chunks, 16, 512, &block)) return forward_go<T, P, VEC, 16, false>(a, block, s, num_sms);
   }
   auto k = layer_norm_long_kernel<T, P>;
-  k<<<resident_grid(k, dim3(1024), 0, num_sms, a.rows), 1024, 0, s>>>(a);
+  k<<<static_cast<int>(std::min<long long>(a.rows, 2 * num_sms)), 1024, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -644,12 +685,15 @@ cudaError_t backward_launch(const LayerNormGradArgs& a, dim3 block, cudaStream_t
   size_t smem = 2 * static_cast<size_t>(Fm::Stream::kBytes) * block.x * block.y;
   const bool sums = a.partial != nullptr;
   if (sums) smem = std::max(smem, 2 * sizeof(float) * static_cast<size_t>(a.cols));
-  cudaError_t e = allow_smem(k, smem);
-  if (e != cudaSuccess) return e;
-  const long long groups = (a.rows + block.y - 1) / block.y;
   const int cluster = sums ? kGradCluster : 1;
+  int resident = 0;
+  cudaError_t e = QKVCTE_RESIDENT(k, block, smem, cluster, num_sms, &resident);
+  if (e != cudaSuccess) return e;
+  if (sums) resident = std::min(resident, a.max_parts);
+  const long long groups = (a.rows + block.y - 1) / block.y;
+  const int grid = static_cast<int>(std::min<long long>((groups + cluster - 1) / cluster, resident)) * cluster;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cluster);
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -659,13 +703,6 @@ cudaError_t backward_launch(const LayerNormGradArgs& a, dim3 block, cudaStream_t
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // one wave: a cluster stays within a GPC, so fewer blocks of clusters than of single
-  // blocks are resident at once
-  int resident = 0;
-  if (cudaOccupancyMaxActiveClusters(&resident, k, &cfg) != cudaSuccess || resident < 1) resident = num_sms / cluster;
-  if (sums) resident = std::min(resident, a.max_parts);
-  const int grid = static_cast<int>(std::min<long long>((groups + cluster - 1) / cluster, resident)) * cluster;
-  cfg.gridDim = dim3(grid);
   e = cudaLaunchKernelEx(&cfg, k, a);
   return e != cudaSuccess || !sums ? e : join<typename Fm::P>(a, grid / cluster, s);
 }
@@ -693,7 +730,7 @@ cudaError_t backward_vec(const LayerNormGradArgs& a, cudaStream_t s, int num_sms
   cudaError_t e = cudaSuccess;
   if (a.dx != nullptr) {
     auto k = layer_norm_backward_long_kernel<T, P>;
-    k<<<resident_grid(k, dim3(1024), 0, num_sms, a.rows), 1024, 0, s>>>(a);
+    k<<<static_cast<int>(std::min<long long>(a.rows, 2 * num_sms)), 1024, 0, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (a.partial == nullptr) return e;
