@@ -20,7 +20,18 @@ __device__ __forceinline__ float apply_act(float z, int act) {
       const float u2 = -1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.0f);
       return __fdividef(z, 1.0f + __expf(u2));
     }
-    case QKV_CTE_ACT_GELU_ERF: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    case QKV_CTE_ACT_GELU_ERF: {
+      // 0.5 z (1 + erf(z / sqrt 2)) = max(z, 0) - 0.5 |z| erfc(|z| / sqrt 2), with formula
+      // 7.1.26 of Abramowitz and Stegun for erfc(x): t (a1 + t (a2 + ...)) exp(-x^2),
+      // t = 1 / (1 + p x), off by 1.5e-7 at most (the library's erfcf took 1.6 times the
+      // MMAs' time at K = 5120). Beyond |z| = 100 the correction is 0 in fp32.
+      const float az = fminf(fabsf(z), 100.0f);
+      const float x = 0.70710678118654752f * az;
+      const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+      const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                                  0.254829592f);
+      return (z < 0.0f ? 0.0f : z) - 0.5f * az * poly * __expf(-x * x);
+    }
     case QKV_CTE_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
     default: return z;
   }

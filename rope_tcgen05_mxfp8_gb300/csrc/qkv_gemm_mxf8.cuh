@@ -474,11 +474,14 @@ __device__ __forceinline__ void epilogue_drain_plain(const GemmShape& g, const G
 // took 1.6 times the MMAs' time at K = 5120), and each thread holds the residual words
 // of its row's next kLinearAhead columns in registers. Rows off 32-byte boundaries and
 // the ragged last 16 columns go element by element.
+// Two warps share each lane quarter, the first taking the tile's first kHalf columns:
+// with one, activation and residual took longer than the MMAs up to K of about 5000.
 constexpr int kLinearAhead = 64;  // columns
 
 template <int BN>
 struct LinearTile {
-  static constexpr int kParamBytes = 4 * 3 * BN * 4;  // 4 warps x (scale, bias, gate) x BN fp32
+  static constexpr int kHalf = (BN / 2 + 15) / 16 * 16;
+  static constexpr int kParamBytes = 8 * 3 * kHalf * 4;  // 8 warps x (scale, bias, gate) x kHalf fp32
 
   uint32_t res[kLinearAhead / 16][16];
 
@@ -486,24 +489,25 @@ struct LinearTile {
     return e.residual != nullptr && e.wide && row < g.T;
   }
 
-  // Before the wait for the accumulator. `params`: this warp's 3 * BN floats.
+  // Before the wait for the accumulator, for the `width` columns from col_base on.
+  // `params`: this warp's 3 * kHalf floats.
   __device__ __forceinline__ void begin(const GemmShape& g, const GemmArgs& a, float* params, int block128,
-                                        int row_in_block, int col_base) {
+                                        int row_in_block, int col_base, int width) {
     const long long row = static_cast<long long>(block128) * 128 + row_in_block;
     if (fetches(g, a.lin, row)) {
 #pragma unroll
       for (int i = 0; i < kLinearAhead / 16; ++i)
-        if (col_base + 16 * (i + 1) <= g.I) load_residual16(a.lin, row, col_base + 16 * i, res[i]);
+        if (16 * i < width && col_base + 16 * (i + 1) <= g.I) load_residual16(a.lin, row, col_base + 16 * i, res[i]);
     }
     __syncwarp();  // every lane has read the previous tile's
 #pragma unroll
-    for (int i = 0; i < (BN + 31) / 32; ++i) {
+    for (int i = 0; i < (kHalf + 31) / 32; ++i) {
       const int j = 32 * i + (threadIdx.x & 31);
       const int c = col_base + j;
-      if (j < BN && c < g.I) {
+      if (j < width && c < g.I) {
         if (a.w_col_scale != nullptr) params[j] = __ldg(a.w_col_scale + c);
-        if (a.bias != nullptr) params[BN + j] = bf16_bits_to_float(__ldg(a.bias + c));
-        if (a.lin.gate != nullptr) params[2 * BN + j] = bf16_bits_to_float(__ldg(a.lin.gate + c));
+        if (a.bias != nullptr) params[kHalf + j] = bf16_bits_to_float(__ldg(a.bias + c));
+        if (a.lin.gate != nullptr) params[2 * kHalf + j] = bf16_bits_to_float(__ldg(a.lin.gate + c));
       }
     }
     __syncwarp();
@@ -511,27 +515,27 @@ struct LinearTile {
 
   // 64 columns per turn, so that the window of residual words is indexed statically.
   __device__ __forceinline__ void drain(const GemmShape& g, const GemmArgs& a, uint32_t t_acc, const float* params,
-                                        int block128, int row_in_block, int col_base, uint64_t pol_out) {
+                                        int block128, int row_in_block, int col_base, int width, uint64_t pol_out) {
     const LinearEpilogue& e = a.lin;
     const long long row = static_cast<long long>(block128) * 128 + row_in_block;
     const bool row_ok = row < g.T;
     const float ascale = row_ok ? a.a_scale[row] : 0.0f;
     const bool fetch = fetches(g, e, row);
 #pragma unroll 1
-    for (int c0 = 0; c0 < BN; c0 += kLinearAhead) {
+    for (int c0 = 0; c0 < width; c0 += kLinearAhead) {
 #pragma unroll
       for (int i = 0; i < kLinearAhead / 16; ++i) {
         const int cc = c0 + 16 * i;
         const int col0 = col_base + cc;
-        if (cc >= BN || col0 >= g.I) break;  // uniform across the warp
+        if (cc >= width || col0 >= g.I) break;  // uniform across the warp
         uint32_t r[16];
         tmem_ld_32x32b_x16(t_acc + static_cast<uint32_t>(cc), r);
         tmem_ld_wait();
         if (row_ok) {
           if (e.wide && col0 + 16 <= g.I) {
             finish16(e, row, col0, r, ascale, a.w_col_scale != nullptr ? params + cc : nullptr,
-                     a.bias != nullptr ? params + BN + cc : nullptr, e.gate != nullptr ? params + 2 * BN + cc : nullptr,
-                     res[i], pol_out);
+                     a.bias != nullptr ? params + kHalf + cc : nullptr,
+                     e.gate != nullptr ? params + 2 * kHalf + cc : nullptr, res[i], pol_out);
           } else {
             for (int j = 0; j < 16; ++j) {
               const int c = col0 + j;
@@ -540,12 +544,12 @@ struct LinearTile {
               for (int k = 0; k < 16; ++k) acc = j == k ? __uint_as_float(r[k]) : acc;
               if (c < g.I)
                 finish_one(e, row, c, acc, a.w_col_scale != nullptr ? ascale * params[cc + j] : ascale,
-                           a.bias != nullptr ? params[BN + cc + j] : 0.0f,
-                           e.gate != nullptr ? params[2 * BN + cc + j] : 1.0f);
+                           a.bias != nullptr ? params[kHalf + cc + j] : 0.0f,
+                           e.gate != nullptr ? params[2 * kHalf + cc + j] : 1.0f);
             }
           }
         }
-        if (fetch && cc + kLinearAhead < BN && col0 + kLinearAhead + 16 <= g.I)
+        if (fetch && cc + kLinearAhead < width && col0 + kLinearAhead + 16 <= g.I)
           load_residual16(e, row, col0 + kLinearAhead, res[i]);
       }
     }
@@ -562,6 +566,12 @@ struct LinearTile {
 //               centred) the norm/RoPE pass finishes from
 //   kEpiLinear: bias, activation, gate and residual to a strided output (qkv_cte_linear_run)
 constexpr int kEpiPlain = 0, kEpiHead = 1, kEpiStatsRms = 2, kEpiStatsLayer = 3, kEpiLinear = 4;
+
+// Epilogue warps of the CTA-pair form, and its threads.
+template <int kEpi>
+constexpr int kEpilogueWarps = kEpi == kEpiLinear ? 8 : 4;
+template <int kEpi>
+constexpr int kPairThreads = 64 + 32 * kEpilogueWarps<kEpi>;
 
 template <int BN, int kEpi>
 __device__ __forceinline__ void epilogue_drain(const GemmShape& g, const GemmArgs& a, uint32_t t_acc, int block128,
@@ -1021,7 +1031,7 @@ __device__ __forceinline__ void fused_finish(const NormRopeArgs& nr, long long n
 }
 
 template <int BN, int kEpi, bool kFused>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kPairThreads<kEpi>, 1)
     qkv_gemm_mxf8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                               const __grid_constant__ CUtensorMap tmSF, const GemmShape g, const GemmArgs a,
                               const __grid_constant__ NormRopeArgs nr) {
@@ -1035,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(sSFA + 512);  // used in the leader
   uint64_t* empty = full + C::STAGES;                         // both
   uint64_t* tfull = empty + C::STAGES;                        // both
-  uint64_t* tempty = tfull + 2;                               // leader: 4 warps x 2 CTAs
+  uint64_t* tempty = tfull + 2;                               // leader: the epilogue warps of both CTAs
   uint64_t* drain = tempty + 2;                               // leader
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -1058,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&tfull[s]), 1);
-      mbar_init(smem_u32(&tempty[s]), 8);
+      mbar_init(smem_u32(&tempty[s]), 2 * kEpilogueWarps<kEpi>);
     }
     mbar_init(smem_u32(drain), 1);
     for (int r = 0; r < kTileRing; ++r) mbar_init(smem_u32(&ring.full[r]), 1);
@@ -1072,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish_pair();
   }
-  if (warp >= 2) {
+  if (warp >= 2 && warp < 6) {
     reinterpret_cast<uint32_t*>(sSFA)[threadIdx.x - 64] = 0x7F7F7F7Fu;  // A-side scales: 2^0
     fence_proxy_async_smem();
   }
@@ -1251,7 +1261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ---------------- epilogue (warps 2..5, both CTAs) ----------------
+    // ---------------- epilogue (warps from 2 on, both CTAs) ----------------
     const uint64_t pol_out = policy_evict_first();
     const int quarter = warp & 3;
     const int row_in_block = quarter * 32 + lane;
@@ -1260,7 +1270,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_phase = 0;
     FusedWork fw;
     [[maybe_unused]] LinearTile<BN> lin;
-    [[maybe_unused]] float* lin_params = reinterpret_cast<float*>(sSFA + 768) + quarter * 3 * BN;
+    constexpr int kHalf = LinearTile<BN>::kHalf;
+    [[maybe_unused]] const int lin_col = warp < 6 ? 0 : kHalf;  // this warp's first column of a tile
+    [[maybe_unused]] const int lin_width = warp < 6 ? kHalf : BN - kHalf;
+    [[maybe_unused]] float* lin_params = reinterpret_cast<float*>(sSFA + 768) + (warp - 2) * 3 * kHalf;
     const long long n_tasks = kFused ? nrp::task_count(nr, kFusedHeadGroup) : 0;
     const uint64_t once = kFused ? nrp::evict_first_policy() : 0;
     for (int seq = 0;; ++seq) {
@@ -1283,7 +1296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A 128-row half wholly past T (T mod 256 in (0, 128]) has nothing to store.
       const bool live = block128 * kBM < g.T;
       if constexpr (kEpi == kEpiLinear) {
-        if (live) lin.begin(g, a, lin_params, block128, row_in_block, n_blk * BN);
+        if (live) lin.begin(g, a, lin_params, block128, row_in_block, n_blk * BN + lin_col, lin_width);
       }
       bool ok;
       if constexpr (kFused)
@@ -1299,8 +1312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float ss_q = 0.0f, ss_k = 0.0f;
       if (live) {
         if constexpr (kEpi == kEpiLinear)
-          lin.drain(g, a, t_lane + static_cast<uint32_t>(acc * BN), lin_params, block128, row_in_block, n_blk * BN,
-                    pol_out);
+          lin.drain(g, a, t_lane + static_cast<uint32_t>(acc * BN + lin_col), lin_params, block128, row_in_block,
+                    n_blk * BN + lin_col, lin_width, pol_out);
         else
           epilogue_drain<BN, kEpi>(g, a, t_lane + static_cast<uint32_t>(acc * BN), block128, row_in_block, n_blk * BN,
                              pol_out, ss_q, ss_k);
@@ -1373,7 +1386,7 @@ cudaError_t launch_gemm_pair_t(const GemmShape& g, const CUtensorMap& tmA, const
   const int grid = 2 * (tiles < pairs ? tiles : pairs);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kPairThreads<kEpi>);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
