@@ -37,14 +37,14 @@ namespace {
 // Token tile and K split of the channel-major form, and whether it is the form for a
 // problem (its rows' alignment aside). Measured on GB300, us a call, K1 against it:
 //   T, K, N            K1     token tile / split
-//   1, 5120, 5120      51     12.4 (16/4)
-//   16, 5120, 20480    107    27.4 (16/1)
-//   128, 1024, 5120    22.7   12.5 (64/2)
-//   256, 5120, 5120    31.0   24.7 (128/2)
-//   128, 5120, 20480   54     36.7 (128/1)
-//   512, 1024, 5120    24.2   20.6 (128/1)
-//   512, 5120, 5120    32.9   34.9 (128/1)
-//   256, 5120, 20480   54     65.7 (128/1, 320 tiles)
+//   1, 5120, 5120      40     12.4 (16/4)
+//   16, 5120, 20480    137    23.5 (16/1)
+//   128, 1024, 5120    19.4   12.4 (64/2)
+//   256, 5120, 5120    28.8   20.7 (128/2)
+//   128, 5120, 20480   50     33.0 (128/1)
+//   512, 1024, 5120    20.3   16.5 (128/1)
+//   512, 5120, 5120    28.8   29.0 (128/1)
+//   256, 5120, 20480   51     57.6 (128/1, 320 tiles)
 // It wins while its tiles fit the SMs about once (two CTAs share an SM, at the expense of
 // each other's loads); smaller token tiles add CTAs while there are few.
 bool choose_few(const GemmShape& g, int* token_tile, int* split) {
@@ -218,8 +218,19 @@ int qkv_cte_linear_run(qkv_cte_linear_plan_t plan, const void* A, const float* a
                               reinterpret_cast<float*>(ws + plan->ws.act_scale_off), nullptr, s, dev.sms);
   if (err != cudaSuccess) return fail(QKV_CTE_ERR_CUDA, "%s: producer launch: %s", who, cudaGetErrorString(err));
   if (few) {
-    const LinearFewArgs fa{scales,     w_col_scale, bias,    w_sf,                            g.T, g.I, g.H / 32, g.k_stages,
-                           plan->split, d.flags,     reinterpret_cast<uint32_t*>(ws), lin};
+    LinearFewArgs fa{};
+    fa.a_scale = scales;
+    fa.w_col_scale = w_col_scale;
+    fa.bias = bias;
+    fa.w_sf = w_sf;
+    fa.T = g.T;
+    fa.N = g.I;
+    fa.k_blocks = g.H / 32;
+    fa.k_stages = g.k_stages;
+    fa.split = plan->split;
+    fa.flags = d.flags;
+    fa.status = reinterpret_cast<uint32_t*>(ws);
+    fa.lin = lin;
     err = launch_linear_few(tmA, tmW, plan->token_tile, fa, produced, s);
     if (err != cudaSuccess) return fail(QKV_CTE_ERR_CUDA, "%s: GEMM launch: %s", who, cudaGetErrorString(err));
     return ok();

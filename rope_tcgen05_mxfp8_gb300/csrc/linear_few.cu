@@ -14,6 +14,12 @@
 // consecutive elements, whatever the alignment of O's rows, which is why rows off 32-byte
 // boundaries take this form at any token count.
 //
+// What bounds it: about 8 us of launch, set-up, joining and storing, then 0.33 us per
+// 128-byte K block and CTA whatever the token tile up to 64: the MMAs are too small to
+// hide their issue (80 cycles each; 300 more per ring stage for its barriers). The loads
+// are not the limit: one token, K = 5120, N = 20480 takes 23.5 us where reading W takes
+// 16.0 at the measured copy rate; N = 5120 with K split four ways 12.4 us (floor 4.0).
+//
 // The tokens carry no block scales (their scale is the fp32 row scale): their side's
 // scale factors are the constant 2^0. Every wait is bounded as in K1.
 #include <algorithm>
@@ -26,9 +32,10 @@ namespace qkvcte {
 
 namespace {
 
-constexpr int kFewThreads = 256;  // load, MMA and scale warps, one idle; four epilogue warps
+constexpr int kFewThreads = 256;  // a load, an MMA and two scale warps; all eight finish
 constexpr int kChannels = 128;
 constexpr int kFewK = 128;  // K elements (bytes) per ring stage
+constexpr int kScaleChunk = 8;  // K blocks whose scales are fetched together (32 bytes of each row of w_sf)
 constexpr int kFewScaleBytes = 512;  // 32 rows x 16 bytes: word c of row r is channel 32 c + r
 constexpr uint64_t kFewWaitNs = 2000000000ull;
 constexpr uint32_t kFewStall = 0x1u;  // QKV_CTE_FLAG_TEST_STALL
@@ -38,14 +45,17 @@ struct FewCfg {
   static constexpr int W_BYTES = kChannels * kFewK;
   static constexpr int A_BYTES = NT * kFewK;
   static constexpr int STAGE_BYTES = W_BYTES + A_BYTES;
-  // alignment slack, the tokens' block scales, barriers, the tokens' row scales
-  static constexpr int FIXED = 1024 + kFewScaleBytes + 256 + NT * 4;
-  static constexpr int BUDGET = 113 * 1024;  // two CTAs share an SM: one's tail overlaps the other's loads
-  static constexpr int FIT = (BUDGET - FIXED) / (STAGE_BYTES + kFewScaleBytes);
+  static constexpr int SF_BYTES = 2 * kScaleChunk * kFewScaleBytes;  // two chunks
+  // alignment slack, W's and the tokens' block scales, barriers, the tokens' row scales
+  static constexpr int FIXED = 1024 + SF_BYTES + kFewScaleBytes + 256 + NT * 4;
+  // Half an SM's shared memory, so that two CTAs share it: one's tail overlaps the other's
+  // loop. (A ring twice as deep for CTAs alone on their SM was no faster: the loop is not
+  // bound by its loads.)
+  static constexpr int FIT = (113 * 1024 - FIXED) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
-  static constexpr size_t SMEM = FIXED + static_cast<size_t>(STAGES) * (STAGE_BYTES + kFewScaleBytes);
-  static constexpr int SFA_COL = NT, SFB_COL = NT + 4;
-  static constexpr uint32_t TMEM_COLS = NT <= 16 ? 32 : 2 * NT;
+  static constexpr size_t SMEM = FIXED + static_cast<size_t>(STAGES) * STAGE_BYTES;
+  static constexpr int SFA_COL = NT, SFB_COL = NT + 2 * kScaleChunk * 4;  // after two chunks of W's scales
+  static constexpr uint32_t TMEM_COLS = NT <= 32 ? 128 : 256;
   static_assert(SFB_COL + 4 <= static_cast<int>(TMEM_COLS) && TMEM_COLS <= 256, "TMEM columns, of two CTAs");
   static_assert(STAGES * STAGE_BYTES >= NT * kChannels * 4, "the partial sums reuse the ring");
   static_assert(STAGES >= 3, "pipeline depth");
@@ -82,6 +92,12 @@ struct ChannelParams {
   }
 };
 
+template <int kBatch, int kAct>
+__device__ __forceinline__ void activate(float2 (&v)[kBatch]) {
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) v[u] = make_float2(apply_act(v[u].x, kAct), apply_act(v[u].y, kAct));
+}
+
 // Tokens t, t + step, ... (kBatch of them, those below `live`) of the tile: the sum of
 // the cluster's parts in rank order, the epilogue, two elements stored. kMaxParts: the
 // cluster's size where it is known, else its largest.
@@ -93,7 +109,7 @@ __device__ __forceinline__ void finish_tokens(const LinearFewArgs& a, const Chan
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
     const int tu = t + u * step;
-    res[u] = make_float2(0.0f, 0.0f);
+    res[u] = v[u] = make_float2(0.0f, 0.0f);
     if (tu < live) {
       if (e.residual != nullptr) {
         const long long i = static_cast<long long>(t0 + tu) * e.ldr + n;
@@ -130,39 +146,66 @@ __device__ __forceinline__ void finish_tokens(const LinearFewArgs& a, const Chan
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
     const int tu = t + u * step;
-    if (tu < live) {
-      const float s = row_scale[tu];
-      float2 o;
-      o.x = fmaf(cp.gate[0], apply_act(fmaf(v[u].x, s * cp.col[0], cp.bias[0]), e.act), res[u].x);
-      o.y = fmaf(cp.gate[1], apply_act(fmaf(v[u].y, s * cp.col[1], cp.bias[1]), e.act), res[u].y);
-      const long long i = static_cast<long long>(t0 + tu) * e.ldo + n;
-      if (e.pairs && n + 1 < a.N) {
-        store_pair(e.out, i, e.dtype, o);
-      } else {
-        store_any(e.out, i, e.dtype, o.x);
-        if (n + 1 < a.N) store_any(e.out, i + 1, e.dtype, o.y);
+    const float s = row_scale[tu < live ? tu : 0];
+    v[u].x = fmaf(v[u].x, s * cp.col[0], cp.bias[0]);
+    v[u].y = fmaf(v[u].y, s * cp.col[1], cp.bias[1]);
+  }
+  switch (e.act) {  // one uniform branch for the batch
+    case QKV_CTE_ACT_GELU_TANH: activate<kBatch, QKV_CTE_ACT_GELU_TANH>(v); break;
+    case QKV_CTE_ACT_GELU_ERF: activate<kBatch, QKV_CTE_ACT_GELU_ERF>(v); break;
+    case QKV_CTE_ACT_SILU: activate<kBatch, QKV_CTE_ACT_SILU>(v); break;
+    default: break;
+  }
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    v[u].x = fmaf(cp.gate[0], v[u].x, res[u].x);
+    v[u].y = fmaf(cp.gate[1], v[u].y, res[u].y);
+  }
+  const bool pair = e.pairs && n + 1 < a.N;
+  const long long i0 = static_cast<long long>(t0 + t) * e.ldo + n;
+  const long long pitch = step * e.ldo;
+  if (pair && e.dtype == QKV_CTE_DTYPE_BF16) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (t + u * step < live) store_pair(e.out, i0 + u * pitch, QKV_CTE_DTYPE_BF16, v[u]);
+  } else if (pair) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (t + u * step < live) store_pair(e.out, i0 + u * pitch, e.dtype, v[u]);
+  } else {
+    for (int u = 0; u < kBatch; ++u) {
+      float2 o = v[0];
+#pragma unroll
+      for (int k = 1; k < kBatch; ++k)
+        if (u == k) o = v[k];
+      if (t + u * step < live) {
+        store_any(e.out, i0 + u * pitch, e.dtype, o.x);
+        if (n + 1 < a.N) store_any(e.out, i0 + u * pitch + 1, e.dtype, o.y);
       }
     }
   }
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kFewThreads)
+__global__ void __launch_bounds__(kFewThreads, 2)
     linear_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                       const LinearFewArgs a) {
   using C = FewCfg<NT>;
   extern __shared__ uint8_t smem_raw[];
+  constexpr int stages = C::STAGES;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sW = smem;
-  uint8_t* sA = sW + C::STAGES * C::W_BYTES;
-  uint8_t* sSF = sA + C::STAGES * C::A_BYTES;
-  uint8_t* sOne = sSF + C::STAGES * kFewScaleBytes;  // the tokens' scales
+  uint8_t* sA = sW + stages * C::W_BYTES;
+  uint8_t* sSF = sA + stages * C::A_BYTES;
+  uint8_t* sOne = sSF + C::SF_BYTES;  // the tokens' scales
   uint64_t* full = reinterpret_cast<uint64_t*>(sOne + kFewScaleBytes);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* tfull = empty + C::STAGES;
+  uint64_t* empty = full + stages;
+  uint64_t* sf_full = empty + stages;  // [2]
+  uint64_t* sf_empty = sf_full + 2;     // [2]
+  uint64_t* tfull = sf_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * C::STAGES + 1) * 8 + 8 <= 256, "barrier area");
+  static_assert((2 * C::STAGES + 5) * 8 + 8 <= 256, "barrier area");
   float* row_scale = reinterpret_cast<float*>(sOne + kFewScaleBytes + 256);  // [NT]
   float* part = reinterpret_cast<float*>(smem);  // [NT][128] once the ring is done
 
@@ -176,9 +219,13 @@ __global__ void __launch_bounds__(kFewThreads)
   const int n_kb = kb1 - kb0;  // at least one: split <= k_stages
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(smem_u32(&full[s]), 2);  // the loads, and the scale warp
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&sf_full[s]), 2);  // the two scale warps
+      mbar_init(smem_u32(&sf_empty[s]), 1);
     }
     mbar_init(smem_u32(tfull), 1);
     *abort_flag = 0;
@@ -221,13 +268,13 @@ __global__ void __launch_bounds__(kFewThreads)
       const bool stall = (a.flags & kFewStall) != 0;  // test hook: load nothing
       // W does not depend on the producer step (bf16 or packed rows) this kernel may
       // have been launched beside: the first stages' W goes out before the wait for it.
-      const int first = stall ? 0 : (n_kb < C::STAGES ? n_kb : C::STAGES);
+      const int first = stall ? 0 : (n_kb < stages ? n_kb : stages);
       for (int i = 0; i < first; ++i) load_w(i, i);
       asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int i = 0; i < first; ++i) load_a(i, i);
       issued = first;
-      int stage = first == C::STAGES ? 0 : first;
-      uint32_t phase = first == C::STAGES ? 1 : 0;
+      int stage = first == stages ? 0 : first;
+      uint32_t phase = first == stages ? 1 : 0;
       for (int i = first; !stall && i < n_kb; ++i) {
         if (!mbar_wait_bounded(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, kFewWaitNs)) {
           few_failure(a.status, abort_flag, kErrProducerEmptyWait);
@@ -236,19 +283,18 @@ __global__ void __launch_bounds__(kFewThreads)
         load_w(i, stage);
         load_a(i, stage);
         ++issued;
-        if (++stage == C::STAGES) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
       // Without a failure the epilogue's wait covers every copy (the MMAs have read them).
-      // After one, stay until the last copies have landed; their barriers also count the
-      // scale warp, which may have left: then the limit ends the wait.
+      // After one, stay until the last copies have landed.
       if (*abort_flag) {
-        const int pending = issued < C::STAGES ? issued : C::STAGES;
+        const int pending = issued < stages ? issued : stages;
         for (int i = 0; i < pending; ++i) {
           if (stage == 0) {
-            stage = C::STAGES - 1;
+            stage = stages - 1;
             phase ^= 1u;
           } else {
             --stage;
@@ -264,24 +310,38 @@ __global__ void __launch_bounds__(kFewThreads)
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = idesc_mxf8_e4m3(kChannels, NT);
-      const uint32_t sfa = tmem_base + C::SFA_COL, sfb = tmem_base + C::SFB_COL;
+      const uint32_t sfb = tmem_base + C::SFB_COL;
       tc_copy_32x128b_x4(sfb, smem_desc_plain(smem_u32(sOne)));
       int stage = 0;
       uint32_t phase = 0;
       for (int i = 0; i < n_kb; ++i) {
+        const int chunk = i / kScaleChunk, slot = chunk & 1;
+        const uint32_t sfa = tmem_base + C::SFA_COL + 4 * (slot * kScaleChunk + i % kScaleChunk);
+        if (i % kScaleChunk == 0) {
+          // all of a chunk's scales at once, into columns the MMAs in flight do not read
+          if (!mbar_wait_bounded(smem_u32(&sf_full[slot]), (chunk >> 1) & 1, abort_flag, kFewWaitNs)) {
+            few_failure(a.status, abort_flag, kErrMmaFullWait);
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < kScaleChunk; ++j)
+            if (i + j < n_kb)
+              tc_copy_32x128b_x4(sfa + 4 * j, smem_desc_plain(smem_u32(sSF + (slot * kScaleChunk + j) * kFewScaleBytes)));
+          tc_commit(smem_u32(&sf_empty[slot]));
+        }
         if (!mbar_wait_bounded(smem_u32(&full[stage]), phase, abort_flag, kFewWaitNs)) {
           few_failure(a.status, abort_flag, kErrMmaFullWait);
           break;
         }
         tc_fence_after();
-        tc_copy_32x128b_x4(sfa, smem_desc_plain(smem_u32(sSF + stage * kFewScaleBytes)));
         const uint64_t wd = smem_desc_sw128(smem_u32(sW + stage * C::W_BYTES));
         const uint64_t ad = smem_desc_sw128(smem_u32(sA + stage * C::A_BYTES));
 #pragma unroll
         for (int k = 0; k < kFewK / 32; ++k)
           mma_mxf8(tmem_base, wd + 2 * k, ad + 2 * k, idesc_with_sf_id(idesc, k, 0), sfa, sfb, (i | k) != 0 ? 1u : 0u);
         tc_commit(smem_u32(&empty[stage]));
-        if (++stage == C::STAGES) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -289,50 +349,40 @@ __global__ void __launch_bounds__(kFewThreads)
       tc_commit(smem_u32(tfull));  // also on failure: every operation issued above has completed
     }
     __syncwarp();
-  } else if (warp == 2) {
-    // Block scales: lane r gathers the words of channels r, 32 + r, 64 + r, 96 + r of each
-    // K block, four K blocks ahead of the one it writes.
-    constexpr int kAhead = 4;
-    uint32_t w[kAhead][4];
-    const uint8_t* row[4];
-    bool live[4];
+  } else if (warp < 4) {
+    // Block scales: warp 2 gathers the words of channels r and 32 + r (r its lane), warp 3
+    // of 64 + r and 96 + r, for kScaleChunk K blocks at a time (beside every ring stage instead:
+    // 26.9 us against 23.5 for one token, K = 5120, N = 20480).
+    const uint8_t* row[2];
+    bool live[2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int n = n0 + 32 * c + lane;
+    for (int c = 0; c < 2; ++c) {
+      const int n = n0 + 32 * (2 * (warp - 2) + c) + lane;
       live[c] = n < a.N;
       row[c] = a.w_sf + static_cast<size_t>(live[c] ? n : 0) * a.k_blocks;
     }
+    for (int chunk = 0; chunk * kScaleChunk < n_kb; ++chunk) {
+      uint32_t w[kScaleChunk][2];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
+      for (int j = 0; j < kScaleChunk; ++j)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) w[j][c] = scale_word(row[c], live[c] && j < n_kb, kb0 + j, a.k_blocks);
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int i0 = 0; ok && i0 < n_kb; i0 += kAhead) {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (ok && i0 + j < n_kb) {
-          ok = mbar_wait_bounded(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, kFewWaitNs);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            *reinterpret_cast<uint4*>(sSF + stage * kFewScaleBytes + 16 * lane) =
-                make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full[stage]));
-            if (++stage == C::STAGES) {
-              stage = 0;
-              phase ^= 1u;
-            }
-          }
-          const int next = i0 + j + kAhead;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) w[j][c] = scale_word(row[c], live[c] && next < n_kb, kb0 + next, a.k_blocks);
-        }
+        for (int c = 0; c < 2; ++c)
+          w[j][c] = scale_word(row[c], live[c] && chunk * kScaleChunk + j < n_kb, kb0 + chunk * kScaleChunk + j, a.k_blocks);
+      const int slot = chunk & 1;
+      bool ok = mbar_wait_bounded(smem_u32(&sf_empty[slot]), ((chunk >> 1) & 1) ^ 1u, abort_flag, kFewWaitNs);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (lane == 0) few_failure(a.status, abort_flag, kErrProducerEmptyWait);
+        break;
       }
+#pragma unroll
+      for (int j = 0; j < kScaleChunk; ++j)
+        *reinterpret_cast<uint2*>(sSF + (slot * kScaleChunk + j) * kFewScaleBytes + 16 * lane + 8 * (warp - 2)) =
+            make_uint2(w[j][0], w[j][1]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sf_full[slot]));
     }
-    if (!ok && lane == 0) few_failure(a.status, abort_flag, kErrProducerEmptyWait);
     __syncwarp();
   } else if (warp >= 4) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the row scales of a producer step
