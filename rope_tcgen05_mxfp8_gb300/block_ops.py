@@ -9,6 +9,7 @@ runs on `stream` (default: that device's current stream) and does not synchronis
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence
 
 import torch
@@ -203,7 +204,9 @@ def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None,
     return out, mean, rstd
 
 
+@functools.lru_cache(maxsize=64)
 def qkv_cte_layer_norm_backward_workspace(rows: int, cols: int) -> int:
+    """Workspace bytes of qkv_cte_layer_norm_backward (a function of the sizes alone)."""
     n = ctypes.c_size_t()
     _check(_lib().qkv_cte_layer_norm_backward_workspace(rows, cols, ctypes.byref(n)))
     return n.value
@@ -226,7 +229,7 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
     if dx is None and dweight is None and dbias is None:
         dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
         sums = torch.empty(2, cols, dtype=pdt, device=dev)
-        dweight, dbias = sums[0], sums[1]
+        dweight, dbias = sums.unbind(0)
         made += [dx, sums]
         pd, ldd = dx.data_ptr(), cols
         pdw = sums.data_ptr()
