@@ -370,7 +370,7 @@ enum { QKV_CTE_DTYPE_BF16 = 0, QKV_CTE_DTYPE_FP16 = 1, QKV_CTE_DTYPE_FP32 = 2 };
  * Any cols >= 1 and any element-aligned pointers are taken; 16-byte aligned pointers and
  * strides and whole 16-byte rows run fastest. rows == 0 launches nothing. Returns 0, -1
  * (null or overlapping buffers, strides, types, eps), -2 (alignment to the element,
- * rows > INT32_MAX), -3 or -4. */
+ * rows > INT32_MAX, cols > 2^28), -3 or -4. */
 int qkv_cte_layer_norm(const void* x, int64_t x_row_stride, const void* weight, const void* bias, void* y,
                        int64_t y_row_stride, float* mean, float* rstd, int64_t rows, int32_t cols, float eps,
                        int32_t dtype, int32_t param_dtype, void* stream);
@@ -468,9 +468,9 @@ enum { QKV_CTE_ACT_NONE = 0,
        QKV_CTE_ACT_SILU = 3 };    /* z / (1 + exp(-z)) */
 
 typedef struct {
-    int64_t tokens;       /* T >= 0, <= INT32_MAX */
-    int32_t in_features;  /* K: a multiple of 32 */
-    int32_t out_features; /* N >= 1 */
+    int64_t tokens;       /* T >= 0, <= INT32_MAX - 255 */
+    int32_t in_features;  /* K: a multiple of 32, <= 2^30 */
+    int32_t out_features; /* N >= 1, <= 2^30 */
     int32_t act;          /* QKV_CTE_ACT_* */
     int32_t out_dtype;    /* QKV_CTE_DTYPE_*: of O and of the residual */
     int32_t input_layout; /* QKV_CTE_INPUT_*: what A holds, as for qkv_cte_run */

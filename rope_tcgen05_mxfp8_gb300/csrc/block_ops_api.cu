@@ -50,6 +50,8 @@ int check_shape(int64_t rows, int32_t cols, const char* who) {
   if (rows < 0) return fail(QKV_CTE_ERR_INVALID, "%s: rows must be >= 0", who);
   if (cols <= 0) return fail(QKV_CTE_ERR_INVALID, "%s: cols must be > 0", who);
   if (rows > INT32_MAX) return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: rows > INT32_MAX", who);
+  if (cols > 1 << 28)  // column indexes and twice them stay well inside 32 bits
+    return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: cols %d > 2^28", who, cols);
   return QKV_CTE_OK;
 }
 

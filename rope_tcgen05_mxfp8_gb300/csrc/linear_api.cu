@@ -73,12 +73,13 @@ int qkv_cte_linear_plan(qkv_cte_linear_plan_t* out, const qkv_cte_linear_desc* d
   *out = nullptr;
   const qkv_cte_linear_desc& d = *desc;
   if (d.tokens < 0) return fail(QKV_CTE_ERR_INVALID, "%s: tokens must be >= 0 (got %lld)", who, (long long)d.tokens);
-  if (d.tokens > INT32_MAX) return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: tokens > INT32_MAX", who);
+  if (d.tokens > INT32_MAX - 255)  // rows rounded up to whole tiles stay inside 32 bits
+    return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: more than INT32_MAX - 255 tokens", who);
   if (d.in_features <= 0 || d.out_features <= 0)
     return fail(QKV_CTE_ERR_INVALID, "%s: in_features and out_features must be > 0", who);
   if (d.in_features % 32 != 0)
     return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: in_features %d is not a multiple of 32", who, d.in_features);
-  if (d.out_features > INT32_MAX / 2) return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: out_features too large", who);
+  if (d.in_features > 1 << 30 || d.out_features > 1 << 30) return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: in_features or out_features > 2^30", who);
   if (d.act < QKV_CTE_ACT_NONE || d.act > QKV_CTE_ACT_SILU)
     return fail(QKV_CTE_ERR_INVALID, "%s: unknown activation %d", who, d.act);
   if (d.out_dtype < QKV_CTE_DTYPE_BF16 || d.out_dtype > QKV_CTE_DTYPE_FP32)

@@ -33,7 +33,7 @@ def _ln(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), -1), (dict(y=None), -1),
     (dict(rows=-1), -1), (dict(rows=0), 0), (dict(rows=0, x=None, y=None), 0), (dict(rows=2 ** 31), -2),
-    (dict(cols=0), -1), (dict(cols=-5), -1),
+    (dict(cols=0), -1), (dict(cols=-5), -1), (dict(cols=2 ** 28 + 1, ldx=2 ** 29, ldy=2 ** 29), -2),
     (dict(eps=-1e-6), -1), (dict(eps=float("nan")), -1), (dict(eps=float("inf")), -1),
     (dict(dtype=3), -1), (dict(dtype=-1), -1), (dict(pdtype=1), -1), (dict(dtype=2, pdtype=0), -1),
     (dict(ldx=63), -1), (dict(ldy=63), -1), (dict(ldy=0), -1), (dict(ldx=-64), -1),
@@ -181,6 +181,7 @@ def test_new_entry_points_are_exported():
 
 @pytest.mark.parametrize("kw,code", [
     (dict(), 0), (dict(tokens=0), 0), (dict(tokens=1), 0), (dict(tokens=-1), -1), (dict(tokens=2 ** 31), -2),
+    (dict(tokens=2 ** 31 - 1), -2), (dict(in_features=2 ** 30 + 32), -2),
     (dict(in_features=0), -1), (dict(in_features=48), -2), (dict(in_features=32), 0), (dict(in_features=-32), -1),
     (dict(out_features=0), -1), (dict(out_features=1), 0), (dict(out_features=2 ** 31 - 1), -2),
     (dict(act=4), -1), (dict(act=-1), -1), (dict(act=3), 0), (dict(out_dtype=3), -1), (dict(out_dtype=2), 0),
