@@ -34,6 +34,25 @@ struct qkv_cte_linear_plan_s {
 
 namespace {
 
+// K1's tile width. A wave of tiles (one per CTA pair, 76 pairs on GB300's 152 SMs) takes
+// about 12.5, 13.9 and 15.4 us at K = 5120 for widths 128, 192 and 240, proportional to
+// the width plus 350, so the widest tile wins many waves and a narrower one few. us a call
+// for 128 / 192 / 240: 1024 x 5120 x 1280 24.7 / 26.8 / 28.8 (one wave each),
+// 2048 x 5120 x 5120 74 / 54 / 57 (5, 3 and 3), 4096 x 5120 x 5120 122 / 96 / 88 (9, 6, 5).
+int choose_tile_n(long long m_tiles, long long N) {
+  int best = 0;
+  long long best_cost = 0;
+  for (int t : {240, 192, 128}) {
+    const long long waves = (m_tiles * ((N + t - 1) / t) + 75) / 76;
+    const long long cost = waves * (t + 350);
+    if (best == 0 || cost < best_cost) {
+      best = t;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
 // Token tile and K split of the channel-major form, and whether it is the form for a
 // problem (its rows' alignment aside). Measured on GB300, us a call, K1 against it:
 //   T, K, N            K1     token tile / split
@@ -42,8 +61,8 @@ namespace {
 //   128, 1024, 5120    19.4   12.4 (64/2)
 //   256, 5120, 5120    28.8   20.7 (128/2)
 //   128, 5120, 20480   50     33.0 (128/1)
-//   512, 1024, 5120    20.3   16.5 (128/1)
-//   512, 5120, 5120    28.8   29.0 (128/1)
+//   512, 1024, 5120    18.6   16.5 (128/1)
+//   512, 5120, 5120    26.9   29.0 (128/1)
 //   256, 5120, 20480   51     57.6 (128/1, 320 tiles)
 // It wins while its tiles fit the SMs about once (two CTAs share an SM, at the expense of
 // each other's loads); smaller token tiles add CTAs while there are few.
@@ -57,7 +76,7 @@ bool choose_few(const GemmShape& g, int* token_tile, int* split) {
   while (s < 8 && 2 * s <= g.k_stages && tiles * 2 * s <= 192) s *= 2;
   *token_tile = nt;
   *split = s;
-  return g.T <= 64 || (g.T <= 512 && tiles <= 160);
+  return g.T <= 64 || (tiles <= 160 && (g.T <= 256 || (g.T <= 512 && g.H <= 2048)));
 }
 
 size_t out_size(const qkv_cte_linear_desc& d) { return d.out_dtype == QKV_CTE_DTYPE_FP32 ? 4 : 2; }
@@ -95,10 +114,10 @@ int qkv_cte_linear_plan(qkv_cte_linear_plan_t* out, const qkv_cte_linear_desc* d
   g.T = (int)d.tokens;
   g.H = d.in_features;
   g.I = d.out_features;
-  g.tile_n = 240;
   g.cta_pair = 1;
   g.blocks128 = (g.T + 127) / 128;
   g.m_tiles = (g.T + 255) / 256;
+  g.tile_n = choose_tile_n(g.m_tiles, g.I);
   g.n_tiles = (g.I + g.tile_n - 1) / g.tile_n;
   g.k_stages = (g.H + 127) / 128;  // a short last K block reads zeros past the row's end
   if ((long long)g.m_tiles * g.n_tiles > INT32_MAX) {

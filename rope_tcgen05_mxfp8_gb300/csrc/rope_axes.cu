@@ -29,8 +29,10 @@ namespace qkvcte {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kHeadsPerThread = 8;  // heads a thread walks with one set of cos and sin
-constexpr int kHeadsAtOnce = 4;     // of which so many are requested ahead
+// Heads a thread turns with one set of cos and sin, all of them requested before cos and
+// sin are computed. 32760 x 40 heads of 128 in bf16: 107 us with 8 heads; 121 with 8
+// requested 4 at a time, 125 with 20, 135 with 40.
+constexpr int kHeadsPerThread = 8;
 
 // cos and sin of pos * step turns (step: a binary fraction of a turn).
 __device__ __forceinline__ void turn(int pos, unsigned long long step, float& c, float& s) {
@@ -79,7 +81,7 @@ __device__ __forceinline__ int pair_axis_position(const RopeArgs& a, int pair, c
 }
 
 // PV pairs per thread: vectors of PV elements at lane p0 and at p0 + d/2 (rotate-half), or
-// one of 2 PV elements at 2 p0 (interleaved). cos and sin are computed while the first heads' loads are in flight.
+// one of 2 PV elements at 2 p0 (interleaved). cos and sin are computed while the heads' loads are in flight.
 template <typename T, int PV>
 struct HalfPairs {
   using V = Vec<T, PV>;
@@ -157,9 +159,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_apply_kernel(const __grid_c
   const T* x = static_cast<const T*>(a.x) + b * a.xb + s * a.xs + h0 * a.xh;
   T* y = static_cast<T*>(a.y) + b * a.yb + s * a.ys + h0 * a.yh;
   const int n = min(a.heads - h0, kHeadsPerThread);
-  Pairs v[kHeadsAtOnce];
+  Pairs v[kHeadsPerThread];
 #pragma unroll
-  for (int k = 0; k < kHeadsAtOnce; ++k)
+  for (int k = 0; k < kHeadsPerThread; ++k)
     if (k < n) v[k].load(x + k * a.xh, p0, half);
   int pos[kRopeMaxAxes];
   const bool live = row_position(a, b, s, pos);
@@ -170,15 +172,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_apply_kernel(const __grid_c
     turn(pair_axis_position(a, p0 + j, pos), a.step[p0 + j], cs[j], sn[j]);
     if (a.inverse) sn[j] = -sn[j];
   }
-  for (int h = 0; h < n; h += kHeadsAtOnce) {
 #pragma unroll
-    for (int k = 0; k < kHeadsAtOnce; ++k) {
-      if (h + k < n) {
-        Pairs o = v[k];
-        if (h + k + kHeadsAtOnce < n) v[k].load(x + (h + k + kHeadsAtOnce) * a.xh, p0, half);
-        if (live) o.rotate(cs, sn);  // padding rows keep their values, whatever they are
-        o.store(y + (h + k) * a.yh, p0, half);
-      }
+  for (int k = 0; k < kHeadsPerThread; ++k) {
+    if (k < n) {
+      if (live) v[k].rotate(cs, sn);  // padding rows keep their values, whatever they are
+      v[k].store(y + k * a.yh, p0, half);
     }
   }
 }
