@@ -221,8 +221,8 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
     dev, cols = x.device, x.shape[-1]
     rows = x.numel() // cols if cols else 0
     pg, ldg = _rows("dy", dy, (x.dtype,), dev, x.shape)
-    param = next((t for t in (weight, dweight, dbias) if isinstance(t, torch.Tensor)), None)
-    pdt = param.dtype if param is not None else torch.float32
+    param = weight if weight is not None else dweight if dweight is not None else dbias
+    pdt = param.dtype if isinstance(param, torch.Tensor) else torch.float32
     if pdt not in (x.dtype, torch.float32):
         raise TypeError(f"weight, dweight and dbias: dtype {pdt} is neither {x.dtype} nor torch.float32")
     made = []

@@ -8,7 +8,7 @@
 // of threads (a warp for short rows, a block for long ones) and is read once; the
 // variance is taken about the mean in a second sweep over the registers, never as a
 // difference of large sums. Rows come through a ring in shared memory that each thread
-// fills for itself with 16-byte asynchronous copies, kRing rows ahead, so that loads
+// fills for itself with 16-byte asynchronous copies, two or three rows ahead, so that loads
 // stay in flight across the reductions; parameters stay in registers over all the rows
 // of a block. The backward pass keeps its column sums dw and db in the registers of the
 // same threads; one partial row per block goes to the workspace, and a second kernel
@@ -18,7 +18,9 @@
 // Arithmetic counts: a first form that converted each element in each sweep, read the
 // parameters from L1 and prefetched one row into registers ran 24 instructions per
 // element and took 204 us for 32760 x 5120 in bf16, twice the floor. Elements are
-// converted once, worked on in pairs (fma.rn.f32x2 and so on) and kept as x - mu.
+// converted once, worked on in pairs (fma.rn.f32x2 and so on) and kept as x - mu: 101 us
+// (6.6 TB/s, 98 % of the measured copy rate). Backward, 4096 x 5120: 35 us with the join
+// of the column sums (3.6 TB/s); 32760 x 5120: 175 us (5.8 TB/s).
 #include <algorithm>
 
 #include "block_ops.h"
@@ -34,7 +36,6 @@ namespace {
 constexpr int kWarpRows = 4;  // rows (warps) per block of the warp-per-row form
 
 constexpr int kGradCluster = 4;  // blocks whose column sums are joined on chip
-constexpr int kRing = 3;      // rows in flight per group of threads
 
 // Sums of N values over the group of threads that holds a row: a warp (blockDim.x ==
 // 32, no barrier) or the whole block of at most 4 * kQuads warps. `slot` alternates
@@ -123,11 +124,10 @@ struct Lanes<1> {
 // A thread's part of a row: CH accesses of VEC elements, blockDim.x accesses apart (kFull:
 // the row fills them all). The next rows are on their way: whole 16-byte accesses go
 // through the ring, single elements wait in registers, one row ahead.
-template <typename T, int VEC, int CH, bool kFull>
+template <typename T, int VEC, int CH, bool kFull, int kRows>
 struct RowStream {
   static constexpr bool kAsync = VEC > 1;
-  // rows kept requested
-  static constexpr int kAhead = !kAsync ? 1 : (CH > 2 ? 2 : kRing);
+  static constexpr int kAhead = kAsync ? kRows : 1;  // rows kept requested
   static constexpr int kBytes = kAsync ? kAhead * CH * 16 : 0;  // of the ring, per thread
 
   const T* next;   // this thread's first element of the next row to request
@@ -213,7 +213,10 @@ struct Form {
   static constexpr bool kKeep = kKeep_, kFull = kFull_;
   static constexpr int kQuads = kKeep ? 2 : 4;
   using L = Lanes<VEC>;
-  using Stream = RowStream<T, VEC, CH, kFull>;
+  // Rows in flight: 32760 x 5120 bf16 forward 118 us with two and 120 with three at four
+  // accesses per thread, backward 182 and 175.
+  using Forward = RowStream<T, VEC, CH, kFull, (CH > 2 ? 2 : 3)>;
+  using Backward = RowStream<T, VEC, CH, kFull, 3>;
 };
 
 template <typename Fm>
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_kernel(Layer
   using T = typename Fm::T;
   using L = typename Fm::L;
   using F = typename L::F;
-  using Stream = typename Fm::Stream;
+  using Stream = typename Fm::Forward;
   constexpr int VEC = Fm::VEC, CH = Fm::CH, kAhead = Stream::kAhead;
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ GroupSums<1, Fm::kQuads> red;
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_backward_ker
   using T = typename Fm::T;
   using L = typename Fm::L;
   using F = typename L::F;
-  using Stream = typename Fm::Stream;
+  using Stream = typename Fm::Backward;
   constexpr int VEC = Fm::VEC, CH = Fm::CH, kAhead = Stream::kAhead;
   // the ring; after the last row, with several rows per block, [2][cols] column sums
   extern __shared__ __align__(16) uint8_t ring_mem[];
@@ -618,11 +621,14 @@ template <typename Fm>
 cudaError_t forward_launch(const LayerNormArgs& a, dim3 block, cudaStream_t s, int num_sms) {
   auto k = layer_norm_kernel<Fm>;
   const long long groups = (a.rows + block.y - 1) / block.y;
-  const size_t smem = static_cast<size_t>(Fm::Stream::kBytes) * block.x * block.y;
+  const size_t smem = static_cast<size_t>(Fm::Forward::kBytes) * block.x * block.y;
   int resident = 0;
   const cudaError_t e = QKVCTE_RESIDENT(k, block, smem, 1, num_sms, &resident);
   if (e != cudaSuccess) return e;
-  k<<<static_cast<int>(std::min<long long>(groups, resident)), block, smem, s>>>(a);
+  // Eight times the resident blocks: with rows dealt out once, the SMs that get less of the
+  // bandwidth finish last (32760 x 5120 bf16 118 us; 113, 106, 101 and 104 with 2, 4, 8
+  // and 16 times).
+  k<<<static_cast<int>(std::min<long long>(groups, 8LL * resident)), block, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -637,7 +643,7 @@ cudaError_t forward_go(const LayerNormArgs& a, dim3 block, cudaStream_t s, int n
 
 // Accesses per thread: one or two for rows of up to 64 (a warp) or 256 accesses, then
 // four. More accesses per thread mean fewer warps per row, each of which pays for the
-// reductions and addresses: 5120 bf16 columns on 160 threads take 105 us for 32760 rows,
+// reductions and addresses: 5120 bf16 columns on 160 threads took 105 us for 32760 rows,
 // on 320 threads 150 us.
 template <typename T, typename P, int VEC>
 cudaError_t forward_vec(const LayerNormArgs& a, cudaStream_t s, int num_sms) {
@@ -682,7 +688,7 @@ cudaError_t join(const LayerNormGradArgs& a, int parts, cudaStream_t s) {
 template <typename Fm>
 cudaError_t backward_launch(const LayerNormGradArgs& a, dim3 block, cudaStream_t s, int num_sms) {
   auto k = layer_norm_backward_kernel<Fm>;
-  size_t smem = 2 * static_cast<size_t>(Fm::Stream::kBytes) * block.x * block.y;
+  size_t smem = 2 * static_cast<size_t>(Fm::Backward::kBytes) * block.x * block.y;
   const bool sums = a.partial != nullptr;
   if (sums) smem = std::max(smem, 2 * sizeof(float) * static_cast<size_t>(a.cols));
   const int cluster = sums ? kGradCluster : 1;
