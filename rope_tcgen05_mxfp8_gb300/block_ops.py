@@ -228,12 +228,10 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
     made = []
     if dx is None and dweight is None and dbias is None:
         dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        sums = torch.empty(2, cols, dtype=pdt, device=dev)
-        dweight, dbias = sums.unbind(0)
-        made += [dx, sums]
-        pd, ldd = dx.data_ptr(), cols
-        pdw = sums.data_ptr()
-        pdb = pdw + cols * sums.element_size()
+        dweight = torch.empty(cols, dtype=pdt, device=dev)
+        dbias = torch.empty(cols, dtype=pdt, device=dev)
+        made += [dx, dweight, dbias]
+        pd, ldd, pdw, pdb = dx.data_ptr(), cols, dweight.data_ptr(), dbias.data_ptr()
     else:
         pd, ldd = _rows("dx", dx, (x.dtype,), dev, x.shape) if dx is not None else (None, 0)
         pdw = _vector("dweight", dweight, (pdt,), dev, cols)
