@@ -53,21 +53,6 @@ __device__ __forceinline__ void store_any(void* p, long long i, int dtype, float
   }
 }
 
-// Two neighbouring elements at an even index from a pointer aligned to both.
-__device__ __forceinline__ float2 load_pair(const void* p, long long i, int dtype) {
-  if (dtype == QKV_CTE_DTYPE_FP32) return *reinterpret_cast<const float2*>(static_cast<const float*>(p) + i);
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i);
-  return dtype == QKV_CTE_DTYPE_BF16 ? unpack_pair<__nv_bfloat16>(w) : unpack_pair<__half>(w);
-}
-
-__device__ __forceinline__ void store_pair(void* p, long long i, int dtype, float2 v) {
-  if (dtype == QKV_CTE_DTYPE_FP32)
-    *reinterpret_cast<float2*>(static_cast<float*>(p) + i) = v;
-  else
-    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + i) =
-        dtype == QKV_CTE_DTYPE_BF16 ? pack_pair<__nv_bfloat16>(v) : pack_pair<__half>(v);
-}
-
 // 32-byte global load. Not the read-only path: the residual may be the output itself.
 __device__ __forceinline__ void ld_global_v8_b32(const void* p, uint32_t* w) {
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -169,7 +154,7 @@ __device__ __forceinline__ void finish16(const LinearEpilogue& e, long long row,
   st_global_v8_b32_hint(static_cast<uint16_t*>(e.out) + row * e.ldo + col0, w, pol);
 }
 
-// One element, any alignment: the few-token form and ragged chunks.
+// One element, any alignment: ragged chunks.
 __device__ __forceinline__ void finish_one(const LinearEpilogue& e, long long row, int c, float acc, float scale,
                                            float bias, float gate) {
   float v = apply_act(fmaf(acc, scale, bias), e.act);

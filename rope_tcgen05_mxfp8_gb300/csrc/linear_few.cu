@@ -77,17 +77,20 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, bool live, in
   return w;
 }
 
-// A thread's two channels.
+// A thread's two channels, n and n + apart: neighbours where rows keep pairs of elements
+// aligned, else 64 apart, so that consecutive lanes store consecutive elements.
 struct ChannelParams {
+  int n, apart;
   float col[2], bias[2], gate[2];
 
-  __device__ __forceinline__ ChannelParams(const LinearFewArgs& a, int n) {
+  __device__ __forceinline__ ChannelParams(const LinearFewArgs& a, int n_, int apart_) : n(n_), apart(apart_) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const bool in = n + k < a.N;
-      col[k] = a.w_col_scale != nullptr && in ? __ldg(a.w_col_scale + n + k) : 1.0f;
-      bias[k] = a.bias != nullptr && in ? to_f32(reinterpret_cast<const __nv_bfloat16*>(a.bias)[n + k]) : 0.0f;
-      gate[k] = a.lin.gate != nullptr && in ? to_f32(reinterpret_cast<const __nv_bfloat16*>(a.lin.gate)[n + k]) : 1.0f;
+      const int c = n + k * apart;
+      const bool in = c < a.N;
+      col[k] = a.w_col_scale != nullptr && in ? __ldg(a.w_col_scale + c) : 1.0f;
+      bias[k] = a.bias != nullptr && in ? to_f32(reinterpret_cast<const __nv_bfloat16*>(a.bias)[c]) : 0.0f;
+      gate[k] = a.lin.gate != nullptr && in ? to_f32(reinterpret_cast<const __nv_bfloat16*>(a.lin.gate)[c]) : 1.0f;
     }
   }
 };
@@ -101,24 +104,27 @@ __device__ __forceinline__ void activate(float2 (&v)[kBatch]) {
 // Tokens t, t + step, ... (kBatch of them, those below `live`) of the tile: the sum of
 // the cluster's parts in rank order, the epilogue, two elements stored. kMaxParts: the
 // cluster's size where it is known, else its largest.
-template <int kBatch, int kMaxParts>
+template <int kBatch, int kMaxParts, bool kPairs, typename T>
 __device__ __forceinline__ void finish_tokens(const LinearFewArgs& a, const ChannelParams& cp, uint32_t base,
-                                              const float* row_scale, int t0, int t, int step, int live, int n) {
+                                              const float* row_scale, int t0, int t, int step, int live) {
   const LinearEpilogue& e = a.lin;
-  float2 v[kBatch], res[kBatch];
+  const int n = cp.n;
+  const bool second = n + cp.apart < a.N;
+  float2 v[kBatch];
+  // the residual as it comes: converting here would wait for each load in turn
+  Vec<T, 2> both[kBatch];
+  T one[kBatch][2];
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
     const int tu = t + u * step;
-    res[u] = v[u] = make_float2(0.0f, 0.0f);
-    if (tu < live) {
-      if (e.residual != nullptr) {
-        const long long i = static_cast<long long>(t0 + tu) * e.ldr + n;
-        if (e.pairs && n + 1 < a.N) {
-          res[u] = load_pair(e.residual, i, e.dtype);
-        } else {
-          res[u].x = load_any(e.residual, i, e.dtype);
-          if (n + 1 < a.N) res[u].y = load_any(e.residual, i + 1, e.dtype);
-        }
+    v[u] = make_float2(0.0f, 0.0f);
+    if (tu < live && e.residual != nullptr) {
+      const T* p = static_cast<const T*>(e.residual) + static_cast<long long>(t0 + tu) * e.ldr + n;
+      if (kPairs && second) {
+        both[u] = *reinterpret_cast<const Vec<T, 2>*>(p);
+      } else {
+        one[u][0] = p[0];
+        if (second) one[u][1] = p[cp.apart];
       }
     }
   }
@@ -127,19 +133,23 @@ __device__ __forceinline__ void finish_tokens(const LinearFewArgs& a, const Chan
     const int tu = t + u * step;
     if (tu < live) {
       const uint32_t addr = base + 4 * kChannels * tu;
-      if constexpr (kMaxParts == 1) {
-        v[u] = ld_shared_f32x2(addr);
-      } else {
-        float2 p[kMaxParts];
+      float2 p[kMaxParts];
 #pragma unroll
-        for (int r = 0; r < kMaxParts; ++r)
-          p[r] = kMaxParts == 2 || r < a.split ? ld_shared_cluster_f32x2(mapa_shared(addr, r)) : make_float2(0.0f, 0.0f);
-        v[u] = p[0];
-#pragma unroll
-        for (int r = 1; r < kMaxParts; ++r) {
-          v[u].x += p[r].x;
-          v[u].y += p[r].y;
+      for (int r = 0; r < kMaxParts; ++r) {
+        p[r] = make_float2(0.0f, 0.0f);
+        if constexpr (kMaxParts == 1) {
+          p[r] = kPairs ? ld_shared_f32x2(addr) : make_float2(ld_shared_f32(addr), ld_shared_f32(addr + 4 * 64));
+        } else if (kMaxParts == 2 || r < a.split) {
+          const uint32_t remote = mapa_shared(addr, r);
+          p[r] = kPairs ? ld_shared_cluster_f32x2(remote)
+                        : make_float2(ld_shared_cluster_f32(remote), ld_shared_cluster_f32(remote + 4 * 64));
         }
+      }
+      v[u] = p[0];
+#pragma unroll
+      for (int r = 1; r < kMaxParts; ++r) {
+        v[u].x += p[r].x;
+        v[u].y += p[r].y;
       }
     }
   }
@@ -156,33 +166,48 @@ __device__ __forceinline__ void finish_tokens(const LinearFewArgs& a, const Chan
     case QKV_CTE_ACT_SILU: activate<kBatch, QKV_CTE_ACT_SILU>(v); break;
     default: break;
   }
+  T* out = static_cast<T*>(e.out) + static_cast<long long>(t0 + t) * e.ldo + n;
+  const long long pitch = step * e.ldo;
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
-    v[u].x = fmaf(cp.gate[0], v[u].x, res[u].x);
-    v[u].y = fmaf(cp.gate[1], v[u].y, res[u].y);
-  }
-  const bool pair = e.pairs && n + 1 < a.N;
-  const long long i0 = static_cast<long long>(t0 + t) * e.ldo + n;
-  const long long pitch = step * e.ldo;
-  if (pair && e.dtype == QKV_CTE_DTYPE_BF16) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      if (t + u * step < live) store_pair(e.out, i0 + u * pitch, QKV_CTE_DTYPE_BF16, v[u]);
-  } else if (pair) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      if (t + u * step < live) store_pair(e.out, i0 + u * pitch, e.dtype, v[u]);
-  } else {
-    for (int u = 0; u < kBatch; ++u) {
-      float2 o = v[0];
-#pragma unroll
-      for (int k = 1; k < kBatch; ++k)
-        if (u == k) o = v[k];
-      if (t + u * step < live) {
-        store_any(e.out, i0 + u * pitch, e.dtype, o.x);
-        if (n + 1 < a.N) store_any(e.out, i0 + u * pitch + 1, e.dtype, o.y);
+    if (t + u * step < live) {
+      float2 o = make_float2(cp.gate[0] * v[u].x, cp.gate[1] * v[u].y);
+      if (e.residual != nullptr) {
+        float2 r = make_float2(0.0f, 0.0f);
+        if (kPairs && second) {
+          r = both[u].pair(0);
+        } else {
+          r.x = to_f32(one[u][0]);
+          if (second) r.y = to_f32(one[u][1]);
+        }
+        o = make_float2(o.x + r.x, o.y + r.y);
+      }
+      T* p = out + u * pitch;
+      if (kPairs && second) {
+        Vec<T, 2> w;
+        w.set_pair(0, o);
+        st_vec(p, w);
+      } else {
+        p[0] = from_f32<T>(o.x);
+        if (second) p[cp.apart] = from_f32<T>(o.y);
       }
     }
+  }
+}
+
+// The CTA's tokens rank + split * (group, group + 4, ...), some at a time so that their
+// loads overlap.
+template <bool kPairs, typename T>
+__device__ __forceinline__ void finish_tile(const LinearFewArgs& a, const ChannelParams& cp, uint32_t base,
+                                            const float* row_scale, int t0, int rank, int live) {
+  const int step = a.split * 4;
+  int t = rank + a.split * (static_cast<int>(threadIdx.x) >> 6);
+  if (a.split == 1) {
+    for (; t < live; t += 8 * step) finish_tokens<8, 1, kPairs, T>(a, cp, base, row_scale, t0, t, step, live);
+  } else if (a.split == 2) {
+    for (; t < live; t += 8 * step) finish_tokens<8, 2, kPairs, T>(a, cp, base, row_scale, t0, t, step, live);
+  } else {
+    for (; t < live; t += 2 * step) finish_tokens<2, 8, kPairs, T>(a, cp, base, row_scale, t0, t, step, live);
   }
 }
 
@@ -248,8 +273,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
   // What the end needs of each thread's two channels is requested now.
   const int live_tokens = a.T - t0 < NT ? a.T - t0 : NT;
-  const int ch = 2 * (static_cast<int>(threadIdx.x) & 63);
-  const ChannelParams cp(a, n0 + ch);
+  const int ch = (static_cast<int>(threadIdx.x) & 63) * (a.lin.pairs ? 2 : 1);
+  const ChannelParams cp(a, n0 + ch, a.lin.pairs ? 1 : 64);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -410,18 +435,16 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   if (split > 1) cluster_sync();  // every CTA's partial sums are in place
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!*abort_flag && n0 + ch < a.N) {
-    // tokens rank + split * (group, group + 4, ...) with two channels per thread, kBatch at
-    // a time so that their loads overlap
     const uint32_t base = smem_u32(part) + 4 * ch;
-    const int step = split * 4;
-    int t = rank + split * (static_cast<int>(threadIdx.x) >> 6);
-    if (split == 1) {
-      for (; t < live_tokens; t += 8 * step) finish_tokens<8, 1>(a, cp, base, row_scale, t0, t, step, live_tokens, n0 + ch);
-    } else if (split == 2) {
-      for (; t < live_tokens; t += 8 * step) finish_tokens<8, 2>(a, cp, base, row_scale, t0, t, step, live_tokens, n0 + ch);
-    } else {
-      for (; t < live_tokens; t += 2 * step) finish_tokens<2, 8>(a, cp, base, row_scale, t0, t, step, live_tokens, n0 + ch);
-    }
+    if (a.lin.dtype == QKV_CTE_DTYPE_BF16)
+      a.lin.pairs ? finish_tile<true, __nv_bfloat16>(a, cp, base, row_scale, t0, rank, live_tokens)
+                  : finish_tile<false, __nv_bfloat16>(a, cp, base, row_scale, t0, rank, live_tokens);
+    else if (a.lin.dtype == QKV_CTE_DTYPE_FP16)
+      a.lin.pairs ? finish_tile<true, __half>(a, cp, base, row_scale, t0, rank, live_tokens)
+                  : finish_tile<false, __half>(a, cp, base, row_scale, t0, rank, live_tokens);
+    else
+      a.lin.pairs ? finish_tile<true, float>(a, cp, base, row_scale, t0, rank, live_tokens)
+                  : finish_tile<false, float>(a, cp, base, row_scale, t0, rank, live_tokens);
   }
   if (split > 1) cluster_sync();  // no CTA leaves while another reads its sums
   if (warp == 1) {
