@@ -122,57 +122,99 @@ struct Lanes<1> {
 };
 
 // A thread's part of a row: CH accesses of VEC elements, blockDim.x accesses apart (kFull:
-// the row fills them all). The next rows are on their way: whole 16-byte accesses go
-// through the ring, single elements wait in registers, one row ahead.
+// the row fills them all), and the ring of rows on their way. Whole 16-byte accesses: each
+// thread copies its own and reads back what it copied, without a barrier. Single elements
+// (rows off 16-byte boundaries): the group copies the 16-byte pieces that cover the row
+// and each thread takes its elements out of them, so a barrier goes before and after.
+// (The first and the last piece may reach past the row's ends, never past the aligned 16
+// bytes that hold one of its elements.)
 template <typename T, int VEC, int CH, bool kFull, int kRows>
 struct RowStream {
-  static constexpr bool kAsync = VEC > 1;
-  static constexpr int kAhead = kAsync ? kRows : 1;  // rows kept requested
-  static constexpr int kBytes = kAsync ? kAhead * CH * 16 : 0;  // of the ring, per thread
+  static constexpr bool kOwn = VEC > 1;
+  static constexpr int kAhead = kRows;  // rows kept requested
 
-  const T* next;   // this thread's first element of the next row to request
+  const T* next;   // kOwn: this thread's first element of the next row to request, else the row
   long long pitch; // elements to the one after
   int left;        // rows still to request
-  uint32_t ring;   // shared address of this thread's first access; a row's are `stride` apart
-  uint32_t stride;
-  Vec<T, VEC> ahead[kAsync ? 1 : CH];
+  uint32_t ring;   // shared address of the group's ring (kOwn: of this thread's first access)
+  uint32_t stride; // kOwn: bytes from one of a row's accesses to the next; else from row to row
+  uint32_t shift;  // !kOwn: bytes of the current row's first piece before the row
+  uint32_t turn;   // !kOwn: what the shift grows by from row to row (modulo 16)
 
+  // Shared memory of a block's ring.
+  static __host__ __device__ __forceinline__ uint32_t row_bytes(int cols) {
+    return (static_cast<uint32_t>(cols) * sizeof(T) + 15 + 15) / 16 * 16;  // any shift
+  }
+  static __host__ __device__ __forceinline__ uint32_t bytes(int cols, int threads_x, int threads_y) {
+    return kAhead * (kOwn ? CH * 16u * threads_x : row_bytes(cols)) * threads_y;
+  }
   static __device__ __forceinline__ bool inside(int i, int cols) {
     return kFull || static_cast<int>(i * blockDim.x + threadIdx.x) * VEC < cols;
   }
-  // `base`: this tensor's part of shared memory, kBytes per thread; the group takes rows
-  // first, first + step, ... below rows.
-  __device__ __forceinline__ void init(uint8_t* base, const void* p, long long ld, int first, int step, int rows) {
-    next = static_cast<const T*>(p) + first * ld + threadIdx.x * VEC;
+  // The group takes rows first, first + step, ... below rows.
+  __device__ __forceinline__ void init(uint8_t* base, const void* p, long long ld, int cols, int first, int step,
+                                       int rows) {
+    next = static_cast<const T*>(p) + first * ld;
     pitch = step * ld;
     left = first < rows ? (rows - 1 - first) / step + 1 : 0;
-    stride = 16 * blockDim.x * blockDim.y;
-    ring = static_cast<uint32_t>(__cvta_generic_to_shared(base)) + 16 * (threadIdx.y * blockDim.x + threadIdx.x);
+    ring = static_cast<uint32_t>(__cvta_generic_to_shared(base));
+    if constexpr (kOwn) {
+      next += threadIdx.x * VEC;
+      stride = 16 * blockDim.x * blockDim.y;
+      ring += 16 * (threadIdx.y * blockDim.x + threadIdx.x);
+    } else {
+      stride = row_bytes(cols);
+      ring += threadIdx.y * kAhead * stride;
+      shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(next) & 15);
+      turn = static_cast<uint32_t>(pitch * static_cast<long long>(sizeof(T))) & 15;
+    }
   }
   // Request the next row, if there is one, into ring slot `slot`.
   __device__ __forceinline__ void request(int cols, int slot) {
     if (left > 0) {
+      if constexpr (kOwn) {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        if (inside(i, cols)) {
-          if constexpr (kAsync)
-            cp_async16(ring + (slot * CH + i) * stride, next + i * blockDim.x * VEC);
-          else
-            ahead[i] = ld_once<T, VEC>(next + i * blockDim.x * VEC);
+        for (int i = 0; i < CH; ++i)
+          if (inside(i, cols)) cp_async16(ring + (slot * CH + i) * stride, next + i * blockDim.x * VEC);
+      } else {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(next);
+        const uintptr_t end = at + static_cast<uintptr_t>(cols) * sizeof(T);
+        uint32_t dst = ring + slot * stride + 16 * threadIdx.x;
+        for (uintptr_t src = (at & ~uintptr_t(15)) + 16 * threadIdx.x; src < end; src += 16 * blockDim.x) {
+          cp_async16(dst, reinterpret_cast<const void*>(src));
+          dst += 16 * blockDim.x;
         }
       }
       next += pitch;
       --left;
     }
   }
+  // After the wait for this thread's copies: the row is there for every thread.
+  __device__ __forceinline__ void arrived() const {
+    if constexpr (!kOwn) sync_group();
+  }
+  // Every thread has taken what it wants of the current row.
+  __device__ __forceinline__ void taken() const {
+    if constexpr (!kOwn) sync_group();
+  }
+  static __device__ __forceinline__ void sync_group() {
+    if (blockDim.x == 32)
+      __syncwarp();
+    else
+      __syncthreads();
+  }
+  __device__ __forceinline__ void advance() {
+    if constexpr (!kOwn) shift = (shift + turn) & 15;
+  }
   __device__ __forceinline__ Vec<T, VEC> take(int i, int slot) const {
-    if constexpr (kAsync) {
-      Vec<T, VEC> r;
+    Vec<T, VEC> r;
+    if constexpr (kOwn) {
       ld_shared16(ring + (slot * CH + i) * stride, r.w);
-      return r;
     } else {
-      return ahead[i];
+      r.v = ld_shared_elem<T>(ring + slot * stride + shift +
+                              static_cast<uint32_t>((i * blockDim.x + threadIdx.x) * sizeof(T)));
     }
+    return r;
   }
 };
 
@@ -184,10 +226,11 @@ struct ParamPart {
   static constexpr int kPer = VEC == 1 ? 1 : N / 2;                       // lanes per access
   Vec<P, N> v[CH][VEC / N];
 
-  __device__ __forceinline__ void load(const void* p, int cols, float absent) {
+  // The parameters of accesses first, first + 1, ...
+  __device__ __forceinline__ void load(const void* p, int cols, float absent, int first = 0) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * VEC;
+      const int c = ((first + i) * blockDim.x + threadIdx.x) * VEC;
 #pragma unroll
       for (int k = 0; k < VEC / N; ++k) {
         if (p != nullptr && c < cols) {
@@ -202,44 +245,46 @@ struct ParamPart {
   __device__ __forceinline__ typename L::F get(int i, int j) const { return L::get(v[i][j / kPer], j % kPer); }
 };
 
-// Forms of the kernels: kKeep holds the parameters in registers over all rows (blocks of
-// 256 threads at most), else they are read for every row (512 threads); kFull rows fill
-// every access of every thread.
+// Forms of the kernels: kKeep holds the parameters in registers over all rows, else they
+// are read for every row; kFull rows fill every access of every thread.
 template <typename T_, typename P_, int VEC_, int CH_, bool kKeep_, bool kFull_>
 struct Form {
   using T = T_;
   using P = P_;
   static constexpr int VEC = VEC_, CH = CH_;
   static constexpr bool kKeep = kKeep_, kFull = kFull_;
-  static constexpr int kQuads = kKeep ? 2 : 4;
   using L = Lanes<VEC>;
   // Rows in flight: 32760 x 5120 bf16 forward 118 us with two and 120 with three at four
   // accesses per thread, backward 182 and 175.
-  using Forward = RowStream<T, VEC, CH, kFull, (CH > 2 ? 2 : 3)>;
+  using Forward = RowStream<T, VEC, CH, kFull, (VEC > 1 && CH > 4 ? 1 : (VEC > 1 && CH > 2 ? 2 : 3))>;
   using Backward = RowStream<T, VEC, CH, kFull, 3>;
 };
 
+// Backward: kept parameters and column sums leave registers for 256 threads only.
 template <typename Fm>
-__global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_kernel(LayerNormArgs a) {
+constexpr int kGradThreads = Fm::kKeep && Fm::VEC > 1 ? 256 : 512;
+
+template <typename Fm>
+__global__ void __launch_bounds__(512) layer_norm_kernel(LayerNormArgs a) {
   using T = typename Fm::T;
   using L = typename Fm::L;
   using F = typename L::F;
   using Stream = typename Fm::Forward;
   constexpr int VEC = Fm::VEC, CH = Fm::CH, kAhead = Stream::kAhead;
   extern __shared__ __align__(16) uint8_t ring_mem[];
-  __shared__ GroupSums<1, Fm::kQuads> red;
+  __shared__ GroupSums<1, 4> red;
   const float inv = 1.0f / static_cast<float>(a.cols);
   const int step = gridDim.x * blockDim.y;
   const int first = blockIdx.x * blockDim.y + threadIdx.y;
   Stream in;
-  in.init(ring_mem, a.x, a.ldx, first, step, static_cast<int>(a.rows));
+  in.init(ring_mem, a.x, a.ldx, a.cols, first, step, static_cast<int>(a.rows));
   const int n = in.left;
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) {
     in.request(a.cols, k);
     cp_async_commit();
   }
-  ParamPart<typename Fm::P, VEC, CH> wp, bp;
+  ParamPart<typename Fm::P, VEC, Fm::kKeep ? CH : 1> wp, bp;
   if (Fm::kKeep) {
     wp.load(a.weight, a.cols, 1.0f);
     bp.load(a.bias, a.cols, 0.0f);
@@ -249,6 +294,7 @@ __global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_kernel(Layer
   int slot = 0;
   for (int k = 0; k < n; ++k) {
     cp_async_wait<kAhead - 1>();
+    in.arrived();
     F d[CH][L::N];
     F s = L::all(0.0f);
 #pragma unroll
@@ -262,8 +308,9 @@ __global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_kernel(Layer
         }
       }
     }
-    // the slot is free: this thread alone filled and read it
+    in.taken();  // the slot is free
     in.request(a.cols, slot);
+    in.advance();
     cp_async_commit();
     slot = slot + 1 == kAhead ? 0 : slot + 1;
     float sum = hsum(s);
@@ -288,17 +335,18 @@ __global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_kernel(Layer
       if (a.mean != nullptr) a.mean[row] = mean;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
-    if (!Fm::kKeep) {
-      wp.load(a.weight, a.cols, 1.0f);
-      bp.load(a.bias, a.cols, 0.0f);
-    }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       if (Stream::inside(i, a.cols)) {
+        if (!Fm::kKeep) {
+          wp.load(a.weight, a.cols, 1.0f, i);
+          bp.load(a.bias, a.cols, 0.0f, i);
+        }
+        const int k = Fm::kKeep ? i : 0;
         Vec<T, VEC> o;
 #pragma unroll
         for (int j = 0; j < L::N; ++j)
-          L::put(o, j, vfma(vmul(d[i][j], L::all(rstd)), wp.get(i, j), bp.get(i, j)));
+          L::put(o, j, vfma(vmul(d[i][j], L::all(rstd)), wp.get(k, j), bp.get(k, j)));
         st_vec(out + i * blockDim.x * VEC, o);
       }
     }
@@ -343,7 +391,7 @@ __global__ void __launch_bounds__(1024) layer_norm_long_kernel(LayerNormArgs a) 
 // The second sweep takes the row from the ring again: keeping xh and g instead cost 64
 // registers at four accesses per thread, and with them the second block on an SM.
 template <typename Fm>
-__global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_backward_kernel(LayerNormGradArgs a) {
+__global__ void __launch_bounds__(kGradThreads<Fm>) layer_norm_backward_kernel(LayerNormGradArgs a) {
   using T = typename Fm::T;
   using L = typename Fm::L;
   using F = typename L::F;
@@ -351,14 +399,14 @@ __global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_backward_ker
   constexpr int VEC = Fm::VEC, CH = Fm::CH, kAhead = Stream::kAhead;
   // the ring; after the last row, with several rows per block, [2][cols] column sums
   extern __shared__ __align__(16) uint8_t ring_mem[];
-  __shared__ GroupSums<2, Fm::kQuads> red;
+  __shared__ GroupSums<2, kGradThreads<Fm> / 128> red;
   const float inv = 1.0f / static_cast<float>(a.cols);
   const int step = gridDim.x * blockDim.y;
   const int first = blockIdx.x * blockDim.y + threadIdx.y;
   const int rows = static_cast<int>(a.rows);
   Stream xin, gin;
-  xin.init(ring_mem, a.x, a.ldx, first, step, rows);
-  gin.init(ring_mem + Stream::kBytes * blockDim.x * blockDim.y, a.dy, a.lddy, first, step, rows);
+  xin.init(ring_mem, a.x, a.ldx, a.cols, first, step, rows);
+  gin.init(ring_mem + Stream::bytes(a.cols, blockDim.x, blockDim.y), a.dy, a.lddy, a.cols, first, step, rows);
   const int n = xin.left;
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) {
@@ -369,7 +417,7 @@ __global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_backward_ker
   const float* mean_p = a.mean + first;
   const float* rstd_p = a.rstd + first;
   float mean = n > 0 ? *mean_p : 0.0f, rstd = n > 0 ? *rstd_p : 0.0f;
-  ParamPart<typename Fm::P, VEC, CH> wp;
+  ParamPart<typename Fm::P, VEC, Fm::kKeep ? CH : 1> wp;
   if (Fm::kKeep) wp.load(a.weight, a.cols, 1.0f);
   clear_sums(red);
   F dw[CH][L::N], db[CH][L::N];
@@ -386,17 +434,18 @@ __global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_backward_ker
       rstd_next = *(rstd_p += step);
     }
     cp_async_wait<kAhead - 1>();
-    if (!Fm::kKeep) wp.load(a.weight, a.cols, 1.0f);
+    xin.arrived();
     F s1 = L::all(0.0f), s2 = L::all(0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       if (Stream::inside(i, a.cols)) {
         const Vec<T, VEC> xv = xin.take(i, slot), gv = gin.take(i, slot);
+        if (!Fm::kKeep) wp.load(a.weight, a.cols, 1.0f, i);
 #pragma unroll
         for (int j = 0; j < L::N; ++j) {
           const F d = L::get(gv, j);
           const F xh = vmul(vadd(L::get(xv, j), L::all(-mean)), L::all(rstd));
-          const F g = vmul(d, wp.get(i, j));
+          const F g = vmul(d, wp.get(Fm::kKeep ? i : 0, j));
           s1 = vadd(s1, g);
           s2 = vfma(g, xh, s2);
           dw[i][j] = vfma(d, xh, dw[i][j]);
@@ -413,11 +462,12 @@ __global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_backward_ker
       for (int i = 0; i < CH; ++i) {
         if (Stream::inside(i, a.cols)) {
           const Vec<T, VEC> xv = xin.take(i, slot), gv = gin.take(i, slot);
+          if (!Fm::kKeep) wp.load(a.weight, a.cols, 1.0f, i);
           Vec<T, VEC> o;
 #pragma unroll
           for (int j = 0; j < L::N; ++j) {
             const F xh = vmul(vadd(L::get(xv, j), L::all(-mean)), L::all(rstd));
-            const F g = vmul(L::get(gv, j), wp.get(i, j));
+            const F g = vmul(L::get(gv, j), wp.get(Fm::kKeep ? i : 0, j));
             L::put(o, j, vmul(vadd(vfma(xh, c2, g), c1), L::all(rstd)));
           }
           st_vec(out_row + i * blockDim.x * VEC, o);
@@ -425,9 +475,11 @@ __global__ void __launch_bounds__(Fm::kKeep ? 256 : 512) layer_norm_backward_ker
       }
       out_row += step * a.lddx;
     }
-    // the slot is free: this thread alone filled and read it
+    xin.taken();  // the slot is free
     xin.request(a.cols, slot);
     gin.request(a.cols, slot);
+    xin.advance();
+    gin.advance();
     cp_async_commit();
     slot = slot + 1 == kAhead ? 0 : slot + 1;
     mean = mean_next;
@@ -621,14 +673,15 @@ template <typename Fm>
 cudaError_t forward_launch(const LayerNormArgs& a, dim3 block, cudaStream_t s, int num_sms) {
   auto k = layer_norm_kernel<Fm>;
   const long long groups = (a.rows + block.y - 1) / block.y;
-  const size_t smem = static_cast<size_t>(Fm::Forward::kBytes) * block.x * block.y;
+  const size_t smem = Fm::Forward::bytes(a.cols, block.x, block.y);
   int resident = 0;
   const cudaError_t e = QKVCTE_RESIDENT(k, block, smem, 1, num_sms, &resident);
   if (e != cudaSuccess) return e;
-  // Eight times the resident blocks: with rows dealt out once, the SMs that get less of the
-  // bandwidth finish last (32760 x 5120 bf16 118 us; 113, 106, 101 and 104 with 2, 4, 8
-  // and 16 times).
-  k<<<static_cast<int>(std::min<long long>(groups, 8LL * resident)), block, smem, s>>>(a);
+  // Eight times the resident blocks, but eight rows for each: with rows dealt out once, the
+  // SMs that get less of the bandwidth finish last (32760 x 5120 bf16 118 us; 113, 106, 101
+  // and 104 with 2, 4, 8 and 16 times).
+  const long long grid = std::max<long long>(resident, std::min<long long>(8LL * resident, groups / 8));
+  k<<<static_cast<int>(std::min(groups, grid)), block, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -641,20 +694,25 @@ cudaError_t forward_go(const LayerNormArgs& a, dim3 block, cudaStream_t s, int n
   return forward_launch<Form<T, P, VEC, CH, kKeep, false>>(a, block, s, num_sms);
 }
 
-// Accesses per thread: one or two for rows of up to 64 (a warp) or 256 accesses, then
-// four. More accesses per thread mean fewer warps per row, each of which pays for the
-// reductions and addresses: 5120 bf16 columns on 160 threads took 105 us for 32760 rows,
-// on 320 threads 150 us.
+// Accesses per thread: one or two for rows of up to 32 (a warp) or 256 accesses, then four,
+// eight (16 single elements) for long rows. More accesses per thread mean fewer warps per
+// row, each of which pays for the reductions and addresses: 5120 bf16 columns on 160
+// threads took 105 us for 32760 rows, on 320 threads 150 us. Rows off 16-byte boundaries
+// (16000 x 5121 bf16) take 152 us where 5120 columns take 55: every element is a shared
+// memory access and a store of its own.
 template <typename T, typename P, int VEC>
 cudaError_t forward_vec(const LayerNormArgs& a, cudaStream_t s, int num_sms) {
   dim3 block;
   const int chunks = a.cols / VEC;
   if (chunks <= 32 && pick_block(chunks, 1, 32, &block)) return forward_go<T, P, VEC, 1, true>(a, block, s, num_sms);
   if (chunks <= 256 && pick_block(chunks, 2, 256, &block)) return forward_go<T, P, VEC, 2, true>(a, block, s, num_sms);
-  if (pick_block(chunks, 4, 256, &block)) return forward_go<T, P, VEC, 4, true>(a, block, s, num_sms);
-  if (pick_block(chunks, 4, 512, &block)) return forward_go<T, P, VEC, 4, false>(a, block, s, num_sms);
-  if constexpr (VEC == 1) {
-    if (pick_block(chunks, 16, 512, &block)) return forward_go<T, P, VEC, 16, false>(a, block, s, num_sms);
+  if (chunks <= 1024 || VEC > 1) {
+    if (pick_block(chunks, 4, 512, &block)) return forward_go<T, P, VEC, 4, true>(a, block, s, num_sms);
+  }
+  if constexpr (VEC > 1) {
+    if (pick_block(chunks, 8, 512, &block)) return forward_go<T, P, VEC, 8, false>(a, block, s, num_sms);
+  } else {
+    if (pick_block(chunks, 16, 512, &block)) return forward_go<T, P, VEC, 16, true>(a, block, s, num_sms);
   }
   auto k = layer_norm_long_kernel<T, P>;
   k<<<static_cast<int>(std::min<long long>(a.rows, 2 * num_sms)), 1024, 0, s>>>(a);
@@ -688,7 +746,7 @@ cudaError_t join(const LayerNormGradArgs& a, int parts, cudaStream_t s) {
 template <typename Fm>
 cudaError_t backward_launch(const LayerNormGradArgs& a, dim3 block, cudaStream_t s, int num_sms) {
   auto k = layer_norm_backward_kernel<Fm>;
-  size_t smem = 2 * static_cast<size_t>(Fm::Backward::kBytes) * block.x * block.y;
+  size_t smem = 2 * static_cast<size_t>(Fm::Backward::bytes(a.cols, block.x, block.y));
   const bool sums = a.partial != nullptr;
   if (sums) smem = std::max(smem, 2 * sizeof(float) * static_cast<size_t>(a.cols));
   const int cluster = sums ? kGradCluster : 1;
@@ -728,10 +786,13 @@ cudaError_t backward_vec(const LayerNormGradArgs& a, cudaStream_t s, int num_sms
   const int chunks = a.cols / VEC;
   if (chunks <= 32 && pick_block(chunks, 1, 32, &block)) return backward_go<T, P, VEC, 1, true>(a, block, s, num_sms);
   if (chunks <= 256 && pick_block(chunks, 2, 256, &block)) return backward_go<T, P, VEC, 2, true>(a, block, s, num_sms);
-  if (pick_block(chunks, 4, 256, &block)) return backward_go<T, P, VEC, 4, true>(a, block, s, num_sms);
-  if (pick_block(chunks, 4, 512, &block)) return backward_go<T, P, VEC, 4, false>(a, block, s, num_sms);
-  if constexpr (VEC == 1) {
-    if (pick_block(chunks, 16, 512, &block)) return backward_go<T, P, VEC, 16, false>(a, block, s, num_sms);
+  if constexpr (VEC > 1) {
+    if (pick_block(chunks, 4, 256, &block)) return backward_go<T, P, VEC, 4, true>(a, block, s, num_sms);
+    if (pick_block(chunks, 4, 512, &block)) return backward_go<T, P, VEC, 4, false>(a, block, s, num_sms);
+  } else {
+    if (chunks <= 1024 && pick_block(chunks, 4, 512, &block))
+      return backward_go<T, P, VEC, 4, true>(a, block, s, num_sms);
+    if (pick_block(chunks, 16, 512, &block)) return backward_go<T, P, VEC, 16, true>(a, block, s, num_sms);
   }
   cudaError_t e = cudaSuccess;
   if (a.dx != nullptr) {

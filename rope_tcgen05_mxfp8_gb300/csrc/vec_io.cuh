@@ -117,6 +117,21 @@ __device__ __forceinline__ void ld_shared16(uint32_t src, uint32_t* w) {
                : "r"(src)
                : "memory");
 }
+// One element at a shared address.
+template <typename T>
+__device__ __forceinline__ T ld_shared_elem(uint32_t src) {
+  T r;
+  if constexpr (sizeof(T) == 4) {
+    uint32_t w;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(src) : "memory");
+    r = *reinterpret_cast<T*>(&w);
+  } else {
+    uint16_t w;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(src) : "memory");
+    r = *reinterpret_cast<T*>(&w);
+  }
+  return r;
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
