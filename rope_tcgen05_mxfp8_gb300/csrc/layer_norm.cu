@@ -9,10 +9,11 @@
 // variance is taken about the mean in a second sweep over the registers, never as a
 // difference of large sums. Rows come through a ring in shared memory that each thread
 // fills for itself with 16-byte asynchronous copies, two or three rows ahead, so that loads
-// stay in flight across the reductions; parameters stay in registers over all the rows
-// of a block. The backward pass keeps its column sums dw and db in the registers of the
-// same threads; one partial row per block goes to the workspace, and a second kernel
-// adds those in a fixed order (no atomics: the result does not depend on the schedule).
+// stay in flight across the reductions (rows off 16-byte boundaries: the group copies the
+// pieces that cover them); parameters stay in registers over all the rows of a block. The
+// backward pass keeps its column sums dw and db in the registers of the same threads,
+// adds those of a cluster of four blocks on chip, and a second kernel adds the clusters'
+// in a fixed order (no atomics: the result does not depend on the schedule).
 // Sums, statistics and gradients are fp32; outputs are rounded once.
 //
 // Arithmetic counts: a first form that converted each element in each sweep, read the
@@ -397,7 +398,7 @@ __global__ void __launch_bounds__(kGradThreads<Fm>) layer_norm_backward_kernel(L
   using F = typename L::F;
   using Stream = typename Fm::Backward;
   constexpr int VEC = Fm::VEC, CH = Fm::CH, kAhead = Stream::kAhead;
-  // the ring; after the last row, with several rows per block, [2][cols] column sums
+  // the ring; after the last row, [2][cols] column sums
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ GroupSums<2, kGradThreads<Fm> / 128> red;
   const float inv = 1.0f / static_cast<float>(a.cols);
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(kGradThreads<Fm>) layer_norm_backward_kernel(L
   cluster_sync();  // no block leaves while another reads its sums
 }
 
-// Rows longer than the registers: dx with two sweeps over the row ...
+// Rows longer than the registers: dx with two sweeps over the row, after ...
 template <typename T, typename P>
 __global__ void __launch_bounds__(1024) layer_norm_backward_long_kernel(LayerNormGradArgs a) {
   __shared__ GroupSums<2, 8> red;
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(1024) layer_norm_backward_long_kernel(LayerNor
   }
 }
 
-// ... and the column sums, a thread per column over a range of rows.
+// ... the column sums, a thread per column over a range of rows.
 template <typename T>
 __global__ void __launch_bounds__(256) layer_norm_columns_kernel(LayerNormGradArgs a, long long rows_per_part) {
   const int c = blockIdx.x * blockDim.x + threadIdx.x;
@@ -794,21 +795,24 @@ cudaError_t backward_vec(const LayerNormGradArgs& a, cudaStream_t s, int num_sms
       return backward_go<T, P, VEC, 4, true>(a, block, s, num_sms);
     if (pick_block(chunks, 16, 512, &block)) return backward_go<T, P, VEC, 16, true>(a, block, s, num_sms);
   }
+  // The column sums first: dx may overwrite dy or x.
   cudaError_t e = cudaSuccess;
+  int parts = 0;
+  if (a.partial != nullptr) {
+    const int strips = (a.cols + 255) / 256;
+    const long long want = std::max<long long>(1, static_cast<long long>(num_sms) * 8 / strips);
+    const long long parts0 = std::min<long long>(std::min<long long>(want, a.max_parts), a.rows);
+    const long long per = (a.rows + parts0 - 1) / parts0;
+    parts = static_cast<int>((a.rows + per - 1) / per);
+    layer_norm_columns_kernel<T><<<dim3(strips, parts), 256, 0, s>>>(a, per);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   if (a.dx != nullptr) {
     auto k = layer_norm_backward_long_kernel<T, P>;
     k<<<static_cast<int>(std::min<long long>(a.rows, 2 * num_sms)), 1024, 0, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if (a.partial == nullptr) return e;
-  const int strips = (a.cols + 255) / 256;
-  const long long want = std::max<long long>(1, static_cast<long long>(num_sms) * 8 / strips);
-  const long long parts0 = std::min<long long>(std::min<long long>(want, a.max_parts), a.rows);
-  const long long per = (a.rows + parts0 - 1) / parts0;
-  const int parts = static_cast<int>((a.rows + per - 1) / per);
-  layer_norm_columns_kernel<T><<<dim3(strips, parts), 256, 0, s>>>(a, per);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return join<P>(a, parts, s);
+  return a.partial == nullptr ? e : join<P>(a, parts, s);
 }
 
 template <typename T, typename P>

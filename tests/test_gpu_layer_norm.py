@@ -271,3 +271,28 @@ def test_binding_refusals():
         lib.qkv_cte_layer_norm(torch.zeros(64, 4, device=DEV).t())
     with pytest.raises(lib.QkvCteError):
         lib.qkv_cte_layer_norm(x, out=x[:1].expand(4, 64))
+
+
+@pytest.mark.parametrize("rows,cols", [(5, 640), (7, 333), (5, 12288), (6, 30000), (4, 9001)])
+@pytest.mark.parametrize("into", ["dy", "x"])
+def test_backward_in_place_at_every_width(rows, cols, into):
+    """dx over dy or over x: the column sums still see what was there."""
+    xt, w, _, dy = _inputs(rows, cols, torch.bfloat16, torch.float32, cols)
+    mean, rstd = _saved(xt)
+    x2, dy2 = xt.clone(), dy.clone()
+    dw, db = torch.empty_like(w), torch.empty_like(w)
+    dx, _, _ = lib.qkv_cte_layer_norm_backward(dy2, x2, mean, rstd, w, dx=dy2 if into == "dy" else x2, dweight=dw,
+                                               dbias=db)
+    _check_backward(dy, xt, mean, rstd, w, dx, dw, db)
+    assert torch.equal(x2 if into == "dy" else dy2, xt if into == "dy" else dy)
+
+
+@pytest.mark.parametrize("cols", [7, 77, 333, 1283, 5121])
+def test_forward_in_place_off_16_byte_boundaries(cols):
+    """Many rows whose 16-byte pieces they share with their neighbours."""
+    xt, w, b, _ = _inputs(3000, cols, torch.bfloat16, torch.float32, cols)
+    y, _, _ = lib.qkv_cte_layer_norm(xt, w, b)
+    _check_forward(xt, w, b, 1e-6, y, None, None)
+    z = xt.clone()
+    lib.qkv_cte_layer_norm(z, w, b, out=z)
+    assert torch.equal(z, y)
