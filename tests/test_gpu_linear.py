@@ -238,3 +238,84 @@ def test_large_offsets():
     ref, tol = c.reference()
     for t0 in (0, T // 2 // 64 * 64, T - 64):
         assert bool(((out[t0: t0 + 64].double() - ref).abs() <= tol).all())
+
+
+# K1's form of the product (more than 512 tokens, rows on 32-byte boundaries), one size for
+# each of its tile widths
+WIDE = [(700, 64, 720), (2560, 96, 1008), (4096, 64, 960)]
+
+
+@pytest.mark.parametrize("T,K,N", WIDE)
+@pytest.mark.parametrize("act", ["none", "gelu_tanh", "gelu_erf", "silu"])
+@pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("parts", ["plain", "bias", "residual", "all"])
+def test_wide_rows_epilogues(T, K, N, act, out, parts):
+    c = Case(T, K, N, act, out, gate=parts == "all", residual=parts in ("residual", "all"), col=parts == "all",
+             bias=parts != "plain")
+    op = c.op()
+    c.check(c.run(op))
+    assert op.status() == 0
+
+
+@pytest.mark.parametrize("T", [513, 768, 769, 897, 1025])
+@pytest.mark.parametrize("K", [32, 288, 416])
+@pytest.mark.parametrize("N", [16, 128, 240, 256, 496])
+def test_wide_rows_tile_edges(T, K, N):
+    c = Case(T, K, N, "none", "bf16", gate=True, residual=True)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("N", [1, 15, 17, 250, 255, 333])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_ragged_columns_in_padded_rows(N, out):
+    """Rows on 32-byte boundaries whose last 16 columns are not whole."""
+    c = Case(600, 160, N, "silu", out, gate=True, residual=True, col=True)
+    wide = torch.full((600, 352), 3.0, dtype=c.dt, device=DEV)
+    res = torch.empty_like(wide)[:, :N]
+    res.copy_(c.res)
+    y = c.run(out=wide[:, :N], residual=res)
+    c.check(y)
+    assert bool((wide[:, N:] == 3.0).all())
+    assert torch.equal(c.run(out=res, residual=res), y)
+
+
+def test_wide_rows_strided_in_place_and_broadcast_residual():
+    c = Case(900, 160, 512, "gelu_tanh", "bf16", gate=True, residual=True)
+    want = c.run()
+    c.check(want)
+    wide = torch.full((900, 640), 3.0, dtype=c.dt, device=DEV)
+    y = c.run(out=wide[:, 64: 576])
+    assert torch.equal(y, want) and bool((wide[:, :64] == 3.0).all()) and bool((wide[:, 576:] == 3.0).all())
+    z = c.res.clone()
+    assert torch.equal(c.run(out=z, residual=z), want)
+    row = c.res[:1].expand(900, 512)
+    c.check(c.run(residual=row), res=row)
+
+
+def test_wide_rows_bounded_waits_report():
+    c = Case(700, 256, 128)
+    op = c.op(flags=lib.QKV_CTE_FLAG_TEST_STALL)
+    c.run(op)
+    with pytest.raises(lib.QkvCteError) as ei:
+        op.status()
+    assert ei.value.code == lib.QKV_CTE_ERR_DEVICE_TIMEOUT
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("T,K,N", [(700, 4128, 97), (2048, 64, 1281), (5000, 160, 333), (3000, 32, 1)])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_many_tokens_off_32_byte_rows(T, K, N, out):
+    c = Case(T, K, N, "gelu_tanh", out, gate=True, residual=True)
+    c.check(c.run())
+
+
+def test_identity_weights_give_the_codes_back():
+    """W = 1 on the diagonal and scales of 2^0: every output is one code times its row scale."""
+    for T in (9, 600):
+        K = 256
+        c = Case(T, K, K, "none", "fp32", bias=False)
+        c.W = torch.zeros(K, K, dtype=torch.uint8, device=DEV)
+        c.W[torch.arange(K), torch.arange(K)] = 0x38  # 1.0
+        c.sf.fill_(127)
+        want = c.A.view(torch.float8_e4m3fn).float() * c.s[:, None]
+        assert torch.equal(c.run(), want)
