@@ -614,14 +614,27 @@ bool vec_ok(const void* p, long long ld, int cols, size_t elem, long long rows) 
 }
 
 // Blocks (or clusters) of a kernel that the current device holds at once. Asking costs
-// more than the launch, so each thread keeps the last answer per kernel; the first use of
-// a shape also raises the kernel's shared memory limit where it exceeds the 48 KB (static
-// part included) that every kernel may use.
+// more than the launch, so each thread keeps the last answer per kernel. Where a shape
+// exceeds the 48 KB (static part included) that every kernel may use, the kernel's shared
+// memory limit goes up first: always to the device's maximum, because the limit belongs to
+// the kernel on the device and other threads launch other shapes under it.
 struct Residency {
   int device = -1, threads = 0, cluster = 0;
+  int raised = -1;  // the device on which this thread last raised the limit
   size_t smem = 0;
   int count = 0;
 };
+
+template <typename K>
+cudaError_t raise_smem_limit(K kernel, int device) {
+  int most = 0;
+  cudaFuncAttributes attr;
+  cudaError_t e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, device);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, kernel);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              most - static_cast<int>(attr.sharedSizeBytes));
+}
 
 template <typename K>
 cudaError_t residency(K kernel, Residency& last, dim3 block, size_t smem, int cluster, int num_sms, int* count) {
@@ -630,9 +643,9 @@ cudaError_t residency(K kernel, Residency& last, dim3 block, size_t smem, int cl
   if (e != cudaSuccess) return e;
   const int threads = static_cast<int>(block.x * block.y);
   if (device != last.device || threads != last.threads || smem != last.smem || cluster != last.cluster) {
-    if (smem > 40 * 1024) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-      if (e != cudaSuccess) return e;
+    if (smem > 40 * 1024 && last.raised != device) {
+      if ((e = raise_smem_limit(kernel, device)) != cudaSuccess) return e;
+      last.raised = device;
     }
     int n = 0;
     if (cluster > 1) {
