@@ -104,16 +104,25 @@ def _launch(fn, device, stream, *args):
         _check(rc)
 
 
-def _kept(stream, device, *tensors):
-    """Tensors allocated here for work on another stream than the one the allocator knows
-    of: their memory is not handed out again before that work is done."""
+def _side(stream, device):
+    """The stream of a call, or None where it is `device`'s current one."""
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if handle == _raw_stream(device.index):
-        return
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=device)
-    for t in tensors:
-        if t is not None:
-            t.record_stream(s)
+        return None
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=device)
+
+
+def _empty(side, shape, dtype, device):
+    """torch.empty for what a call writes on stream `side` (None: the current one). The
+    memory is that stream's own: taken from the current one's, it could have work of the
+    current stream still to come. The caller reads the result on the current stream, which
+    the allocator is told, so that it may be dropped at any time."""
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _tensor(name: str, t, dtypes, device=None):
@@ -181,24 +190,19 @@ def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None,
         raise TypeError(f"weight and bias: dtype {pdt} is neither {dt} nor torch.float32")
     pw = _vector("weight", weight, (pdt,), dev, cols)
     pb = _vector("bias", bias, (pdt,), dev, cols)
-    made = []
+    side = None if stream is None else _side(stream, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
-        made.append(out)
+        out = _empty(side, shape, dt, dev)
         py, ldy = out.data_ptr(), cols
     else:
         py, ldy = _rows("out", out, (dt,), dev, shape)
     if stats:
         if mean is None:
-            mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-            made.append(mean)
+            mean = _empty(side, shape[:-1], torch.float32, dev)
         if rstd is None:
-            rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-            made.append(rstd)
+            rstd = _empty(side, shape[:-1], torch.float32, dev)
     pm = _vector("mean", mean, (torch.float32,), dev, rows)
     pr = _vector("rstd", rstd, (torch.float32,), dev, rows)
-    if stream is not None:
-        _kept(stream, dev, *made)
     _launch(_lib().qkv_cte_layer_norm, dev, stream, px, ldx, pw, pb, py, ldy, pm, pr, rows, cols, eps, _DTYPE[dt],
             _DTYPE[pdt])
     return out, mean, rstd
@@ -225,12 +229,11 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
     pdt = param.dtype if isinstance(param, torch.Tensor) else torch.float32
     if pdt not in (x.dtype, torch.float32):
         raise TypeError(f"weight, dweight and dbias: dtype {pdt} is neither {x.dtype} nor torch.float32")
-    made = []
+    side = None if stream is None else _side(stream, dev)
     if dx is None and dweight is None and dbias is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        dweight = torch.empty(cols, dtype=pdt, device=dev)
-        dbias = torch.empty(cols, dtype=pdt, device=dev)
-        made += [dx, dweight, dbias]
+        dx = _empty(side, x.shape, x.dtype, dev)
+        dweight = _empty(side, (cols,), pdt, dev)
+        dbias = _empty(side, (cols,), pdt, dev)
         pd, ldd, pdw, pdb = dx.data_ptr(), cols, dweight.data_ptr(), dbias.data_ptr()
     else:
         pd, ldd = _rows("dx", dx, (x.dtype,), dev, x.shape) if dx is not None else (None, 0)
@@ -242,12 +245,9 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
     ws_bytes, pws = 0, None
     if (dweight is not None or dbias is not None) and rows:
         if workspace is None:
-            workspace = torch.empty(qkv_cte_layer_norm_backward_workspace(rows, cols), dtype=torch.uint8, device=dev)
-            made.append(workspace)
+            workspace = _empty(side, (qkv_cte_layer_norm_backward_workspace(rows, cols),), torch.uint8, dev)
         ws_bytes = workspace.numel()
         pws = _vector("workspace", workspace, (torch.uint8,), dev, ws_bytes)
-    if stream is not None:
-        _kept(stream, dev, *made)
     _launch(_lib().qkv_cte_layer_norm_backward, dev, stream, pg, ldg, px, ldx, pw, pm, pr, pd, ldd, pdw, pdb, rows,
             cols, _DTYPE[x.dtype], _DTYPE[pdt], pws, ws_bytes)
     return dx, dweight, dbias
@@ -293,17 +293,13 @@ class QkvCteRopeAxes:
             raise ValueError("give positions or grids (one of them)")
         dev = where.device
         p, stride, g = self._where(batch, seq, positions, grids, dev)
-        made = []
+        side = None if stream is None or dev.type != "cuda" else _side(stream, dev)
         if cos is None:
-            cos = torch.empty(batch * seq, self.d_head, dtype=torch.float32, device=dev)
-            made.append(cos)
+            cos = _empty(side, (batch * seq, self.d_head), torch.float32, dev)
         if sin is None:
-            sin = torch.empty(batch * seq, self.d_head, dtype=torch.float32, device=dev)
-            made.append(sin)
+            sin = _empty(side, (batch * seq, self.d_head), torch.float32, dev)
         n = batch * seq * self.d_head
         pc, ps = _vector("cos", cos, (torch.float32,), dev, n), _vector("sin", sin, (torch.float32,), dev, n)
-        if stream is not None:
-            _kept(stream, dev, *made)
         _launch(_lib().qkv_cte_rope_tables, dev, stream, self.plan, batch, seq, p, stride, g, pc, ps)
         return cos, sin
 
@@ -318,9 +314,7 @@ class QkvCteRopeAxes:
         if sx[-1] != 1:
             raise ValueError("x: the last dimension must be contiguous")
         if out is None:
-            out = torch.empty(shape, dtype=dt, device=dev)
-            if stream is not None:
-                _kept(stream, dev, out)
+            out = _empty(None if stream is None else _side(stream, dev), shape, dt, dev)
         else:
             _tensor("out", out, (dt,), dev)
             if out.shape != shape:
@@ -394,9 +388,7 @@ class QkvCteLinear:
         pg = _vector("gate", gate, _BF16_BITS, dev, N)
         pr, ldr = _rows("residual", residual, (self.out_dtype,), dev, (T, N)) if residual is not None else (None, 0)
         if out is None:
-            out = torch.empty(self.shape, dtype=self.out_dtype, device=dev)
-            if stream is not None:
-                _kept(stream, dev, out)
+            out = _empty(None if stream is None else _side(stream, dev), self.shape, self.out_dtype, dev)
         po, ldo = _rows("out", out, (self.out_dtype,), dev, (T, N))
         _launch(_lib().qkv_cte_linear_run, dev, stream, self.plan, pa, ps, pw, pf, pc, pb, pg, pr, ldr, po, ldo,
                 self.workspace.data_ptr(), self.workspace.numel())
