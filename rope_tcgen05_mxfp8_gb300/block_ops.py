@@ -125,6 +125,16 @@ def _empty(side, shape, dtype, device):
     return t
 
 
+def _cleared(nbytes, device):
+    """A workspace of zeros that any stream may use at once: the fill has run when this
+    returns (within a graph capture it is part of the graph instead)."""
+    t = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.device(device):
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+    return t
+
+
 def _tensor(name: str, t, dtypes, device=None):
     """t, checked to be a CUDA tensor of one of `dtypes` (on `device`)."""
     if not isinstance(t, torch.Tensor):
@@ -354,7 +364,10 @@ class QkvCteLinear:
 
     A, a_scale, W and w_sf are the operands of QkvCte; `residual` and `out` are [T, N] of
     `out_dtype` with contiguous rows (strided rows are fine, and `out` may be `residual`).
-    Calls that overlap on the GPU need an object each: they would share the workspace.
+    Calls that overlap on the GPU need an object each: they would share the workspace. The
+    first call may run on any stream, and the object may go while its calls are pending; a
+    stream given as a raw handle has to outlive the object, and the object the graphs that
+    captured its calls. The constructor waits for the stream that is current.
     """
 
     def __init__(self, tokens: int, in_features: int, out_features: int, act: int = QKV_CTE_ACT_NONE,
@@ -372,7 +385,19 @@ class QkvCteLinear:
         if dev.index is None:
             dev = torch.device(dev.type, torch.cuda.current_device())
         self.device = dev
-        self.workspace = torch.zeros(max(self.workspace_bytes, 256), dtype=torch.uint8, device=dev)
+        self.workspace = _cleared(max(self.workspace_bytes, 256), dev)
+        self._streams = {_raw_stream(dev.index)}  # those the allocator knows to use the workspace
+
+    def _on(self, stream) -> int:
+        """The handle of the stream a call runs on, known to the workspace's allocator."""
+        if stream is None:
+            handle = _raw_stream(self.device.index)
+        else:
+            handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if handle not in self._streams:
+            self.workspace.record_stream(torch.cuda.ExternalStream(handle, device=self.device))
+            self._streams.add(handle)
+        return handle
 
     def __call__(self, A, a_scale, W, w_sf, bias=None, gate=None, residual=None, out=None, w_col_scale=None,
                  stream=None):
@@ -390,7 +415,7 @@ class QkvCteLinear:
         if out is None:
             out = _empty(None if stream is None else _side(stream, dev), self.shape, self.out_dtype, dev)
         po, ldo = _rows("out", out, (self.out_dtype,), dev, (T, N))
-        _launch(_lib().qkv_cte_linear_run, dev, stream, self.plan, pa, ps, pw, pf, pc, pb, pg, pr, ldr, po, ldo,
+        _launch(_lib().qkv_cte_linear_run, dev, self._on(stream), self.plan, pa, ps, pw, pf, pc, pb, pg, pr, ldr, po, ldo,
                 self.workspace.data_ptr(), self.workspace.numel())
         return out
 

@@ -83,3 +83,64 @@ def test_results_used_on_the_current_stream_are_kept_for_it(make):
         late = [torch.full((t.numel() * t.element_size(),), 7, dtype=torch.uint8, device=DEV) for t in want * 3]
     torch.cuda.synchronize()
     assert all(torch.equal(c, w) for c, w in zip(copies, want)) and late
+
+
+def _dirty(n):
+    """Leave n bytes of ones with the allocator."""
+    t = torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+    del t
+
+
+def _run_linear(T):
+    c = Case(T, 640, 512, "silu", "bf16")
+    size = c.op(input_layout=lib.QKV_CTE_INPUT_BF16).workspace.numel()
+    make = lambda: c.op(input_layout=lib.QKV_CTE_INPUT_BF16)  # noqa: E731
+    return make, lambda op, s: c.run(op, A=c.x, stream=s), size, c.run(make(), A=c.x)
+
+
+def _workspace_is_ready(make, run, size, want):
+    """An object made while the constructor's stream is busy, used at once on another
+    stream: its workspace already holds what the first run needs."""
+    _dirty(size)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(SPIN // 4)
+    op = make()
+    with torch.cuda.stream(s):
+        left = op.workspace.count_nonzero()
+    got = run(op, s)
+    s.synchronize()
+    assert left.item() == 0
+    assert op.status(s) == 0
+    assert torch.equal(got, want)
+    torch.cuda.synchronize()
+    assert torch.equal(run(op, None), want) and op.status() == 0
+
+
+def _workspace_outlives_its_object(make, run, size, want, current):
+    """An object dropped while its call is pending: no later tensor gets the workspace
+    before the call has run."""
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    op = make()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(SPIN)
+        got = run(op, None) if current else None
+    if not current:
+        got = run(op, s)
+    del op
+    late = [torch.full((size,), 255, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert all(bool((t == 255).all()) for t in late)
+
+
+@pytest.mark.parametrize("T", [3, 40, 700])
+def test_linear_workspace_is_ready_for_any_stream(T):
+    _workspace_is_ready(*_run_linear(T))
+
+
+@pytest.mark.parametrize("current", [False, True])
+@pytest.mark.parametrize("T", [3, 40, 700])
+def test_linear_workspace_outlives_its_object(T, current):
+    _workspace_outlives_its_object(*_run_linear(T), current)
