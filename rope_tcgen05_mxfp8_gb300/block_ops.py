@@ -14,8 +14,8 @@ from typing import Optional, Sequence
 
 import torch
 
-from .qkv_cte import (QKV_CTE_INPUT_BF16, QKV_CTE_INPUT_PACKED, QKV_CTE_INPUT_ROW_FP8, _check, load,
-                      qkv_cte_status)
+from .qkv_cte import (QKV_CTE_INPUT_BF16, QKV_CTE_INPUT_PACKED, QKV_CTE_INPUT_ROW_FP8, _check, _cleared,
+                      _current_device, _empty, _raw_stream, _side, _used_on, load, qkv_cte_status)
 
 QKV_CTE_DTYPE_BF16 = 0
 QKV_CTE_DTYPE_FP16 = 1
@@ -85,10 +85,6 @@ def _lib() -> ctypes.CDLL:
     return lib
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
-_current_device = torch._C._cuda_getDevice
-
-
 def _launch(fn, device, stream, *args):
     """fn(*args, stream) with `device` current."""
     if stream is None:
@@ -102,37 +98,6 @@ def _launch(fn, device, stream, *args):
             rc = fn(*args, handle)
     if rc:
         _check(rc)
-
-
-def _side(stream, device):
-    """The stream of a call, or None where it is `device`'s current one."""
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if handle == _raw_stream(device.index):
-        return None
-    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=device)
-
-
-def _empty(side, shape, dtype, device):
-    """torch.empty for what a call writes on stream `side` (None: the current one). The
-    memory is that stream's own: taken from the current one's, it could have work of the
-    current stream still to come. The caller reads the result on the current stream, which
-    the allocator is told, so that it may be dropped at any time."""
-    if side is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(side):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
-    return t
-
-
-def _cleared(nbytes, device):
-    """A workspace of zeros that any stream may use at once: the fill has run when this
-    returns (within a graph capture it is part of the graph instead)."""
-    t = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    with torch.cuda.device(device):
-        if not torch.cuda.is_current_stream_capturing():
-            torch.cuda.current_stream().synchronize()
-    return t
 
 
 def _tensor(name: str, t, dtypes, device=None):
@@ -388,17 +353,6 @@ class QkvCteLinear:
         self.workspace = _cleared(max(self.workspace_bytes, 256), dev)
         self._streams = {_raw_stream(dev.index)}  # those the allocator knows to use the workspace
 
-    def _on(self, stream) -> int:
-        """The handle of the stream a call runs on, known to the workspace's allocator."""
-        if stream is None:
-            handle = _raw_stream(self.device.index)
-        else:
-            handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if handle not in self._streams:
-            self.workspace.record_stream(torch.cuda.ExternalStream(handle, device=self.device))
-            self._streams.add(handle)
-        return handle
-
     def __call__(self, A, a_scale, W, w_sf, bias=None, gate=None, residual=None, out=None, w_col_scale=None,
                  stream=None):
         (T, N), K, dev = self.shape, self.in_features, self.device
@@ -415,7 +369,8 @@ class QkvCteLinear:
         if out is None:
             out = _empty(None if stream is None else _side(stream, dev), self.shape, self.out_dtype, dev)
         po, ldo = _rows("out", out, (self.out_dtype,), dev, (T, N))
-        _launch(_lib().qkv_cte_linear_run, dev, self._on(stream), self.plan, pa, ps, pw, pf, pc, pb, pg, pr, ldr, po, ldo,
+        handle = _used_on(self.workspace, self._streams, stream)
+        _launch(_lib().qkv_cte_linear_run, dev, handle, self.plan, pa, ps, pw, pf, pc, pb, pg, pr, ldr, po, ldo,
                 self.workspace.data_ptr(), self.workspace.numel())
         return out
 

@@ -203,6 +203,59 @@ def _ptr(name: str, t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
+_current_device = torch._C._cuda_getDevice
+
+
+def _side(stream, device):
+    """The stream of a call, or None where it is `device`'s current one."""
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle == _raw_stream(device.index):
+        return None
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=device)
+
+
+def _side_of(stream, t):
+    """_side for a call whose results go beside tensor t."""
+    return _side(stream, t.device) if stream is not None and t.is_cuda else None
+
+
+def _empty(side, shape, dtype, device):
+    """torch.empty for what a call writes on stream `side` (None: the current one). The
+    memory is that stream's own: taken from the current one's, it could have work of the
+    current stream still to come. The caller reads the result on the current stream, which
+    the allocator is told, so that it may be dropped at any time."""
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _cleared(nbytes, device):
+    """A workspace of zeros that any stream may use at once: the fill has run when this
+    returns (within a graph capture it is part of the graph instead)."""
+    t = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.device(t.device):
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+    return t
+
+
+def _used_on(workspace, known, stream) -> int:
+    """The handle of the stream a call on `workspace` runs on; the allocator learns of each
+    such stream once (`known`: their handles)."""
+    if stream is None:
+        handle = _raw_stream(workspace.device.index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle not in known:
+        workspace.record_stream(torch.cuda.ExternalStream(handle, device=workspace.device))
+        known.add(handle)
+    return handle
+
+
 def qkv_cte_run(plan, A, a_scale, W, w_sf, w_col_scale, bias, gamma_q, gamma_k, cos, sin, O,
                 sumsq, inv_rms, workspace, stream=None) -> int:
     """Launch the path on `stream` (torch.cuda.Stream, raw handle, or None = current stream)."""
@@ -243,8 +296,9 @@ def qkv_cte_row_quantize(X, A=None, a_scale=None, packed=None, stream=None):
     Returns (A, a_scale, packed)."""
     T, H = X.shape
     if A is None and a_scale is None and packed is None:
-        A = torch.empty(T, H, dtype=torch.uint8, device=X.device)
-        a_scale = torch.empty(T, dtype=torch.float32, device=X.device)
+        side = _side_of(stream, X)
+        A = _empty(side, (T, H), torch.uint8, X.device)
+        a_scale = _empty(side, (T,), torch.float32, X.device)
     _check(load().qkv_cte_row_quantize(_ptr("X", X), T, H, _ptr("A", A), _ptr("a_scale", a_scale),
                                        _ptr("packed", packed), _stream_handle(stream)))
     return A, a_scale, packed
@@ -253,10 +307,11 @@ def qkv_cte_row_quantize(X, A=None, a_scale=None, packed=None, stream=None):
 def qkv_cte_unpack_rows(packed, A=None, a_scale=None, stream=None):
     """Packed [T, H + 4] rows -> (A uint8 [T, H], a_scale fp32 [T])."""
     T, H = packed.shape[0], packed.shape[1] - 4
+    side = _side_of(stream, packed)
     if A is None:
-        A = torch.empty(T, H, dtype=torch.uint8, device=packed.device)
+        A = _empty(side, (T, H), torch.uint8, packed.device)
     if a_scale is None:
-        a_scale = torch.empty(T, dtype=torch.float32, device=packed.device)
+        a_scale = _empty(side, (T,), torch.float32, packed.device)
     _check(load().qkv_cte_unpack_rows(_ptr("packed", packed), T, H, _ptr("A", A), _ptr("a_scale", a_scale),
                                       _stream_handle(stream)))
     return A, a_scale
@@ -269,7 +324,7 @@ def qkv_cte_interleaved_to_rotate_half(src, n_q_heads, n_kv_heads, d_head, dst=N
     if not (src.is_cuda and src.is_contiguous()):
         raise ValueError("src: must be a contiguous CUDA tensor")
     if dst is None:
-        dst = torch.empty_like(src)
+        dst = _empty(_side_of(stream, src), src.shape, src.dtype, src.device)
     if not (dst.is_cuda and dst.is_contiguous()) or dst.numel() * dst.element_size() != src.numel() * src.element_size():
         raise ValueError("dst: must be a contiguous CUDA tensor of src's size")
     rows = src.shape[0] if src.dim() > 0 else 0
@@ -337,6 +392,10 @@ class QkvCte:
 
     >>> op = QkvCte(tokens=T, hidden=H, n_q_heads=40, n_kv_heads=40, d_head=128)
     >>> op(A, a_scale, W, w_sf, bias, gamma_q, gamma_k, cos, sin, out=O)
+
+    The first call may run on any stream, and the object may go while its calls are
+    pending; a stream given as a raw handle has to outlive the object, and the object the
+    graphs that captured its calls. The constructor waits for the stream that is current.
     """
 
     def __init__(self, tokens, hidden, n_q_heads, n_kv_heads, d_head, norm=1, rope=1, eps=1e-6,
@@ -349,7 +408,8 @@ class QkvCte:
         self.info = qkv_cte_get_plan_info(self.plan)
         self.width = (n_q_heads + 2 * n_kv_heads) * d_head
         dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
-        self.workspace = torch.zeros(max(self.workspace_bytes, 256), dtype=torch.uint8, device=dev)
+        self.workspace = _cleared(max(self.workspace_bytes, 256), dev)
+        self._streams = {_raw_stream(self.workspace.device.index)}  # those the allocator knows to use the workspace
 
     def plan_info(self) -> qkv_cte_plan_info:
         """The plan's choices."""
@@ -358,11 +418,12 @@ class QkvCte:
     def __call__(self, A, a_scale, W, w_sf, bias, gamma_q, gamma_k, cos, sin, out=None,
                  w_col_scale=None, sumsq=None, inv_rms=None, stream=None):
         if out is None:
+            shape = (self.desc.tokens, self.width)
             if self.desc.output_layout == QKV_CTE_LAYOUT_NBSD:
                 d = self.desc.d_head
-                out = torch.empty(self.width // d, self.desc.tokens, d, dtype=torch.bfloat16, device=A.device)
-            else:
-                out = torch.empty(self.desc.tokens, self.width, dtype=torch.bfloat16, device=A.device)
+                shape = (self.width // d, self.desc.tokens, d)
+            out = _empty(_side_of(stream, A), shape, torch.bfloat16, A.device)
+        _used_on(self.workspace, self._streams, stream)
         qkv_cte_run(self.plan, A, a_scale, W, w_sf, w_col_scale, bias, gamma_q, gamma_k, cos, sin, out,
                     sumsq, inv_rms, self.workspace, stream)
         return out
@@ -372,8 +433,9 @@ class QkvCte:
         """qkv_cte_run_host with a scratch buffer kept per chunk size."""
         n = qkv_cte_host_scratch_bytes(self.plan, chunk_rows)
         if getattr(self, "_host_scratch", None) is None or self._host_scratch.numel() < max(n, 256):
-            dev = self.workspace.device
-            self._host_scratch = torch.zeros(max(n, 256), dtype=torch.uint8, device=dev)
+            self._host_scratch = _cleared(max(n, 256), self.workspace.device)
+            self._host_streams = {_raw_stream(self.workspace.device.index)}
+        _used_on(self._host_scratch, self._host_streams, stream)
         qkv_cte_run_host(self.plan, A_host, a_scale_host, W, w_sf, w_col_scale, bias, gamma_q, gamma_k, cos, sin,
                          O_host, sumsq, inv_rms, self._host_scratch, chunk_rows, stream)
         return O_host
