@@ -116,15 +116,28 @@ def _tensor(name: str, t, dtypes, device=None):
 # The checks below test what is right first, with as few calls into torch as will do (a
 # small kernel's call is bound by the host), and look for what is wrong afterwards.
 
-def _vector(name: str, t, dtypes, device, n: int) -> Optional[int]:
-    """Address of a contiguous tensor of n elements, or None."""
+def _vector(name: str, t, dtypes, device, n: int, last: int = 1) -> Optional[int]:
+    """Address of a contiguous tensor of n elements, or None. `last`: the length of the last
+    dimension of a tensor that is not flat (unless its order cannot matter)."""
     if t is None:
         return None
     if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == device and t.numel() == n
-            and t.is_contiguous()):
+            and t.is_contiguous() and (last == 1 or n == last or t.dim() == 1 or t.shape[-1] == last)):
         return t.data_ptr()
     _tensor(name, t, dtypes, device)
-    raise ValueError(f"{name}: must be contiguous with {n} elements, got shape {tuple(t.shape)}")
+    rows = f" in rows of {last}" if last != 1 else ""
+    raise ValueError(f"{name}: must be contiguous with {n} elements{rows}, got shape {tuple(t.shape)}")
+
+
+def _statistic(name: str, t, device, lead, rows: int) -> Optional[int]:
+    """Address of an fp32 value per row of a tensor with leading dimensions `lead`, or None.
+    Several dimensions have to be `lead`'s (dimensions of one element aside)."""
+    p = _vector(name, t, (torch.float32,), device, rows)
+    if p is None or len(lead) < 2 or t.dim() < 2 or t.shape == lead:
+        return p
+    if [v for v in t.shape if v != 1] != [v for v in lead if v != 1]:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} is neither {tuple(lead)} nor flat")
+    return p
 
 
 def _rows(name: str, t, dtypes, device=None, shape=None):
@@ -176,8 +189,8 @@ def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None,
             mean = _empty(side, shape[:-1], torch.float32, dev)
         if rstd is None:
             rstd = _empty(side, shape[:-1], torch.float32, dev)
-    pm = _vector("mean", mean, (torch.float32,), dev, rows)
-    pr = _vector("rstd", rstd, (torch.float32,), dev, rows)
+    pm = _statistic("mean", mean, dev, shape[:-1], rows)
+    pr = _statistic("rstd", rstd, dev, shape[:-1], rows)
     _launch(_lib().qkv_cte_layer_norm, dev, stream, px, ldx, pw, pb, py, ldy, pm, pr, rows, cols, eps, _DTYPE[dt],
             _DTYPE[pdt])
     return out, mean, rstd
@@ -215,8 +228,8 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
         pdw = _vector("dweight", dweight, (pdt,), dev, cols)
         pdb = _vector("dbias", dbias, (pdt,), dev, cols)
     pw = _vector("weight", weight, (pdt,), dev, cols)
-    pm = _vector("mean", mean, (torch.float32,), dev, rows)
-    pr = _vector("rstd", rstd, (torch.float32,), dev, rows)
+    pm = _statistic("mean", mean, dev, x.shape[:-1], rows)
+    pr = _statistic("rstd", rstd, dev, x.shape[:-1], rows)
     ws_bytes, pws = 0, None
     if (dweight is not None or dbias is not None) and rows:
         if workspace is None:
@@ -238,7 +251,7 @@ class QkvCteRopeAxes:
 
     A row stands either at positions[s] (int32 [S, axes], or [B, S, axes]) or at the s-th
     point of its batch's grid (grids: int32 [B, axes], last axis fastest; rows behind the
-    grid's end are padding and not rotated).
+    grid's end are padding and not rotated). Flat tensors in that order are taken too.
     """
 
     def __init__(self, d_head: int, axis_dims: Sequence[int], theta: float = 10000.0,
@@ -255,10 +268,12 @@ class QkvCteRopeAxes:
         if (positions is None) == (grids is None):
             raise ValueError("give positions or grids (one of them)")
         if grids is not None:
-            return None, 0, _vector("grids", grids, (torch.int32,), device, batch * self.n_axes)
+            return None, 0, _vector("grids", grids, (torch.int32,), device, batch * self.n_axes, self.n_axes)
         one = seq * self.n_axes
         per_batch = isinstance(positions, torch.Tensor) and positions.dim() == 3
-        p = _vector("positions", positions, (torch.int32,), device, one * batch if per_batch else one)
+        if per_batch and positions.shape[:2] != (batch, seq):
+            raise ValueError(f"positions: shape {tuple(positions.shape)} is not {(batch, seq, self.n_axes)}")
+        p = _vector("positions", positions, (torch.int32,), device, one * batch if per_batch else one, self.n_axes)
         return p, one if per_batch else 0, None
 
     def tables(self, batch: int, seq: int, positions=None, grids=None, cos=None, sin=None, stream=None):
@@ -266,15 +281,15 @@ class QkvCteRopeAxes:
         where = grids if grids is not None else positions
         if not isinstance(where, torch.Tensor):
             raise ValueError("give positions or grids (one of them)")
-        dev = where.device
+        dev = _tensor("positions and grids", where, (torch.int32,)).device
         p, stride, g = self._where(batch, seq, positions, grids, dev)
-        side = None if stream is None or dev.type != "cuda" else _side(stream, dev)
+        side = None if stream is None else _side(stream, dev)
         if cos is None:
             cos = _empty(side, (batch * seq, self.d_head), torch.float32, dev)
         if sin is None:
             sin = _empty(side, (batch * seq, self.d_head), torch.float32, dev)
-        n = batch * seq * self.d_head
-        pc, ps = _vector("cos", cos, (torch.float32,), dev, n), _vector("sin", sin, (torch.float32,), dev, n)
+        n, d = batch * seq * self.d_head, self.d_head
+        pc, ps = _vector("cos", cos, (torch.float32,), dev, n, d), _vector("sin", sin, (torch.float32,), dev, n, d)
         _launch(_lib().qkv_cte_rope_tables, dev, stream, self.plan, batch, seq, p, stride, g, pc, ps)
         return cos, sin
 
@@ -327,7 +342,8 @@ class QkvCteLinear:
     >>> h = op(x, None, W, w_sf, bias=b)
     >>> x = out_proj(A, a_scale, W, w_sf, bias=b, gate=g, residual=x, out=x)
 
-    A, a_scale, W and w_sf are the operands of QkvCte; `residual` and `out` are [T, N] of
+    A [T, K], a_scale [T], W [N, K] and w_sf [N, K/32] are the operands of QkvCte (flat, or
+    with more leading dimensions: the last one counts); `residual` and `out` are [T, N] of
     `out_dtype` with contiguous rows (strided rows are fine, and `out` may be `residual`).
     Calls that overlap on the GPU need an object each: they would share the workspace. The
     first call may run on any stream, and the object may go while its calls are pending; a
@@ -347,8 +363,10 @@ class QkvCteLinear:
         self.shape, self.in_features, self.out_dtype, self.input_layout = (
             (tokens, out_features), in_features, out_dtype, input_layout)
         dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if dev.type != "cuda":
+            raise ValueError(f"device: {dev} is not a CUDA device")
         if dev.index is None:
-            dev = torch.device(dev.type, torch.cuda.current_device())
+            dev = torch.device("cuda", torch.cuda.current_device())
         self.device = dev
         self.workspace = _cleared(max(self.workspace_bytes, 256), dev)
         self._streams = {_raw_stream(dev.index)}  # those the allocator knows to use the workspace
@@ -357,11 +375,11 @@ class QkvCteLinear:
                  stream=None):
         (T, N), K, dev = self.shape, self.in_features, self.device
         layout = self.input_layout
-        pa = _vector("A", A, _BF16_BITS if layout == QKV_CTE_INPUT_BF16 else (torch.uint8,), dev,
-                     T * (K + 4 if layout == QKV_CTE_INPUT_PACKED else K))
+        row = K + 4 if layout == QKV_CTE_INPUT_PACKED else K
+        pa = _vector("A", A, _BF16_BITS if layout == QKV_CTE_INPUT_BF16 else (torch.uint8,), dev, T * row, row)
         ps = _vector("a_scale", a_scale, (torch.float32,), dev, T)
-        pw = _vector("W", W, (torch.uint8,), dev, N * K)
-        pf = _vector("w_sf", w_sf, (torch.uint8,), dev, N * (K // 32))
+        pw = _vector("W", W, (torch.uint8,), dev, N * K, K)
+        pf = _vector("w_sf", w_sf, (torch.uint8,), dev, N * (K // 32), K // 32)
         pc = _vector("w_col_scale", w_col_scale, (torch.float32,), dev, N)
         pb = _vector("bias", bias, _BF16_BITS, dev, N)
         pg = _vector("gate", gate, _BF16_BITS, dev, N)

@@ -1,0 +1,83 @@
+"""Calls of the block operators that must be refused."""
+import pytest
+import torch
+
+import rope_tcgen05_mxfp8_gb300 as lib
+from test_gpu_linear import Case
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def test_transposed_positions_and_grids_are_refused():
+    rope = lib.QkvCteRopeAxes(24, (8, 8, 8))
+    x = torch.randn(2, 10, 4, 24, device=DEV)
+    pos = torch.randint(0, 50, (10, 3), device=DEV, dtype=torch.int32)
+    both = torch.stack([pos, pos + 1])
+    want = rope(x, positions=pos)
+    assert torch.equal(rope(x, positions=pos.reshape(-1)), want)             # flat
+    assert not torch.equal(rope(x, positions=both), want)
+    grid = torch.tensor([[2, 5, 1], [3, 2, 1]], dtype=torch.int32, device=DEV)
+    assert torch.equal(rope(x, grids=grid.reshape(-1)), rope(x, grids=grid))
+    for bad in (dict(positions=pos.t().contiguous()), dict(positions=both.transpose(0, 1).contiguous()),
+                dict(positions=both.transpose(1, 2).contiguous()), dict(positions=pos.reshape(1, 30)),
+                dict(grids=grid.t().contiguous())):
+        with pytest.raises(ValueError):
+            rope(x, **bad)
+        with pytest.raises(ValueError):
+            rope.tables(2, 10, **bad)
+    n = (20, 24)
+    for bad in (torch.empty(24, 20, device=DEV), torch.empty(10, 48, device=DEV)):
+        with pytest.raises(ValueError):
+            rope.tables(2, 10, positions=pos, cos=bad, sin=torch.empty(n, device=DEV))
+        with pytest.raises(ValueError):
+            rope.tables(2, 10, positions=pos, cos=torch.empty(n, device=DEV), sin=bad)
+
+
+def test_transposed_operands_of_the_product_are_refused():
+    c = Case(6, 64, 96)
+    op = c.op()
+    want = c.run(op)
+    lead = op(c.A.view(2, 3, 64), c.s.view(2, 3), c.W.view(4, 24, 64), c.sf.view(4, 24, 2), bias=c.bias)
+    assert torch.equal(lead, want)                                            # leading dimensions
+    assert torch.equal(op(c.A.reshape(-1), c.s, c.W.reshape(-1), c.sf.reshape(-1), bias=c.bias), want)
+    for kw in (dict(A=c.A.t().contiguous()), dict(W=c.W.t().contiguous()), dict(w_sf=c.sf.t().contiguous())):
+        a = dict(dict(A=c.A, W=c.W, w_sf=c.sf), **kw)
+        with pytest.raises(ValueError):
+            op(a["A"], c.s, a["W"], a["w_sf"], bias=c.bias)
+    packed = torch.cat([c.A, c.s.view(torch.uint8).view(6, 4)], dim=1).contiguous()
+    pop = c.op(input_layout=lib.QKV_CTE_INPUT_PACKED)
+    assert torch.equal(pop(packed, None, c.W, c.sf, bias=c.bias), want)
+    with pytest.raises(ValueError):
+        pop(packed.t().contiguous(), None, c.W, c.sf, bias=c.bias)
+
+
+def test_reordered_statistics_are_refused():
+    x = torch.randn(2, 3, 64, device=DEV)
+    y, mean, rstd = lib.qkv_cte_layer_norm(x, stats=True)
+    want = lib.qkv_cte_layer_norm_backward(y, x, mean, rstd)
+    for m, r in ((mean.reshape(-1), rstd.reshape(-1)), (mean[..., None], rstd[..., None])):
+        assert all(torch.equal(a, b) for a, b in zip(lib.qkv_cte_layer_norm_backward(y, x, m, r), want))
+    flat = lib.qkv_cte_layer_norm_backward(y.view(6, 64), x.view(6, 64), mean, rstd)
+    assert torch.equal(flat[0].view(2, 3, 64), want[0])
+    bad = torch.empty(3, 2, device=DEV)
+    with pytest.raises(ValueError):
+        lib.qkv_cte_layer_norm(x, mean=bad, rstd=rstd)
+    with pytest.raises(ValueError):
+        lib.qkv_cte_layer_norm(x, mean=mean, rstd=bad)
+    with pytest.raises(ValueError):
+        lib.qkv_cte_layer_norm_backward(y, x, bad, rstd)
+    with pytest.raises(ValueError):
+        lib.qkv_cte_layer_norm_backward(y, x, mean, bad)
+
+
+def test_host_positions_and_devices_are_refused():
+    rope = lib.QkvCteRopeAxes(24, (8, 8, 8))
+    pos = torch.zeros(10, 3, dtype=torch.int32)
+    for stream in (None, torch.cuda.Stream()):
+        with pytest.raises(ValueError, match="CUDA"):
+            rope.tables(1, 10, positions=pos, stream=stream)
+        with pytest.raises(ValueError, match="CUDA"):
+            rope.tables(1, 10, grids=pos[:1], stream=stream)
+    with pytest.raises(ValueError, match="CUDA"):
+        lib.QkvCteLinear(4, 64, 32, device="cpu")
