@@ -14,8 +14,8 @@ from typing import Optional, Sequence
 
 import torch
 
-from .qkv_cte import (QKV_CTE_INPUT_BF16, QKV_CTE_INPUT_PACKED, QKV_CTE_INPUT_ROW_FP8, _check, _cleared,
-                      _current_device, _empty, _raw_stream, _side, _used_on, load, qkv_cte_status)
+from .qkv_cte import (QKV_CTE_ERR_UNSUPPORTED, QKV_CTE_INPUT_BF16, QKV_CTE_INPUT_PACKED,
+                      QKV_CTE_INPUT_ROW_FP8, QkvCteError, _check, _cleared, _current_device, _empty, _raw_stream, _side, _used_on, load, qkv_cte_status)
 
 QKV_CTE_DTYPE_BF16 = 0
 QKV_CTE_DTYPE_FP16 = 1
@@ -83,6 +83,13 @@ def _lib() -> ctypes.CDLL:
     lib.qkv_cte_linear_destroy.restype = None
     _bound = lib
     return lib
+
+
+def _fits(name: str, v, bits: int = 31):
+    """v, refused where ctypes would cut it down to the C type's width without a word."""
+    if not -1 << bits <= v < 1 << bits:
+        raise QkvCteError(QKV_CTE_ERR_UNSUPPORTED, f"{name} {v} does not fit {bits + 1} bits")
+    return v
 
 
 def _launch(fn, device, stream, *args):
@@ -170,7 +177,7 @@ def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None,
     `out` may be x."""
     px, ldx = _rows("x", x, _DTYPE)
     dev, shape, dt = x.device, x.shape, x.dtype
-    cols = shape[-1]
+    cols = _fits("cols", shape[-1])
     rows = x.numel() // cols if cols else 0
     param = weight if weight is not None else bias
     pdt = param.dtype if isinstance(param, torch.Tensor) else dt
@@ -200,7 +207,7 @@ def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None,
 def qkv_cte_layer_norm_backward_workspace(rows: int, cols: int) -> int:
     """Workspace bytes of qkv_cte_layer_norm_backward (a function of the sizes alone)."""
     n = ctypes.c_size_t()
-    _check(_lib().qkv_cte_layer_norm_backward_workspace(rows, cols, ctypes.byref(n)))
+    _check(_lib().qkv_cte_layer_norm_backward_workspace(_fits("rows", rows, 63), _fits("cols", cols), ctypes.byref(n)))
     return n.value
 
 
@@ -210,7 +217,7 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
     none given, all three allocated here (dweight and dbias of weight's type, fp32 without
     a weight). mean, rstd: the forward pass's statistics. dx may be dy or x."""
     px, ldx = _rows("x", x, _DTYPE)
-    dev, cols = x.device, x.shape[-1]
+    dev, cols = x.device, _fits("cols", x.shape[-1])
     rows = x.numel() // cols if cols else 0
     pg, ldg = _rows("dy", dy, (x.dtype,), dev, x.shape)
     param = weight if weight is not None else dweight if dweight is not None else dbias
@@ -257,7 +264,9 @@ class QkvCteRopeAxes:
     def __init__(self, d_head: int, axis_dims: Sequence[int], theta: float = 10000.0,
                  spectrum: int = QKV_CTE_ROPE_PER_AXIS, pairing: int = QKV_CTE_ROPE_ROTATE_HALF):
         self.plan = None
-        dims = [int(v) for v in axis_dims]
+        dims = [_fits("axis_dims", int(v)) for v in axis_dims]
+        for name, v in (("d_head", d_head), ("spectrum", spectrum), ("pairing", pairing)):
+            _fits(name, v)
         desc = qkv_cte_rope_desc(d_head, len(dims), (ctypes.c_int32 * 4)(*dims[:4]), spectrum, pairing, theta)
         plan = ctypes.c_void_p()
         _check(_lib().qkv_cte_rope_plan(ctypes.byref(plan), ctypes.byref(desc)))
@@ -313,7 +322,7 @@ class QkvCteRopeAxes:
         if sy[-1] != 1:
             raise ValueError("out: the last dimension must be contiguous")
         batch, bx, by = (shape[0], sx[0], sy[0]) if len(shape) == 4 else (1, 0, 0)
-        seq, heads = shape[-3], shape[-2]
+        seq, heads = shape[-3], _fits("heads", shape[-2])
         p, stride, g = self._where(batch, seq, positions, grids, dev)
         _launch(_lib().qkv_cte_rope_apply, dev, stream, self.plan, x.data_ptr(), bx, sx[-3], sx[-2], out.data_ptr(),
                 by, sy[-3], sy[-2], batch, seq, heads, p, stride, g, _DTYPE[dt], 1 if inverse else 0)
@@ -356,6 +365,10 @@ class QkvCteLinear:
         self.plan = None
         if out_dtype not in _DTYPE:
             raise TypeError(f"out_dtype: {out_dtype} not in {tuple(_DTYPE)}")
+        _fits("tokens", tokens, 63)
+        for name, v in (("in_features", in_features), ("out_features", out_features), ("act", act),
+                        ("input_layout", input_layout), ("flags", flags)):
+            _fits(name, v)
         desc = qkv_cte_linear_desc(tokens, in_features, out_features, act, _DTYPE[out_dtype], input_layout, flags)
         plan, n = ctypes.c_void_p(), ctypes.c_size_t()
         _check(_lib().qkv_cte_linear_plan(ctypes.byref(plan), ctypes.byref(desc), ctypes.byref(n)))

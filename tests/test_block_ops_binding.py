@@ -30,3 +30,19 @@ def test_binding_refuses_transposed_shapes():
     assert one._where(1, 10, torch.zeros(1, 10, **i32), None, host)[1] == 0
     with pytest.raises(ValueError, match="CUDA"):
         rope.tables(1, 10, positions=torch.zeros(10, 3, **i32))
+
+
+def test_numbers_beyond_the_c_types_are_refused():
+    """ctypes keeps the low 32 bits of a number: 2^32 + 64 columns are not 64."""
+    big = 2 ** 32
+    calls = [lambda: pkg.qkv_cte_layer_norm_backward_workspace(8, big + 64),
+             lambda: pkg.qkv_cte_layer_norm_backward_workspace(2 ** 64 + 8, 64),
+             lambda: pkg.QkvCteRopeAxes(big + 8, (8,)), lambda: pkg.QkvCteRopeAxes(8, (big + 8,)),
+             lambda: pkg.QkvCteRopeAxes(8, (8,), spectrum=big), lambda: pkg.QkvCteRopeAxes(8, (8,), pairing=-big),
+             lambda: pkg.QkvCteLinear(4, big + 64, 32), lambda: pkg.QkvCteLinear(4, 64, big + 32),
+             lambda: pkg.QkvCteLinear(2 ** 64 + 4, 64, 32), lambda: pkg.QkvCteLinear(4, 64, 32, act=big),
+             lambda: pkg.QkvCteLinear(4, 64, 32, flags=big), lambda: pkg.QkvCteLinear(4, 64, 32, input_layout=big)]
+    for call in calls:
+        with pytest.raises(pkg.QkvCteError) as ei:
+            call()
+        assert ei.value.code == pkg.QKV_CTE_ERR_UNSUPPORTED

@@ -81,3 +81,12 @@ def test_host_positions_and_devices_are_refused():
             rope.tables(1, 10, grids=pos[:1], stream=stream)
     with pytest.raises(ValueError, match="CUDA"):
         lib.QkvCteLinear(4, 64, 32, device="cpu")
+
+
+def test_more_columns_than_32_bits_are_refused():
+    """2^32 + 64 columns are not 64."""
+    x = torch.zeros(1, 2 ** 32 + 64, device=DEV, dtype=torch.bfloat16)
+    with pytest.raises((ValueError, lib.QkvCteError)):
+        lib.qkv_cte_layer_norm(x, out=x)
+    with pytest.raises((ValueError, lib.QkvCteError)):
+        lib.qkv_cte_layer_norm_backward(x, x, torch.zeros(1, device=DEV), torch.ones(1, device=DEV), dx=x)
