@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kQuantThreads, 10) row_quantize_kernel(const u
   const int chunks = H >> 3;  // 8 bf16 = 16 bytes per chunk
   const uint64_t once = policy_evict_first();
   int parity = 0;
-  for (int row = blockIdx.x; row < T; row += gridDim.x, parity ^= 1) {
+  for (long long row = blockIdx.x; row < T; row += gridDim.x, parity ^= 1) {  // (row + grid may pass 2^31)
     const uint16_t* xr = X + static_cast<size_t>(row) * H;
     uint4 v[kRegChunks];
     uint32_t m2 = 0;
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) unpack_rows_kernel(const uint8_t* __
   const int n_warps = static_cast<int>((gridDim.x * static_cast<unsigned>(kThreads)) >> 5);
   const int chunks = H >> 4;
   const uint64_t once = policy_evict_first();
-  for (int row = warp; row < T; row += n_warps) {
+  for (long long row = warp; row < T; row += n_warps) {
     const uint8_t* pr = packed + static_cast<size_t>(row) * (H + 4);
     uint8_t* cr = codes + static_cast<size_t>(row) * H;
     for (int c0 = 0; c0 < chunks; c0 += 4 * 32) {
@@ -220,7 +220,7 @@ cudaError_t launch_unpack_rows(const uint8_t* packed, int T, int H, uint8_t* cod
   if (T <= 0) return cudaSuccess;
   const int rows_per_block = kThreads / 32;
   int grid = resident_blocks(unpack_rows_kernel, kThreads, num_sms);
-  grid = min(grid, (T + rows_per_block - 1) / rows_per_block);
+  grid = min(grid, (T - 1) / rows_per_block + 1);
   unpack_rows_kernel<<<grid, kThreads, 0, s>>>(packed, T, H, codes, scale);
   return cudaGetLastError();
 }
