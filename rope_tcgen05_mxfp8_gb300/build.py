@@ -22,7 +22,7 @@ LIB = os.path.join(LIBDIR, "libqkvcte.so")
 
 SOURCES = ["qkv_cte_api.cu", "qkv_gemm_mxf8.cu", "qkv_gemm_mxf8_head.cu", "qkv_gemm_mxf8_stats.cu", "qkv_gemm_mxf8_fused.cu", "qk_norm_rope.cu", "row_quant.cu", "rope_permute.cu",
            "layer_norm.cu", "rope_axes.cu", "linear_api.cu", "qkv_gemm_mxf8_linear.cu",
-           "linear_few.cu", "block_ops_api.cu"]
+           "qkv_gemm_mxf8_linear_f32.cu", "linear_few.cu", "block_ops_api.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "qkv_gemm_mxf8.cuh", "qk_norm_rope.cuh", "fp32x2.cuh", "kernel_kinds.cuh", "api_common.h",
            "block_ops.h", "vec_io.cuh", "linear_epilogue.cuh"]
 

@@ -268,9 +268,12 @@ cudaError_t launch_gemm(const GemmShape& g, const CUtensorMap& tmA, const CUtens
 // (qkv_gemm_mxf8_head.cu); launch_gemm calls it when a.head_norm or a.stats_kind is set.
 cudaError_t launch_gemm_head(const GemmShape& g, const CUtensorMap& tmA, const CUtensorMap& tmW,
                              const CUtensorMap& tmSF, const GemmArgs& a, cudaStream_t s, int num_sms);
-// K1 (CTA-pair form) with the product's epilogue (qkv_gemm_mxf8_linear.cu).
+// K1 (CTA-pair form) with the product's epilogue (qkv_gemm_mxf8_linear.cu), and its fp32
+// outputs' (qkv_gemm_mxf8_linear_f32.cu), which the first calls.
 cudaError_t launch_gemm_linear(const GemmShape& g, const CUtensorMap& tmA, const CUtensorMap& tmW,
                                const CUtensorMap& tmSF, const GemmArgs& a, cudaStream_t s, int num_sms);
+cudaError_t launch_gemm_linear_f32(const GemmShape& g, const CUtensorMap& tmA, const CUtensorMap& tmW,
+                                   const CUtensorMap& tmSF, const GemmArgs& a, cudaStream_t s, int num_sms);
 // The product's channel-major form: token tiles of 16, 32, 64 or 128; tmA boxes
 // of token_tile rows, tmW boxes of 128. After a producer step it is launched as its
 // programmatic dependent.

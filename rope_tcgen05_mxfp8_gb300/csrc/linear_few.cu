@@ -95,10 +95,10 @@ struct ChannelParams {
   }
 };
 
-template <int kBatch, int kAct>
+template <int kBatch, int kAct, bool kFull>
 __device__ __forceinline__ void activate(float2 (&v)[kBatch]) {
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) v[u] = make_float2(apply_act(v[u].x, kAct), apply_act(v[u].y, kAct));
+  for (int u = 0; u < kBatch; ++u) v[u] = make_float2(apply_act<kFull>(v[u].x, kAct), apply_act<kFull>(v[u].y, kAct));
 }
 
 // Tokens t, t + step, ... (kBatch of them, those below `live`) of the tile: the sum of
@@ -160,10 +160,11 @@ __device__ __forceinline__ void finish_tokens(const LinearFewArgs& a, const Chan
     v[u].x = fmaf(v[u].x, s * cp.col[0], cp.bias[0]);
     v[u].y = fmaf(v[u].y, s * cp.col[1], cp.bias[1]);
   }
+  constexpr bool kFull = sizeof(T) == 4;
   switch (e.act) {  // one uniform branch for the batch
-    case QKV_CTE_ACT_GELU_TANH: activate<kBatch, QKV_CTE_ACT_GELU_TANH>(v); break;
-    case QKV_CTE_ACT_GELU_ERF: activate<kBatch, QKV_CTE_ACT_GELU_ERF>(v); break;
-    case QKV_CTE_ACT_SILU: activate<kBatch, QKV_CTE_ACT_SILU>(v); break;
+    case QKV_CTE_ACT_GELU_TANH: activate<kBatch, QKV_CTE_ACT_GELU_TANH, kFull>(v); break;
+    case QKV_CTE_ACT_GELU_ERF: activate<kBatch, QKV_CTE_ACT_GELU_ERF, kFull>(v); break;
+    case QKV_CTE_ACT_SILU: activate<kBatch, QKV_CTE_ACT_SILU, kFull>(v); break;
     default: break;
   }
   T* out = static_cast<T*>(e.out) + static_cast<long long>(t0 + t) * e.ldo + n;

@@ -1,6 +1,6 @@
 // Kernel K1 templates, instantiated by qkv_gemm_mxf8.cu (plain epilogue),
-// qkv_gemm_mxf8_head.cu (per-head qk-norm epilogue) and qkv_gemm_mxf8_linear.cu (the
-// product's epilogue: bias, activation, gate, residual).
+// qkv_gemm_mxf8_head.cu (per-head qk-norm epilogue), qkv_gemm_mxf8_linear.cu and
+// qkv_gemm_mxf8_linear_f32.cu (the product's epilogue: bias, activation, gate, residual).
 //
 // Kernel K1: O = dequant(A_fp8 @ W_fp8^T) * a_scale[t] * w_col_scale[i] + bias[i] -> bf16,
 // plus the per-token sum of o^2 over the Q and the K columns.
@@ -468,7 +468,7 @@ __device__ __forceinline__ void epilogue_drain_plain(const GemmShape& g, const G
   }
 }
 
-// Epilogue of the product (kEpiLinear). What a tile needs beside its accumulator is
+// Epilogue of the product (kEpiLinear, kEpiLinearF32). What a tile needs beside its accumulator is
 // requested while the MMAs still run: each epilogue warp copies the tile's column scales,
 // biases and gates into shared memory of its own (read back as broadcasts; loading them
 // from global memory 16 columns at a time exposed three L2 latencies per 16 columns and
@@ -482,12 +482,12 @@ __device__ __forceinline__ void epilogue_drain_plain(const GemmShape& g, const G
 // (2.98 PFLOP/s; without residual and gate 526); 32760 x 1024 x 5120: 472 -> 328.
 constexpr int kLinearAhead = 64;  // columns
 
-template <int BN>
+template <int BN, bool kF32>
 struct LinearTile {
   static constexpr int kHalf = (BN / 2 + 15) / 16 * 16;
   static constexpr int kParamBytes = 8 * 3 * kHalf * 4;  // 8 warps x (scale, bias, gate) x kHalf fp32
 
-  uint32_t res[kLinearAhead / 16][16];
+  uint32_t res[kLinearAhead / 16][kF32 ? 16 : 8];
 
   static __device__ __forceinline__ bool fetches(const GemmShape& g, const LinearEpilogue& e, long long row) {
     return e.residual != nullptr && e.wide && row < g.T;
@@ -501,7 +501,7 @@ struct LinearTile {
     if (fetches(g, a.lin, row)) {
 #pragma unroll
       for (int i = 0; i < kLinearAhead / 16; ++i)
-        if (16 * i < width && col_base + 16 * (i + 1) <= g.I) load_residual16(a.lin, row, col_base + 16 * i, res[i]);
+        if (16 * i < width && col_base + 16 * (i + 1) <= g.I) load_residual16<kF32>(a.lin, row, col_base + 16 * i, res[i]);
     }
     __syncwarp();  // every lane has read the previous tile's
 #pragma unroll
@@ -537,7 +537,7 @@ struct LinearTile {
         tmem_ld_wait();
         if (row_ok) {
           if (e.wide && col0 + 16 <= g.I) {
-            finish16(e, row, col0, r, ascale, a.w_col_scale != nullptr ? params + cc : nullptr,
+            finish16<kF32>(e, row, col0, r, ascale, a.w_col_scale != nullptr ? params + cc : nullptr,
                      a.bias != nullptr ? params + kHalf + cc : nullptr,
                      e.gate != nullptr ? params + 2 * kHalf + cc : nullptr, res[i], pol_out);
           } else {
@@ -547,14 +547,14 @@ struct LinearTile {
 #pragma unroll
               for (int k = 0; k < 16; ++k) acc = j == k ? __uint_as_float(r[k]) : acc;
               if (c < g.I)
-                finish_one(e, row, c, acc, a.w_col_scale != nullptr ? ascale * params[cc + j] : ascale,
+                finish_one<kF32>(e, row, c, acc, a.w_col_scale != nullptr ? ascale * params[cc + j] : ascale,
                            a.bias != nullptr ? params[kHalf + cc + j] : 0.0f,
                            e.gate != nullptr ? params[2 * kHalf + cc + j] : 1.0f);
             }
           }
         }
         if (fetch && cc + kLinearAhead < width && col0 + kLinearAhead + 16 <= g.I)
-          load_residual16(e, row, col0 + kLinearAhead, res[i]);
+          load_residual16<kF32>(e, row, col0 + kLinearAhead, res[i]);
       }
     }
   }
@@ -568,12 +568,17 @@ struct LinearTile {
 //   kEpiStatsRms / kEpiStatsLayer : as plain, plus the per-head statistics (RMS: sums of
 //               squares; LayerNorm: each part's mean and centred M2, values handed over
 //               centred) the norm/RoPE pass finishes from
-//   kEpiLinear: bias, activation, gate and residual to a strided output (qkv_cte_linear_run)
-constexpr int kEpiPlain = 0, kEpiHead = 1, kEpiStatsRms = 2, kEpiStatsLayer = 3, kEpiLinear = 4;
+//   kEpiLinear / kEpiLinearF32: bias, activation, gate and residual to a strided output of
+//               a 16-bit type or fp32 (qkv_cte_linear_run). Two kinds because fp32's longer
+//               exponentials and residual words in one with the 16-bit types' cost those 18 % at
+//               small K (32760 x 1024 x 5120 bf16, no activation: 190 -> 230 us)
+constexpr int kEpiPlain = 0, kEpiHead = 1, kEpiStatsRms = 2, kEpiStatsLayer = 3, kEpiLinear = 4, kEpiLinearF32 = 5;
+template <int kEpi>
+constexpr bool kProduct = kEpi == kEpiLinear || kEpi == kEpiLinearF32;
 
 // Epilogue warps of the CTA-pair form, and its threads.
 template <int kEpi>
-constexpr int kEpilogueWarps = kEpi == kEpiLinear ? 8 : 4;
+constexpr int kEpilogueWarps = kProduct<kEpi> ? 8 : 4;
 template <int kEpi>
 constexpr int kPairThreads = 64 + 32 * kEpilogueWarps<kEpi>;
 
@@ -1273,8 +1278,9 @@ __global__ void __launch_bounds__(kPairThreads<kEpi>, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     FusedWork fw;
-    [[maybe_unused]] LinearTile<BN> lin;
-    constexpr int kHalf = LinearTile<BN>::kHalf;
+    using Linear = LinearTile<BN, kEpi == kEpiLinearF32>;
+    [[maybe_unused]] Linear lin;
+    constexpr int kHalf = Linear::kHalf;
     [[maybe_unused]] const int lin_col = warp < 6 ? 0 : kHalf;  // this warp's first column of a tile
     [[maybe_unused]] const int lin_width = warp < 6 ? kHalf : BN - kHalf;
     [[maybe_unused]] float* lin_params = reinterpret_cast<float*>(sSFA + 768) + (warp - 2) * 3 * kHalf;
@@ -1299,7 +1305,7 @@ __global__ void __launch_bounds__(kPairThreads<kEpi>, 1)
       const int block128 = m_blk * 2 + static_cast<int>(rank);
       // A 128-row half wholly past T (T mod 256 in (0, 128]) has nothing to store.
       const bool live = block128 * kBM < g.T;
-      if constexpr (kEpi == kEpiLinear) {
+      if constexpr (kProduct<kEpi>) {
         if (live) lin.begin(g, a, lin_params, block128, row_in_block, n_blk * BN + lin_col, lin_width);
       }
       bool ok;
@@ -1315,7 +1321,7 @@ __global__ void __launch_bounds__(kPairThreads<kEpi>, 1)
       tc_fence_after();
       float ss_q = 0.0f, ss_k = 0.0f;
       if (live) {
-        if constexpr (kEpi == kEpiLinear)
+        if constexpr (kProduct<kEpi>)
           lin.drain(g, a, t_lane + static_cast<uint32_t>(acc * BN + lin_col), lin_params, block128, row_in_block,
                     n_blk * BN + lin_col, lin_width, pol_out);
         else
@@ -1381,7 +1387,7 @@ cudaError_t launch_gemm_pair_t(const GemmShape& g, const CUtensorMap& tmA, const
                                int num_sms) {
   using C = K1PairCfg<BN>;
   auto kern = qkv_gemm_mxf8_pair_kernel<BN, kEpi, kFused>;
-  constexpr size_t smem = C::SMEM + (kEpi == kEpiLinear ? LinearTile<BN>::kParamBytes : 0);
+  constexpr size_t smem = C::SMEM + (kProduct<kEpi> ? LinearTile<BN, kEpi == kEpiLinearF32>::kParamBytes : 0);
   static_assert(smem <= C::SMEM_LIMIT, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
