@@ -55,6 +55,8 @@ int fail(int code, const char* fmt, ...) {
   va_start(ap, fmt);
   vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
   va_end(ap);
+  // The runtime remembers a refused call, too: the next launch would report it as its own.
+  if (code == QKV_CTE_ERR_CUDA) (void)cudaGetLastError();
   return code;
 }
 

@@ -1,4 +1,8 @@
-"""Calls of the block operators that must be refused."""
+"""Calls of the block operators that must be refused, or that an earlier failed call must
+not make fail."""
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -90,3 +94,54 @@ def test_more_columns_than_32_bits_are_refused():
         lib.qkv_cte_layer_norm(x, out=x)
     with pytest.raises((ValueError, lib.QkvCteError)):
         lib.qkv_cte_layer_norm_backward(x, x, torch.zeros(1, device=DEV), torch.ones(1, device=DEV), dx=x)
+
+
+STALE = r"""
+import os
+import sys
+
+import torch
+import rope_tcgen05_mxfp8_gb300 as lib
+rope = lib.QkvCteRopeAxes(64, (64,))
+x = torch.randn(6, 2, 64, device="cuda")
+pos = torch.arange(6, device="cuda", dtype=torch.int32)[:, None]
+want = rope(x, positions=pos)
+op = lib.QkvCteLinear(2, 64, 32)
+A = torch.zeros(2, 64, dtype=torch.uint8, device="cuda")
+s = torch.ones(2, device="cuda")
+W = torch.zeros(32, 64, dtype=torch.uint8, device="cuda")
+sf = torch.full((32, 2), 127, dtype=torch.uint8, device="cuda")
+out = op(A, s, W, sf)
+y = torch.empty_like(x)
+torch.cuda.synchronize()
+side = torch.cuda.Stream()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.stream(side):
+    graph.capture_begin()
+    try:
+        side.synchronize()                    # not allowed here: the capture is lost
+    except Exception as e:
+        print("lost:", type(e).__name__)
+    try:
+        op(A, s, W, sf, out=out)
+        raise SystemExit("the call into a lost capture went through")
+    except lib.QkvCteError as e:
+        print("refused:", e)
+    try:
+        graph.capture_end()
+    except Exception as e:
+        print("ended:", type(e).__name__)
+rope(x, positions=pos, out=y)                 # a call of its own: nothing is wrong with it
+torch.cuda.synchronize()
+assert torch.equal(y, want)
+print("fine")
+sys.stdout.flush()
+os._exit(0)                                   # without tearing the graph down
+"""
+
+
+def test_a_failed_launch_is_not_reported_again():
+    """A launch that CUDA refuses is reported by its own call only. (In a process of its
+    own: it ends a graph capture half way.)"""
+    r = subprocess.run([sys.executable, "-c", STALE], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "refused" in r.stdout and "fine" in r.stdout, r.stdout + r.stderr
