@@ -5,6 +5,7 @@ activation, gate and residual.
 Argument marshalling only, as in qkv_cte.py: every computation runs in the library's
 kernels. Tensors live on one CUDA device, which need not be the current one; a call
 runs on `stream` (default: that device's current stream) and does not synchronise.
+Results carry no autograd graph; tensors given for them count as modified in place.
 """
 from __future__ import annotations
 
@@ -15,7 +16,8 @@ from typing import Optional, Sequence
 import torch
 
 from .qkv_cte import (QKV_CTE_ERR_UNSUPPORTED, QKV_CTE_INPUT_BF16, QKV_CTE_INPUT_PACKED,
-                      QKV_CTE_INPUT_ROW_FP8, QkvCteError, _check, _cleared, _current_device, _empty, _raw_stream, _side, _used_on, load, qkv_cte_status)
+                      QKV_CTE_INPUT_ROW_FP8, QkvCteError, _check, _cleared, _current_device, _empty, _raw_stream,
+                      _side, _used_on, _written, load, qkv_cte_status)
 
 QKV_CTE_DTYPE_BF16 = 0
 QKV_CTE_DTYPE_FP16 = 1
@@ -185,6 +187,7 @@ def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None,
         raise TypeError(f"weight and bias: dtype {pdt} is neither {dt} nor torch.float32")
     pw = _vector("weight", weight, (pdt,), dev, cols)
     pb = _vector("bias", bias, (pdt,), dev, cols)
+    given = out, mean, rstd
     side = None if stream is None else _side(stream, dev)
     if out is None:
         out = _empty(side, shape, dt, dev)
@@ -200,6 +203,7 @@ def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None,
     pr = _statistic("rstd", rstd, dev, shape[:-1], rows)
     _launch(_lib().qkv_cte_layer_norm, dev, stream, px, ldx, pw, pb, py, ldy, pm, pr, rows, cols, eps, _DTYPE[dt],
             _DTYPE[pdt])
+    _written(*given)
     return out, mean, rstd
 
 
@@ -225,6 +229,7 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
     if pdt not in (x.dtype, torch.float32):
         raise TypeError(f"weight, dweight and dbias: dtype {pdt} is neither {x.dtype} nor torch.float32")
     side = None if stream is None else _side(stream, dev)
+    given = ()
     if dx is None and dweight is None and dbias is None:
         dx = _empty(side, x.shape, x.dtype, dev)
         dweight = _empty(side, (cols,), pdt, dev)
@@ -234,6 +239,7 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
         pd, ldd = _rows("dx", dx, (x.dtype,), dev, x.shape) if dx is not None else (None, 0)
         pdw = _vector("dweight", dweight, (pdt,), dev, cols)
         pdb = _vector("dbias", dbias, (pdt,), dev, cols)
+        given = dx, dweight, dbias
     pw = _vector("weight", weight, (pdt,), dev, cols)
     pm = _statistic("mean", mean, dev, x.shape[:-1], rows)
     pr = _statistic("rstd", rstd, dev, x.shape[:-1], rows)
@@ -245,6 +251,7 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
         pws = _vector("workspace", workspace, (torch.uint8,), dev, ws_bytes)
     _launch(_lib().qkv_cte_layer_norm_backward, dev, stream, pg, ldg, px, ldx, pw, pm, pr, pd, ldd, pdw, pdb, rows,
             cols, _DTYPE[x.dtype], _DTYPE[pdt], pws, ws_bytes)
+    _written(*given)
     return dx, dweight, dbias
 
 
@@ -292,6 +299,7 @@ class QkvCteRopeAxes:
             raise ValueError("give positions or grids (one of them)")
         dev = _tensor("positions and grids", where, (torch.int32,)).device
         p, stride, g = self._where(batch, seq, positions, grids, dev)
+        given = cos, sin
         side = None if stream is None else _side(stream, dev)
         if cos is None:
             cos = _empty(side, (batch * seq, self.d_head), torch.float32, dev)
@@ -300,6 +308,7 @@ class QkvCteRopeAxes:
         n, d = batch * seq * self.d_head, self.d_head
         pc, ps = _vector("cos", cos, (torch.float32,), dev, n, d), _vector("sin", sin, (torch.float32,), dev, n, d)
         _launch(_lib().qkv_cte_rope_tables, dev, stream, self.plan, batch, seq, p, stride, g, pc, ps)
+        _written(*given)
         return cos, sin
 
     def __call__(self, x, positions=None, grids=None, out=None, inverse=False, stream=None):
@@ -312,6 +321,7 @@ class QkvCteRopeAxes:
                              f"got {tuple(shape)}")
         if sx[-1] != 1:
             raise ValueError("x: the last dimension must be contiguous")
+        given = out
         if out is None:
             out = _empty(None if stream is None else _side(stream, dev), shape, dt, dev)
         else:
@@ -326,6 +336,7 @@ class QkvCteRopeAxes:
         p, stride, g = self._where(batch, seq, positions, grids, dev)
         _launch(_lib().qkv_cte_rope_apply, dev, stream, self.plan, x.data_ptr(), bx, sx[-3], sx[-2], out.data_ptr(),
                 by, sy[-3], sy[-2], batch, seq, heads, p, stride, g, _DTYPE[dt], 1 if inverse else 0)
+        _written(given)
         return out
 
     def close(self):
@@ -397,12 +408,14 @@ class QkvCteLinear:
         pb = _vector("bias", bias, _BF16_BITS, dev, N)
         pg = _vector("gate", gate, _BF16_BITS, dev, N)
         pr, ldr = _rows("residual", residual, (self.out_dtype,), dev, (T, N)) if residual is not None else (None, 0)
+        given = out
         if out is None:
             out = _empty(None if stream is None else _side(stream, dev), self.shape, self.out_dtype, dev)
         po, ldo = _rows("out", out, (self.out_dtype,), dev, (T, N))
         handle = _used_on(self.workspace, self._streams, stream)
         _launch(_lib().qkv_cte_linear_run, dev, handle, self.plan, pa, ps, pw, pf, pc, pb, pg, pr, ldr, po, ldo,
                 self.workspace.data_ptr(), self.workspace.numel())
+        _written(given)
         return out
 
     def status(self, stream=None) -> int:

@@ -207,6 +207,14 @@ _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle,
 _current_device = torch._C._cuda_getDevice
 
 
+def _written(*tensors):
+    """Count a write to each of the caller's tensors (or None), as torch's in-place
+    operations do: autograd then refuses to use a value it saved and that is gone."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _side(stream, device):
     """The stream of a call, or None where it is `device`'s current one."""
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -267,7 +275,9 @@ def qkv_cte_run(plan, A, a_scale, W, w_sf, w_col_scale, bias, gamma_q, gamma_k, 
             _ptr("w_col_scale", w_col_scale), _ptr("bias", bias), _ptr("gamma_q", gamma_q),
             _ptr("gamma_k", gamma_k), _ptr("cos", cos), _ptr("sin", sin), _ptr("O", O),
             _ptr("sumsq", sumsq), _ptr("inv_rms", inv_rms), _ptr("workspace", workspace)]
-    return _check(load().qkv_cte_run(plan, *args, ctypes.c_size_t(ws_bytes), ctypes.c_void_p(handle)))
+    rc = _check(load().qkv_cte_run(plan, *args, ctypes.c_size_t(ws_bytes), ctypes.c_void_p(handle)))
+    _written(O, sumsq, inv_rms)
+    return rc
 
 
 def qkv_cte_run_noalloc(plan, A, a_scale, W, w_sf, w_col_scale, bias, gamma_q, gamma_k, cos, sin, O,
@@ -281,7 +291,9 @@ def qkv_cte_run_noalloc(plan, A, a_scale, W, w_sf, w_col_scale, bias, gamma_q, g
             _ptr("w_col_scale", w_col_scale), _ptr("bias", bias), _ptr("gamma_q", gamma_q),
             _ptr("gamma_k", gamma_k), _ptr("cos", cos), _ptr("sin", sin), _ptr("O", O),
             _ptr("sumsq", sumsq), _ptr("inv_rms", inv_rms)]
-    return _check(load().qkv_cte_run_noalloc(plan, *args, ctypes.c_void_p(handle)))
+    rc = _check(load().qkv_cte_run_noalloc(plan, *args, ctypes.c_void_p(handle)))
+    _written(O, sumsq, inv_rms)
+    return rc
 
 
 def _stream_handle(stream):
@@ -301,6 +313,7 @@ def qkv_cte_row_quantize(X, A=None, a_scale=None, packed=None, stream=None):
         a_scale = _empty(side, (T,), torch.float32, X.device)
     _check(load().qkv_cte_row_quantize(_ptr("X", X), T, H, _ptr("A", A), _ptr("a_scale", a_scale),
                                        _ptr("packed", packed), _stream_handle(stream)))
+    _written(A, a_scale, packed)
     return A, a_scale, packed
 
 
@@ -314,6 +327,7 @@ def qkv_cte_unpack_rows(packed, A=None, a_scale=None, stream=None):
         a_scale = _empty(side, (T,), torch.float32, packed.device)
     _check(load().qkv_cte_unpack_rows(_ptr("packed", packed), T, H, _ptr("A", A), _ptr("a_scale", a_scale),
                                       _stream_handle(stream)))
+    _written(A, a_scale)
     return A, a_scale
 
 
@@ -332,6 +346,7 @@ def qkv_cte_interleaved_to_rotate_half(src, n_q_heads, n_kv_heads, d_head, dst=N
     _check(load().qkv_cte_interleaved_to_rotate_half(ctypes.c_void_p(src.data_ptr()), ctypes.c_void_p(dst.data_ptr()),
                                                      rows, row_bytes, n_q_heads, n_kv_heads, d_head,
                                                      _stream_handle(stream)))
+    _written(dst)
     return dst
 
 
@@ -360,8 +375,10 @@ def qkv_cte_run_host(plan, A_host, a_scale_host, W, w_sf, w_col_scale, bias, gam
             _ptr("w_col_scale", w_col_scale), _ptr("bias", bias), _ptr("gamma_q", gamma_q),
             _ptr("gamma_k", gamma_k), _ptr("cos", cos), _ptr("sin", sin), _host_ptr("O_host", O_host),
             _ptr("sumsq", sumsq), _ptr("inv_rms", inv_rms), _ptr("workspace", scratch)]
-    return _check(load().qkv_cte_run_host(plan, *args, ctypes.c_size_t(ws_bytes), chunk_rows,
-                                          _stream_handle(stream)))
+    rc = _check(load().qkv_cte_run_host(plan, *args, ctypes.c_size_t(ws_bytes), chunk_rows,
+                                        _stream_handle(stream)))
+    _written(O_host, sumsq, inv_rms)
+    return rc
 
 
 def qkv_cte_status(workspace, stream=None) -> int:

@@ -96,6 +96,39 @@ def test_more_columns_than_32_bits_are_refused():
         lib.qkv_cte_layer_norm_backward(x, x, torch.zeros(1, device=DEV), torch.ones(1, device=DEV), dx=x)
 
 
+def test_in_place_results_count_as_changes():
+    """autograd sees that a tensor it saved was overwritten."""
+    rope = lib.QkvCteRopeAxes(64, (64,))
+    pos = torch.arange(6, device=DEV, dtype=torch.int32)[:, None]
+    c = Case(6, 64, 64, residual=True, out="fp32")
+    op = c.op()
+
+    def norm(t):
+        lib.qkv_cte_layer_norm(t, out=t)
+
+    def norm_backward(t):
+        lib.qkv_cte_layer_norm_backward(t, t, torch.zeros(6, device=DEV), torch.ones(6, device=DEV), dx=t)
+
+    def turn(t):
+        rope(t.view(6, 1, 64), positions=pos, out=t.view(6, 1, 64))
+
+    def product(t):
+        c.run(op, residual=t, out=t)
+
+    for write in (norm, norm_backward, turn, product):
+        leaf = torch.randn(6, 64, device=DEV, requires_grad=True)
+        z = leaf * 1.0
+        loss = (z * z).sum()                       # saves z
+        with torch.no_grad():
+            write(z.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with torch.inference_mode():                   # tensors without a version counter
+        t = torch.randn(6, 64, device=DEV)
+        for write in (norm, norm_backward, turn, product):
+            write(t)
+
+
 STALE = r"""
 import os
 import sys
