@@ -17,7 +17,7 @@ import torch
 
 from .qkv_cte import (QKV_CTE_ERR_UNSUPPORTED, QKV_CTE_INPUT_BF16, QKV_CTE_INPUT_PACKED,
                       QKV_CTE_INPUT_ROW_FP8, QkvCteError, _check, _cleared, _current_device, _empty, _raw_stream,
-                      _side, _used_on, _written, load, qkv_cte_status)
+                      _handle, _side, _used_on, _written, load, qkv_cte_status)
 
 QKV_CTE_DTYPE_BF16 = 0
 QKV_CTE_DTYPE_FP16 = 1
@@ -99,7 +99,7 @@ def _launch(fn, device, stream, *args):
     if stream is None:
         handle = _raw_stream(device.index)
     else:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        handle = stream if type(stream) is int else _handle(stream)
     if device.index == _current_device():
         rc = fn(*args, handle)
     else:
@@ -138,14 +138,12 @@ def _vector(name: str, t, dtypes, device, n: int, last: int = 1) -> Optional[int
     raise ValueError(f"{name}: must be contiguous with {n} elements{rows}, got shape {tuple(t.shape)}")
 
 
-def _statistic(name: str, t, device, lead, rows: int) -> Optional[int]:
-    """Address of an fp32 value per row of a tensor with leading dimensions `lead`, or None.
-    Several dimensions have to be `lead`'s (dimensions of one element aside)."""
+def _statistic(name: str, t, device, shape, rows: int) -> int:
+    """Address of an fp32 value per row of a tensor of `shape`. Where that has several
+    leading dimensions, t's have to be the same (those of one element aside) unless flat."""
     p = _vector(name, t, (torch.float32,), device, rows)
-    if p is None or len(lead) < 2 or t.dim() < 2 or t.shape == lead:
-        return p
-    if [v for v in t.shape if v != 1] != [v for v in lead if v != 1]:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} is neither {tuple(lead)} nor flat")
+    if len(shape) > 2 and t.dim() > 1 and [v for v in t.shape if v != 1] != [v for v in shape[:-1] if v != 1]:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} is neither {tuple(shape[:-1])} nor flat")
     return p
 
 
@@ -179,7 +177,9 @@ def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None,
     `out` may be x."""
     px, ldx = _rows("x", x, _DTYPE)
     dev, shape, dt = x.device, x.shape, x.dtype
-    cols = _fits("cols", shape[-1])
+    cols = shape[-1]
+    if cols >> 31:
+        _fits("cols", cols)
     rows = x.numel() // cols if cols else 0
     param = weight if weight is not None else bias
     pdt = param.dtype if isinstance(param, torch.Tensor) else dt
@@ -187,10 +187,10 @@ def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None,
         raise TypeError(f"weight and bias: dtype {pdt} is neither {dt} nor torch.float32")
     pw = _vector("weight", weight, (pdt,), dev, cols)
     pb = _vector("bias", bias, (pdt,), dev, cols)
-    given = out, mean, rstd
+    given = None if out is None and mean is None and rstd is None else (out, mean, rstd)
     side = None if stream is None else _side(stream, dev)
     if out is None:
-        out = _empty(side, shape, dt, dev)
+        out = torch.empty(shape, dtype=dt, device=dev) if side is None else _empty(side, shape, dt, dev)
         py, ldy = out.data_ptr(), cols
     else:
         py, ldy = _rows("out", out, (dt,), dev, shape)
@@ -199,11 +199,12 @@ def qkv_cte_layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, mean=None,
             mean = _empty(side, shape[:-1], torch.float32, dev)
         if rstd is None:
             rstd = _empty(side, shape[:-1], torch.float32, dev)
-    pm = _statistic("mean", mean, dev, shape[:-1], rows)
-    pr = _statistic("rstd", rstd, dev, shape[:-1], rows)
+    pm = None if mean is None else _statistic("mean", mean, dev, shape, rows)
+    pr = None if rstd is None else _statistic("rstd", rstd, dev, shape, rows)
     _launch(_lib().qkv_cte_layer_norm, dev, stream, px, ldx, pw, pb, py, ldy, pm, pr, rows, cols, eps, _DTYPE[dt],
             _DTYPE[pdt])
-    _written(*given)
+    if given:
+        _written(*given)
     return out, mean, rstd
 
 
@@ -221,7 +222,9 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
     none given, all three allocated here (dweight and dbias of weight's type, fp32 without
     a weight). mean, rstd: the forward pass's statistics. dx may be dy or x."""
     px, ldx = _rows("x", x, _DTYPE)
-    dev, cols = x.device, _fits("cols", x.shape[-1])
+    dev, cols = x.device, x.shape[-1]
+    if cols >> 31:
+        _fits("cols", cols)
     rows = x.numel() // cols if cols else 0
     pg, ldg = _rows("dy", dy, (x.dtype,), dev, x.shape)
     param = weight if weight is not None else dweight if dweight is not None else dbias
@@ -229,11 +232,16 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
     if pdt not in (x.dtype, torch.float32):
         raise TypeError(f"weight, dweight and dbias: dtype {pdt} is neither {x.dtype} nor torch.float32")
     side = None if stream is None else _side(stream, dev)
-    given = ()
+    given = None
     if dx is None and dweight is None and dbias is None:
-        dx = _empty(side, x.shape, x.dtype, dev)
-        dweight = _empty(side, (cols,), pdt, dev)
-        dbias = _empty(side, (cols,), pdt, dev)
+        if side is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            dweight = torch.empty(cols, dtype=pdt, device=dev)
+            dbias = torch.empty(cols, dtype=pdt, device=dev)
+        else:
+            dx = _empty(side, x.shape, x.dtype, dev)
+            dweight = _empty(side, (cols,), pdt, dev)
+            dbias = _empty(side, (cols,), pdt, dev)
         pd, ldd, pdw, pdb = dx.data_ptr(), cols, dweight.data_ptr(), dbias.data_ptr()
     else:
         pd, ldd = _rows("dx", dx, (x.dtype,), dev, x.shape) if dx is not None else (None, 0)
@@ -241,8 +249,8 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
         pdb = _vector("dbias", dbias, (pdt,), dev, cols)
         given = dx, dweight, dbias
     pw = _vector("weight", weight, (pdt,), dev, cols)
-    pm = _statistic("mean", mean, dev, x.shape[:-1], rows)
-    pr = _statistic("rstd", rstd, dev, x.shape[:-1], rows)
+    pm = None if mean is None else _statistic("mean", mean, dev, x.shape, rows)
+    pr = None if rstd is None else _statistic("rstd", rstd, dev, x.shape, rows)
     ws_bytes, pws = 0, None
     if (dweight is not None or dbias is not None) and rows:
         if workspace is None:
@@ -251,7 +259,8 @@ def qkv_cte_layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight
         pws = _vector("workspace", workspace, (torch.uint8,), dev, ws_bytes)
     _launch(_lib().qkv_cte_layer_norm_backward, dev, stream, pg, ldg, px, ldx, pw, pm, pr, pd, ldd, pdw, pdb, rows,
             cols, _DTYPE[x.dtype], _DTYPE[pdt], pws, ws_bytes)
-    _written(*given)
+    if given:
+        _written(*given)
     return dx, dweight, dbias
 
 
@@ -297,18 +306,24 @@ class QkvCteRopeAxes:
         where = grids if grids is not None else positions
         if not isinstance(where, torch.Tensor):
             raise ValueError("give positions or grids (one of them)")
-        dev = _tensor("positions and grids", where, (torch.int32,)).device
+        dev = where.device
+        if not where.is_cuda:
+            raise ValueError("positions and grids: must be CUDA tensors")
         p, stride, g = self._where(batch, seq, positions, grids, dev)
-        given = cos, sin
+        given = None if cos is None and sin is None else (cos, sin)
+        n, d, f32 = batch * seq, self.d_head, (torch.float32,)
         side = None if stream is None else _side(stream, dev)
         if cos is None:
-            cos = _empty(side, (batch * seq, self.d_head), torch.float32, dev)
+            cos = _empty(side, (n, d), torch.float32, dev)
         if sin is None:
-            sin = _empty(side, (batch * seq, self.d_head), torch.float32, dev)
-        n, d = batch * seq * self.d_head, self.d_head
-        pc, ps = _vector("cos", cos, (torch.float32,), dev, n, d), _vector("sin", sin, (torch.float32,), dev, n, d)
+            sin = _empty(side, (n, d), torch.float32, dev)
+        if given is None:
+            pc, ps = cos.data_ptr(), sin.data_ptr()
+        else:
+            pc, ps = _vector("cos", cos, f32, dev, n * d, d), _vector("sin", sin, f32, dev, n * d, d)
         _launch(_lib().qkv_cte_rope_tables, dev, stream, self.plan, batch, seq, p, stride, g, pc, ps)
-        _written(*given)
+        if given:
+            _written(*given)
         return cos, sin
 
     def __call__(self, x, positions=None, grids=None, out=None, inverse=False, stream=None):
@@ -323,7 +338,8 @@ class QkvCteRopeAxes:
             raise ValueError("x: the last dimension must be contiguous")
         given = out
         if out is None:
-            out = _empty(None if stream is None else _side(stream, dev), shape, dt, dev)
+            side = None if stream is None else _side(stream, dev)
+            out = torch.empty(shape, dtype=dt, device=dev) if side is None else _empty(side, shape, dt, dev)
         else:
             _tensor("out", out, (dt,), dev)
             if out.shape != shape:
@@ -332,11 +348,14 @@ class QkvCteRopeAxes:
         if sy[-1] != 1:
             raise ValueError("out: the last dimension must be contiguous")
         batch, bx, by = (shape[0], sx[0], sy[0]) if len(shape) == 4 else (1, 0, 0)
-        seq, heads = shape[-3], _fits("heads", shape[-2])
+        seq, heads = shape[-3], shape[-2]
+        if heads >> 31:
+            _fits("heads", heads)
         p, stride, g = self._where(batch, seq, positions, grids, dev)
         _launch(_lib().qkv_cte_rope_apply, dev, stream, self.plan, x.data_ptr(), bx, sx[-3], sx[-2], out.data_ptr(),
                 by, sy[-3], sy[-2], batch, seq, heads, p, stride, g, _DTYPE[dt], 1 if inverse else 0)
-        _written(given)
+        if given is not None:
+            _written(given)
         return out
 
     def close(self):
@@ -410,12 +429,17 @@ class QkvCteLinear:
         pr, ldr = _rows("residual", residual, (self.out_dtype,), dev, (T, N)) if residual is not None else (None, 0)
         given = out
         if out is None:
-            out = _empty(None if stream is None else _side(stream, dev), self.shape, self.out_dtype, dev)
+            side = None if stream is None else _side(stream, dev)
+            out = (torch.empty(self.shape, dtype=self.out_dtype, device=dev) if side is None
+                   else _empty(side, self.shape, self.out_dtype, dev))
         po, ldo = _rows("out", out, (self.out_dtype,), dev, (T, N))
-        handle = _used_on(self.workspace, self._streams, stream)
+        handle = _raw_stream(dev.index) if stream is None else _handle(stream)
+        if handle not in self._streams:
+            _used_on(self.workspace, self._streams, handle)
         _launch(_lib().qkv_cte_linear_run, dev, handle, self.plan, pa, ps, pw, pf, pc, pb, pg, pr, ldr, po, ldo,
                 self.workspace.data_ptr(), self.workspace.numel())
-        _written(given)
+        if given is not None:
+            _written(given)
         return out
 
     def status(self, stream=None) -> int:

@@ -207,6 +207,11 @@ _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle,
 _current_device = torch._C._cuda_getDevice
 
 
+def _handle(stream) -> int:
+    """The raw handle of a torch stream (or of a raw handle)."""
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _written(*tensors):
     """Count a write to each of the caller's tensors (or None), as torch's in-place
     operations do: autograd then refuses to use a value it saved and that is gone."""
@@ -217,7 +222,7 @@ def _written(*tensors):
 
 def _side(stream, device):
     """The stream of a call, or None where it is `device`'s current one."""
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    handle = _handle(stream)
     if handle == _raw_stream(device.index):
         return None
     return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=device)
@@ -254,10 +259,7 @@ def _cleared(nbytes, device):
 def _used_on(workspace, known, stream) -> int:
     """The handle of the stream a call on `workspace` runs on; the allocator learns of each
     such stream once (`known`: their handles)."""
-    if stream is None:
-        handle = _raw_stream(workspace.device.index)
-    else:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    handle = _raw_stream(workspace.device.index) if stream is None else _handle(stream)
     if handle not in known:
         workspace.record_stream(torch.cuda.ExternalStream(handle, device=workspace.device))
         known.add(handle)
