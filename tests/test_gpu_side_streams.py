@@ -200,3 +200,20 @@ def test_projection_workspace_is_ready_for_any_stream():
 @pytest.mark.parametrize("current", [False, True])
 def test_projection_workspace_outlives_its_object(current):
     _workspace_outlives_its_object(*_run_projection(0), current)
+
+
+@pytest.mark.parametrize("T", [3, 700])
+def test_object_made_within_a_capture(T):
+    """The workspace's fill is then part of the graph, before the run that needs it."""
+    make, run, size, want = _run_linear(T)
+    _dirty(size)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op = make()
+        got = run(op, None)
+    for _ in range(2):
+        op.workspace.fill_(255)
+        got.zero_()
+        graph.replay()
+        assert op.status() == 0 and torch.equal(got, want)
