@@ -212,6 +212,13 @@ def _handle(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _stream_of(handle, device):
+    """The torch stream of a raw handle (ExternalStream takes 0 for none given)."""
+    if handle == 0:
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
 def _written(*tensors):
     """Count a write to each of the caller's tensors (or None), as torch's in-place
     operations do: autograd then refuses to use a value it saved and that is gone."""
@@ -225,7 +232,7 @@ def _side(stream, device):
     handle = _handle(stream)
     if handle == _raw_stream(device.index):
         return None
-    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=device)
+    return stream if isinstance(stream, torch.cuda.Stream) else _stream_of(handle, device)
 
 
 def _side_of(stream, t):
@@ -261,7 +268,7 @@ def _used_on(workspace, known, stream) -> int:
     such stream once (`known`: their handles)."""
     handle = _raw_stream(workspace.device.index) if stream is None else _handle(stream)
     if handle not in known:
-        workspace.record_stream(torch.cuda.ExternalStream(handle, device=workspace.device))
+        workspace.record_stream(_stream_of(handle, workspace.device))
         known.add(handle)
     return handle
 

@@ -6,6 +6,7 @@ import torch
 
 import rope_tcgen05_mxfp8_gb300 as lib
 import workloads as wl
+from rope_tcgen05_mxfp8_gb300 import qkv_cte as q
 from gpu_harness import assert_same_to_rounding
 from test_gpu_linear import Case
 
@@ -217,3 +218,40 @@ def test_object_made_within_a_capture(T):
         got.zero_()
         graph.replay()
         assert op.status() == 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("stream", [0, "default"])
+@pytest.mark.parametrize("make", BLOCK_OPS + PROJECTION)
+def test_results_on_the_default_stream_from_another(make, stream):
+    """The default stream, by its handle 0 or as an object, while another one is current."""
+    with torch.cuda.stream(torch.cuda.Stream()):
+        f = make()
+        want = [t.clone() for t in f()]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(SPIN)
+        late = [torch.full((n,), 7, dtype=torch.uint8, device=DEV)
+                for t in want for n in [t.numel() * t.element_size()] * 3]
+        late += [torch.full((1 << 19,), 7, dtype=torch.uint8, device=DEV) for _ in range(8)]
+        del late
+        got = f(stream=torch.cuda.default_stream() if stream else 0)
+        torch.cuda.synchronize()
+        assert all(_same(g, w) for g, w in zip(got, want))
+        # as memory of that stream, not of some other that a handle of 0 might name
+        assert q._side(torch.cuda.default_stream() if stream else 0, got[0].device).cuda_stream == 0
+
+
+@pytest.mark.parametrize("case", [lambda: _run_linear(3), lambda: _run_linear(700), lambda: _run_projection(0)])
+def test_workspace_of_another_stream_outlives_a_call_on_the_default_one(case):
+    make, run, size, want = case()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        op = make()
+    torch.cuda._sleep(SPIN)
+    got = run(op, None)
+    del op
+    with torch.cuda.stream(s):
+        late = [torch.full((size,), 255, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    torch.cuda.synchronize()
+    assert _same(got, want)
+    assert all(bool((t == 255).all()) for t in late)
