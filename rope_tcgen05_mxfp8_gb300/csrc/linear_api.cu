@@ -37,8 +37,13 @@ namespace {
 // K1's tile width. A wave of tiles (one per CTA pair, 76 pairs on GB300's 152 SMs) takes
 // about 12.5, 13.9 and 15.4 us at K = 5120 for widths 128, 192 and 240, proportional to
 // the width plus 350, so the widest tile wins many waves and a narrower one few. us a call
-// for 128 / 192 / 240: 1024 x 5120 x 1280 24.7 / 26.8 / 28.8 (one wave each),
-// 2048 x 5120 x 5120 74 / 54 / 57 (5, 3 and 3), 4096 x 5120 x 5120 122 / 96 / 88 (9, 6, 5).
+// in a captured graph for 128 / 192 / 240: 1024 x 5120 x 1280 21.2 / 22.6 / 23.3 (one wave
+// each), 2048 x 5120 x 5120 67 / 48 / 48 (5, 3 and 3), 4096 x 5120 x 5120 113 / 88 / 78 (9,
+// 6, 5). At small K the epilogue bounds a tile, and its time goes by the width as well:
+// 32760 x 512 x 5120 201 / 178 / 169, 32760 x 1536 x 1536 94 / 76 / 72 (with GELU tanh 110 /
+// 98 / 101), 2048 x 1024 x 5120 25.5 / 23.0 / 24.3, 1024 x 1536 x 1536 14.0 / 15.1 / 15.7.
+// Of 13 sizes with K from 512 to 20480, with and without GELU, the choice was the fastest or
+// within 4 % of it.
 int choose_tile_n(long long m_tiles, long long N) {
   int best = 0;
   long long best_cost = 0;
@@ -54,18 +59,22 @@ int choose_tile_n(long long m_tiles, long long N) {
 }
 
 // Token tile and K split of the channel-major form, and whether it is the form for a
-// problem (its rows' alignment aside). Measured on GB300, us a call, K1 against it:
+// problem (its rows' alignment aside). Measured on GB300, us a call in a captured graph (for
+// K1 with the scales' repack), K1 against it:
 //   T, K, N            K1     token tile / split
-//   1, 5120, 5120      40     12.4 (16/4)
-//   16, 5120, 20480    137    23.5 (16/1)
-//   128, 1024, 5120    19.4   12.4 (64/2)
-//   256, 5120, 5120    28.8   20.7 (128/2)
-//   128, 5120, 20480   50     33.0 (128/1)
-//   512, 1024, 5120    18.6   16.5 (128/1)
-//   512, 5120, 5120    26.9   29.0 (128/1)
-//   256, 5120, 20480   51     57.6 (128/1, 320 tiles)
+//   1, 5120, 5120      62     9.2 (16/4)
+//   16, 5120, 20480    114    21.2 (16/1)
+//   64, 5120, 20480    43     22.4 (64/1)
+//   128, 1024, 5120    12.7   8.6 (64/2)
+//   256, 5120, 5120    21.5   18.0 (128/2)
+//   128, 5120, 20480   43     27.6 (128/1)
+//   512, 1024, 5120    14.1   12.6 (128/1)
+//   512, 5120, 5120    23.2   25.7 (128/1)
+//   256, 5120, 20480   43     51.2 (128/1, 320 tiles)
 // It wins while its tiles fit the SMs about once (two CTAs share an SM, at the expense of
-// each other's loads); smaller token tiles add CTAs while there are few.
+// each other's loads); smaller token tiles add CTAs while there are few. (K1 is slow where
+// no tile has more than 16 rows, 53 to 121 us; a ragged last panel of tokens costs it what
+// a whole one does: 513, 640 and 768 tokens, 5120 x 20480, 68 to 70.)
 bool choose_few(const GemmShape& g, int* token_tile, int* split) {
   const long long channel_tiles = (g.I + 127) / 128;
   int nt = 16;
@@ -219,7 +228,10 @@ int qkv_cte_linear_run(qkv_cte_linear_plan_t plan, const void* A, const float* a
   lin.wide = aligned(O, 32) && (lin.ldo * e) % 32 == 0 &&
              (!residual || (aligned(residual, 32) && (lin.ldr * e) % 32 == 0));
   lin.pairs = aligned(O, 2 * e) && lin.ldo % 2 == 0 && (!residual || (aligned(residual, 2 * e) && lin.ldr % 2 == 0));
-  // K1 would store rows off 32-byte boundaries element by element
+  // K1 would store rows off 32-byte boundaries element by element, a row of its own for each
+  // lane. us a call, K1 so / channel-major / K1 on whole rows of one column more: 2048 x 5120 x
+  // 5119 124 / 72 / 49, 4096 x 5120 x 20479 817 / 493 / 264, 32760 x 5120 x 5119 1537 / 822 / 493,
+  // 32760 x 512 x 5119 1349 / 328 / 169.
   const bool few = plan->few || (!lin.wide && (g.T + plan->token_tile - 1) / plan->token_tile <= 65535);
   uint8_t* sf_packed = ws + plan->ws.sf_off;
   CUtensorMap tmA, tmW, tmSF;

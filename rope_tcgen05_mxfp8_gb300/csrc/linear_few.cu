@@ -17,8 +17,9 @@
 // What bounds it: about 8 us of launch, set-up, joining and storing, then 0.33 us per
 // 128-byte K block and CTA whatever the token tile up to 64: the MMAs are too small to
 // hide their issue (80 cycles each; 300 more per ring stage for its barriers). The loads
-// are not the limit: one token, K = 5120, N = 20480 takes 23.5 us where reading W takes
-// 16.0 at the measured copy rate; N = 5120 with K split four ways 12.4 us (floor 4.0).
+// are not the limit: one token, K = 5120, N = 20480 takes 20.7 us in a captured graph (23.5
+// launched one by one) where reading W takes 16.0 at the measured copy rate; N = 5120 with K
+// split four ways 9.2 us (12.4; floor 4.0).
 //
 // The tokens carry no block scales (their scale is the fp32 row scale): their side's
 // scale factors are the constant 2^0. Every wait is bounded as in K1.

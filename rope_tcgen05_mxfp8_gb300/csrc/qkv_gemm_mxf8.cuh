@@ -479,7 +479,9 @@ __device__ __forceinline__ void epilogue_drain_plain(const GemmShape& g, const G
 // with one, activation and residual took longer than the MMAs up to K of about 5000.
 // 32760 x 5120 x 5120 with gate and residual: 825 us with parameters from global memory,
 // 595 with them in shared memory and the residual ahead, 577 with two warps per quarter
-// (2.98 PFLOP/s; without residual and gate 526); 32760 x 1024 x 5120: 472 -> 328.
+// (2.98 PFLOP/s; without residual and gate 526, now 493); 32760 x 1024 x 5120: 472 -> 328,
+// and 310 (184 without) with a kind of its own for fp32: the epilogue bounds it there, each
+// lane storing 32 bytes of a row of its own (floor 104 and 92).
 constexpr int kLinearAhead = 64;  // columns
 
 template <int BN, bool kF32>
