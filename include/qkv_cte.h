@@ -507,6 +507,117 @@ int qkv_cte_linear_run(qkv_cte_linear_plan_t plan, const void* A, const float* a
                        const void* residual, int64_t residual_row_stride, void* O, int64_t out_row_stride,
                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A cache of keys and values in 8 bits, and attention over it: what becomes of the
+ * projection's output. Keys and values that many calls read (a context over all steps, the
+ * frames made so far, a sequence that grows) are held as e4m3 codes in pages of tokens; each
+ * page and head has one scale for K and one for V. Additions of this library, with the rules
+ * of the operators above.
+ *
+ * Pool. k_codes and v_codes hold [pages, n_kv_heads, block_tokens, d_head] codes (16-byte
+ * aligned), k_sf and v_sf [pages, n_kv_heads] UE8M0 scales: a value is code * 2^(sf - 127).
+ * A scale of 255 is NaN, and so is every value of that page and head. The pool needs no
+ * preparation: a slot is read only where a sequence has a token.
+ *
+ * Table. Block j of sequence b (its tokens j * block_tokens ...) is page
+ * table[b * table_stride + j], j < max_blocks; without a table, page b * max_blocks + j. A
+ * stride of 0: every sequence reads the same pages. An entry that is no page of the pool
+ * (-1, say) is a hole: its tokens are not attended, read as zeros, and what is written there
+ * is dropped. Tokens past max_blocks * block_tokens are treated likewise, and a length beyond
+ * that counts as that.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int64_t pages;         /* <= INT32_MAX */
+    int32_t n_kv_heads;    /* <= 65535 */
+    int32_t d_head;        /* a multiple of 16, <= 128 */
+    int32_t block_tokens;  /* tokens per page: 16, 32, 64 or 128 */
+    uint32_t flags;        /* 0 or QKV_CTE_FLAG_TEST_STALL */
+} qkv_cte_cache_desc;
+
+typedef struct {
+    uint8_t* k_codes;
+    uint8_t* k_sf;
+    uint8_t* v_codes;
+    uint8_t* v_sf;
+    const int32_t* table;  /* or NULL */
+    int64_t table_stride;  /* elements from one sequence's row to the next, or 0 */
+    int32_t max_blocks;    /* pages per sequence; max_blocks * block_tokens < 2^31 - 1024 */
+} qkv_cte_cache_pages;
+
+typedef struct qkv_cte_cache_plan_s* qkv_cte_cache_plan_t;
+
+/* Validate `desc` (host only) and create a plan; reports the bytes of the codes and of the
+ * scales of K (V has as many; either pointer may be NULL). The plan holds host memory only
+ * and may be used by any number of threads and streams at once. Returns 0, -1 or -2. */
+int qkv_cte_cache_plan(qkv_cte_cache_plan_t* out, const qkv_cte_cache_desc* desc, size_t* code_bytes,
+                       size_t* scale_bytes);
+
+/* Release a plan. NULL is a no-op. */
+void qkv_cte_cache_destroy(qkv_cte_cache_plan_t plan);
+
+/* Quantise keys and values into the cache: row s < counts[b] of sequence b becomes its token
+ * starts[b] + s. For each page and head that receives tokens:
+ *   E = the least exponent (1 to 254) with max|x| <= 448 * 2^(E - 127) over its new tokens,
+ *       255 if one of them is not finite;
+ *   where the page holds earlier tokens of the sequence (starts[b] lies inside it) E is at
+ *   least the old scale, and their codes become e4m3(code * 2^(old - E));
+ *   code = e4m3(x * 2^(127 - E)), to nearest even; zeros where E is 255.
+ * Slots behind the new tokens keep what they hold. Appending token by token thus ends with the
+ * scales of one write of the whole, up to the rounding of codes that were moved.
+ *
+ * k, v   : dtype [batch, seq, n_kv_heads, d_head] with the strides given in elements (lanes
+ *          contiguous), such as the K and V columns of the projection's output; one of them
+ *          may be NULL. Rows on 16-byte boundaries run fastest.
+ * starts : int32 [batch]; tokens before 0 are dropped. counts: int32 [batch], or NULL: seq
+ * The pages that one call writes must be distinct (else their contents are undefined), and
+ * calls that write and read the same pages must not overlap on the GPU. Returns 0, -1, -2,
+ * -3 or -4. No rows: nothing is launched. */
+int qkv_cte_cache_write(qkv_cte_cache_plan_t plan, const qkv_cte_cache_pages* pages, const void* k,
+                        int64_t k_batch_stride, int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                        int64_t v_batch_stride, int64_t v_row_stride, int64_t v_head_stride, int64_t batch,
+                        int64_t seq, const int32_t* starts, const int32_t* counts, int32_t dtype, void* stream);
+
+/* Tokens starts[b] + s, s < seq, of each sequence as dtype (rounded once): row s of k and v.
+ * Rows of tokens before 0, at or past lengths[b], or in holes are zeros. Strides and NULL as
+ * for qkv_cte_cache_write; the elements of k and v must be distinct. */
+int qkv_cte_cache_read(qkv_cte_cache_plan_t plan, const qkv_cte_cache_pages* pages, void* k,
+                       int64_t k_batch_stride, int64_t k_row_stride, int64_t k_head_stride, void* v,
+                       int64_t v_batch_stride, int64_t v_row_stride, int64_t v_head_stride, int64_t batch,
+                       int64_t seq, const int32_t* starts, const int32_t* lengths, int32_t dtype, void* stream);
+
+/* Attention over the cache: for query head i and key head i / (n_q_heads / n_kv_heads)
+ *   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q . k_t),  lse = log(sum_t p_t)
+ * over the tokens t that the query sees. The queries are the last tokens of their sequence:
+ * row s < counts[b] stands at position lengths[b] - counts[b] + s. It sees every t <
+ * lengths[b]; with causal = 1 only t <= its position, and of these with window > 0 only the
+ * last `window`. A row that sees nothing, and rows from counts[b] on, become zeros with an lse
+ * of -infinity. Products and statistics are fp32, the weights are rounded to fp16 before they
+ * multiply the values, out is rounded once.
+ *
+ * q, out    : dtype (bf16 or fp16) [batch, seq, n_q_heads, d_head] with strides in elements,
+ *             lanes contiguous; out's elements are distinct and overlap nothing else (column
+ *             ranges of one wide tensor do not). lse: fp32 [batch, seq, n_q_heads] or NULL
+ * lengths   : int32 [batch], tokens of each sequence in the cache; counts: int32 [batch], or
+ *             NULL: seq
+ * max_length: a length that no sequence is expected to pass. Only how the keys are divided
+ *             depends on it (a graph captured with it may replay with other lengths).
+ * workspace : qkv_cte_cache_attention_workspace bytes, 256-byte aligned, its contents need no
+ *             preparation; may be NULL where that is 0. Calls that overlap on the GPU must not
+ *             share it.
+ * status    : a device word, zero before its first use, which a call sets but never clears
+ *             when a bounded wait runs out: qkv_cte_status(status, stream) reads it
+ * Returns 0, -1, -2, -3 or -4. */
+int qkv_cte_cache_attention(qkv_cte_cache_plan_t plan, const qkv_cte_cache_pages* pages, const void* q,
+                            int64_t q_batch_stride, int64_t q_row_stride, int64_t q_head_stride, void* out,
+                            int64_t out_batch_stride, int64_t out_row_stride, int64_t out_head_stride, float* lse,
+                            int64_t batch, int64_t seq, int32_t n_q_heads, const int32_t* lengths,
+                            const int32_t* counts, int64_t max_length, float scale, int32_t causal, int32_t window,
+                            int32_t dtype, void* workspace, size_t workspace_bytes, uint32_t* status, void* stream);
+
+/* Workspace bytes of qkv_cte_cache_attention (host only). Returns 0, -1 or -2. */
+int qkv_cte_cache_attention_workspace(qkv_cte_cache_plan_t plan, int64_t batch, int64_t seq, int32_t n_q_heads,
+                                      int64_t max_length, size_t* bytes);
+
 /* Release a plan. NULL is a no-op. */
 void qkv_cte_destroy(qkv_cte_plan_t plan);
 

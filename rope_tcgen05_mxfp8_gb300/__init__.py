@@ -23,3 +23,4 @@ from .block_ops import (  # noqa: F401
     qkv_cte_layer_norm_backward,
     qkv_cte_layer_norm_backward_workspace, qkv_cte_linear_desc, qkv_cte_rope_desc,
 )
+from .kv_cache import QkvCteCache, qkv_cte_cache_desc, qkv_cte_cache_pages  # noqa: F401

@@ -3,10 +3,10 @@
 #include <climits>
 #include <cmath>
 #include <new>
-#include <utility>
 
 #include "api_common.h"
 #include "block_ops.h"
+#include "heads_tensor.h"
 #include "internal.h"
 #include "qkv_cte.h"
 
@@ -65,34 +65,6 @@ int check_tensor(const void* p, int64_t stride, int64_t rows, int32_t cols, size
                 name, cols);
   if (stride > INT64_MAX / 8 / (rows > 0 ? rows : 1))
     return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: size of %s overflows", who, name);
-  return QKV_CTE_OK;
-}
-
-// Extents of a [batch, seq, heads, d] tensor (elements), from the strides of its first
-// three dimensions. `distinct` demands that no two elements share an address.
-struct Strided {
-  int64_t stride, size;
-};
-
-int rope_tensor(const void* p, int64_t sb, int64_t ss, int64_t sh, const qkv_cte_rope_desc& d, int64_t batch,
-                int64_t seq, int64_t heads, size_t elem, bool distinct, const char* name, size_t* bytes) {
-  const char* who = "qkv_cte_rope_apply";
-  if (p == nullptr) return fail(QKV_CTE_ERR_INVALID, "%s: null %s", who, name);
-  if (!aligned(p, elem)) return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: %s is not aligned to its elements", who, name);
-  Strided dims[3] = {{sb, batch}, {ss, seq}, {sh, heads}};
-  for (int i = 1; i < 3; ++i)  // by stride, ascending
-    for (int j = i; j > 0 && dims[j].stride < dims[j - 1].stride; --j) std::swap(dims[j], dims[j - 1]);
-  int64_t extent = d.d_head;
-  for (const Strided& t : dims) {
-    if (t.size <= 1) continue;
-    if (t.stride < 0) return fail(QKV_CTE_ERR_INVALID, "%s: negative stride of %s", who, name);
-    if (distinct && t.stride < extent)
-      return fail(QKV_CTE_ERR_INVALID, "%s: the strides of %s make its elements overlap", who, name);
-    if (t.stride > (INT64_MAX / 16 - extent) / (t.size - 1))
-      return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: size of %s overflows", who, name);
-    extent += t.stride * (t.size - 1);
-  }
-  *bytes = (size_t)extent * elem;
   return QKV_CTE_OK;
 }
 
@@ -213,24 +185,14 @@ int qkv_cte_rope_apply(qkv_cte_rope_plan_t plan, const void* x, int64_t x_batch_
   if (batch * seq * heads == 0) return ok();
   const size_t e = elem_size(dtype);
   size_t xn = 0, yn = 0;
-  rc = rope_tensor(x, x_batch_stride, x_row_stride, x_head_stride, plan->d, batch, seq, heads, e, false, "x", &xn);
-  if (rc != QKV_CTE_OK) return rc;
-  rc = rope_tensor(y, y_batch_stride, y_row_stride, y_head_stride, plan->d, batch, seq, heads, e, true, "y", &yn);
-  if (rc != QKV_CTE_OK) return rc;
+  const HeadsView vx{x, x_batch_stride, x_row_stride, x_head_stride, batch, seq, heads, plan->d.d_head, e};
+  const HeadsView vy{y, y_batch_stride, y_row_stride, y_head_stride, batch, seq, heads, plan->d.d_head, e};
+  if ((rc = check_heads(vx, false, "x", who, &xn)) != QKV_CTE_OK) return rc;
+  if ((rc = check_heads(vy, true, "y", who, &yn)) != QKV_CTE_OK) return rc;
   const bool same = x == y && (batch == 1 || x_batch_stride == y_batch_stride) &&
                     (seq == 1 || x_row_stride == y_row_stride) && (heads == 1 || x_head_stride == y_head_stride);
-  if (!same && overlaps(x, xn, y, yn)) {
-    // two column ranges of one wide [batch * seq, ...] tensor lie side by side
-    const bool rows = (batch == 1 || (x_batch_stride == seq * x_row_stride && y_batch_stride == seq * y_row_stride)) &&
-                      (heads == 1 || (x_head_stride >= 0 && y_head_stride >= 0));
-    const int64_t one = (int64_t)e;
-    const Rows rx{x, batch * seq, x_row_stride * one,
-                  ((int64_t)(heads > 1 ? (heads - 1) * x_head_stride : 0) + plan->d.d_head) * one};
-    const Rows ry{y, batch * seq, y_row_stride * one,
-                  ((int64_t)(heads > 1 ? (heads - 1) * y_head_stride : 0) + plan->d.d_head) * one};
-    if (!rows || rx.row_bytes > rx.stride || ry.row_bytes > ry.stride || rows_overlap(rx, ry))
-      return fail(QKV_CTE_ERR_INVALID, "%s: x and y overlap without being the same elements", who);
-  }
+  if (!same && heads_overlap(vx, xn, vy, yn))
+    return fail(QKV_CTE_ERR_INVALID, "%s: x and y overlap without being the same elements", who);
   const void* from = grids != nullptr ? static_cast<const void*>(grids) : positions;
   if (overlaps(y, yn, from, src)) return fail(QKV_CTE_ERR_INVALID, "%s: y overlaps the positions", who);
   DeviceInfo dev;

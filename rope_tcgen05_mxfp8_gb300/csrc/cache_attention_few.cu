@@ -1,0 +1,415 @@
+// Attention of few queries over the 8-bit cache, and the joining of the keys' parts.
+//
+//   z_t = c q . k_t,  p_t = 2^(z_t - m),  o = sum_t p_t v_t / sum_t p_t
+// with c = scale log2(e) and m the running maximum: one pass over the keys.
+//
+// With a few query rows per key head (a token of each sequence, times the query heads that
+// share a key head) the cache is read once and the read is all that counts. A warp takes 32
+// keys at a time and multiplies them with up to 16 rows by warp-level tensor instructions
+// (m16n8k16, fp16 in, fp32 out): the codes become fp16 exactly, and the instruction wants
+// them in registers, where the global loads put them. No shared memory, no barrier and no
+// conversion pass stands between memory and the product. tcgen05 would want the same codes
+// converted and stored to shared memory first, for a tile whose 128 rows would be mostly
+// padding.
+//
+// Layouts. Lane 4g + t holds column g of the B operand and rows g, g + 8 of A and C.
+//   Scores: B's column g is key g; a lane reads 16-byte pieces t, t + 4 of its key's row, so
+//   an instruction's 16 contracted lanes are bytes 4w .. 4w + 3 of the four lanes' pieces
+//   (the order of a contraction is free; the queries are loaded in the same one).
+//   Values: B's rows are keys 2t, 2t + 1, 2t + 8, 2t + 9, as the scores come out; a lane reads
+//   the 16-byte piece g of those four keys, byte j of it being column g of the j-th of 16
+//   products: its output columns are 16 g + j.
+//
+// Numerics. Queries are fp16 after a power of two per row (exact but for what is 2^-28 of the
+// row's largest), codes are exact, products and sums fp32. Each key's block scales multiply
+// its score and its weight in fp32. Weights are rounded to fp16 (2^-11) relative to the
+// largest value scale so far, 2^14 above, so that 28 binary orders below it keep their digits.
+#include "kv_cache.cuh"
+#include "qkv_cte.h"
+#include "vec_io.cuh"
+
+namespace qkvcte {
+
+namespace {
+
+constexpr int kFewWarps = 4;
+constexpr int kFewKeys = 32;       // keys a warp takes at a time
+constexpr int kWeightBias = 14;    // weights are held 2^14 above their value
+constexpr int kPitch = 132;        // floats per row of the warps' partial outputs (banks)
+
+__device__ __forceinline__ void mma_16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));  // 2 ulp
+  return y;
+}
+
+__device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// Where 16 keys lie: their page (or none) and both scales.
+struct KeyGroup {
+  long long row;   // (page * heads + head) * block_tokens + slot, or -1
+  int ek, ev;
+
+  __device__ __forceinline__ void find(const CachePool& p, int b, int h, int key) {
+    const long long page = cache_page(p, b, key >> p.log_bt);
+    row = -1;
+    ek = ev = 1;
+    if (page >= 0) {
+      const long long ph = page * p.heads + h;
+      row = (ph << p.log_bt) + (key & ((1 << p.log_bt) - 1));
+      ek = __ldg(p.k_sf + ph);
+      ev = __ldg(p.v_sf + ph);
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ float query_elem(const T* p) {
+  return to_f32(*p);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(const CacheAttentionArgs a) {
+  __shared__ float s_o[kFewWarps][kCacheFewRows][kPitch];
+  __shared__ float s_m[kFewWarps][kCacheFewRows], s_l[kFewWarps][kCacheFewRows];
+  __shared__ int s_ev[kFewWarps];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  long long item = blockIdx.x;
+  const int split = static_cast<int>(item % a.splits);
+  item /= a.splits;
+  const int h = static_cast<int>(item % a.pool.heads);
+  item /= a.pool.heads;
+  const int tile = static_cast<int>(item % a.row_tiles);
+  const int b = static_cast<int>(item / a.row_tiles);
+  const int rows = a.seq * a.group;  // of this key head
+  const int r0 = tile * kCacheFewRows;
+  const int pieces = a.pool.d >> 4;  // 16-byte pieces of a code row
+
+  // what the tile's rows see: from the first row's first key to the last row's last
+  const Visible vis(a, b);
+  const int s_first = r0 / a.group;
+  int s_last = (r0 + kCacheFewRows - 1) / a.group;
+  if (s_last > vis.count - 1) s_last = vis.count - 1;
+  const int lo = vis.lo(a, s_first);
+  const int hi = s_first > s_last ? 0 : vis.hi(a, s_last);
+  const int c_begin = lo / kFewKeys, c_end = hi > lo ? (hi + kFewKeys - 1) / kFewKeys : c_begin;
+  const int n_chunks = c_end - c_begin;
+  const int c0 = c_begin + static_cast<int>(static_cast<long long>(n_chunks) * split / a.splits);
+  const int c1 = c_begin + static_cast<int>(static_cast<long long>(n_chunks) * (split + 1) / a.splits);
+
+  // queries: rows g and g + 8, elements 64 i + 16 t + 4 w .. + 3
+  uint32_t qf[8][4];
+  float coef[2];
+  int row_lo[2], row_hi[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = r0 + g + 8 * k;
+    const int s = r / a.group;
+    const bool live = r < rows && s < vis.count;
+    row_lo[k] = live ? vis.lo(a, s) : 0;
+    row_hi[k] = live ? vis.hi(a, s) : 0;
+    const T* p = static_cast<const T*>(a.q.p) + b * a.q.sb + s * a.q.ss + (h * a.group + r % a.group) * a.q.sh;
+    float x[32];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        x[16 * i + j] = live && 4 * i + t < pieces ? query_elem(p + 64 * i + 16 * t + j) : 0.0f;
+        top = max(top, __float_as_uint(x[16 * i + j]) & 0x7FFFFFFFu);
+      }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int f = query_factor_field(top);
+    const float up = scale_value(f);
+    coef[k] = a.scale_log2 * scale_value(254 - f);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      qf[n][k] = pack_pair<__half>(make_float2(x[4 * n] * up, x[4 * n + 1] * up));
+      qf[n][2 + k] = pack_pair<__half>(make_float2(x[4 * n + 2] * up, x[4 * n + 3] * up));
+    }
+  }
+  // keys of [all_lo, all_hi) are seen by every live row
+  const int all_lo = vis.lo(a, s_last < 0 ? 0 : s_last), all_hi = vis.hi(a, s_first);
+
+  float o[16][4];
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[j][k] = 0.0f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  int ref = 1;  // exponent of the largest value scale so far
+
+  KeyGroup now[2], next[2];
+  uint4 kr[4][2], vr[2][4];
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto find = [&](KeyGroup (&kg)[2], int c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      kg[i].row = -1;
+      kg[i].ek = kg[i].ev = 1;
+      const int key = c * kFewKeys + 16 * i;
+      if (c < c1 && key < hi) kg[i].find(a.pool, b, h, key);
+    }
+  };
+  auto load_k = [&](const KeyGroup (&kg)[2]) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        kr[n][i] = kg[n >> 1].row >= 0 && 4 * i + t < pieces
+                       ? ld_codes(a.pool.k + (kg[n >> 1].row + 8 * (n & 1) + g) * a.pool.d + 64 * i + 16 * t)
+                       : zero;
+  };
+  // rows of V past the sequence's end may hold anything: they count as zeros
+  auto load_v = [&](const KeyGroup (&kg)[2], int c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int slot = 2 * t + (n & 1) + 8 * (n >> 1);
+        vr[i][n] = kg[i].row >= 0 && g < pieces && c * kFewKeys + 16 * i + slot < vis.length
+                       ? ld_codes(a.pool.v + (kg[i].row + slot) * a.pool.d + 16 * g)
+                       : zero;
+      }
+  };
+
+  int c = c0 + warp;
+  find(now, c);
+  load_k(now);
+  load_v(now, c);
+  for (; c < c1; c += kFewWarps) {
+    find(next, c + kFewWarps);
+    // scores
+    float z[4][4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) z[n][k] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t word = w == 0 ? kr[n][i].x : w == 1 ? kr[n][i].y : w == 2 ? kr[n][i].z : kr[n][i].w;
+          mma_16816(z[n], qf[4 * i + w], codes_to_half2(word), codes_hi_to_half2(word));
+        }
+    load_k(next);
+
+    // scale, mask, maximum
+    const int key0 = c * kFewKeys;
+    const bool whole = key0 >= all_lo && key0 + kFewKeys <= all_hi && now[0].row >= 0 && now[1].row >= 0;
+    float top[2] = {m[0], m[1]};
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const float sk = scale_value(now[n >> 1].ek);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int key = key0 + 8 * n + 2 * t + (k & 1);
+        z[n][k] *= coef[k >> 1] * sk;
+        if (!whole && !(key >= row_lo[k >> 1] && key < row_hi[k >> 1] && now[n >> 1].row >= 0)) z[n][k] = -INFINITY;
+        top[k >> 1] = fmaxf(top[k >> 1], z[n][k]);
+      }
+    }
+    int newref = ref;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (now[i].row >= 0 && now[i].ev != kScaleNan) newref = max(newref, now[i].ev);
+    float use[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      top[k] = quad_max(top[k]);
+      use[k] = top[k] == -INFINITY ? 0.0f : top[k];
+      const float keep = exp2_fast(m[k] - use[k]);
+      m[k] = top[k];
+      l[k] *= keep;
+      const float ko = keep * scale_value(max(127 - (newref - ref), 1));
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        o[j][2 * k] *= ko;
+        o[j][2 * k + 1] *= ko;
+      }
+    }
+    ref = newref;
+    // weights and values
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float fv = now[i].ev == kScaleNan ? scale_value(kScaleNan)
+                                              : scale_value(max(127 + kWeightBias + now[i].ev - ref, 1));
+      uint32_t pa[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        float p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float zz = z[2 * i + n][k];
+          const float e = exp2_fast(zz - use[k >> 1]);
+          l[k >> 1] += e;
+          p[k] = !whole && zz == -INFINITY ? 0.0f : e * fv;  // (a scale that is NaN shows where it is seen)
+        }
+        pa[2 * n] = pack_pair<__half>(make_float2(p[0], p[1]));
+        pa[2 * n + 1] = pack_pair<__half>(make_float2(p[2], p[3]));
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t q[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) q[n] = w == 0 ? vr[i][n].x : w == 1 ? vr[i][n].y : w == 2 ? vr[i][n].z : vr[i][n].w;
+        // bytes of keys 2t and 2t + 1 (2t + 8 and 2t + 9) side by side, per column
+        const uint32_t lo01 = __byte_perm(q[0], q[1], 0x5140), hi01 = __byte_perm(q[0], q[1], 0x7362);
+        const uint32_t lo89 = __byte_perm(q[2], q[3], 0x5140), hi89 = __byte_perm(q[2], q[3], 0x7362);
+        mma_16816(o[4 * w], pa, codes_to_half2(lo01), codes_to_half2(lo89));
+        mma_16816(o[4 * w + 1], pa, codes_hi_to_half2(lo01), codes_hi_to_half2(lo89));
+        mma_16816(o[4 * w + 2], pa, codes_to_half2(hi01), codes_to_half2(hi89));
+        mma_16816(o[4 * w + 3], pa, codes_hi_to_half2(hi01), codes_hi_to_half2(hi89));
+      }
+    }
+    load_v(next, c + kFewWarps);
+    now[0] = next[0];
+    now[1] = next[1];
+  }
+
+  // the warps' parts: element 16 n + j of a row lies at 8 j + n
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    l[k] = quad_sum(l[k]);
+    if (t == 0) {
+      s_m[warp][g + 8 * k] = m[k];
+      s_l[warp][g + 8 * k] = l[k];
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      *reinterpret_cast<float2*>(&s_o[warp][g + 8 * k][8 * j + 2 * t]) = make_float2(o[j][2 * k], o[j][2 * k + 1]);
+  }
+  if (lane == 0) s_ev[warp] = ref;
+  __syncthreads();
+  int top_ev = s_ev[0];
+#pragma unroll
+  for (int w = 1; w < kFewWarps; ++w) top_ev = max(top_ev, s_ev[w]);
+  const int n_rows = rows - r0 < kCacheFewRows ? rows - r0 : kCacheFewRows;
+  const long long all_rows = static_cast<long long>(a.batch) * a.seq * a.q_heads;
+  for (int r = warp; r < n_rows; r += kFewWarps) {
+    const int s = (r0 + r) / a.group;
+    const int head = h * a.group + (r0 + r) % a.group;
+    float mm = s_m[0][r];
+#pragma unroll
+    for (int w = 1; w < kFewWarps; ++w) mm = fmaxf(mm, s_m[w][r]);
+    const float base = mm == -INFINITY ? 0.0f : mm;
+    float wt[kFewWarps], total = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) {
+      const float e = exp2_fast(s_m[w][r] - base);
+      total += s_l[w][r] * e;
+      wt[w] = e * scale_value(max(127 - (top_ev - s_ev[w]), 1));
+    }
+    const bool none = total == 0.0f || s >= vis.count;  // no key seen, or a row of padding: zeros
+    const float inv = none ? 0.0f : 1.0f / total;
+    const long long out_row = (static_cast<long long>(b) * a.seq + s) * a.q_heads + head;
+    const float unit = scale_value(top_ev), unbias = 0x1p-14f;
+    static_assert(kWeightBias == 14, "unbias");
+    T* out = static_cast<T*>(a.out.p) + b * a.out.sb + s * a.out.ss + head * a.out.sh;
+    for (int col = lane; col < a.pool.d; col += 32) {
+      const int at = 8 * (col & 15) + (col >> 4);
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) v += s_o[w][r][at] * wt[w];
+      v = none ? 0.0f : v * inv * unbias * unit;
+      if (a.splits == 1)
+        out[col] = from_f32<T>(v);
+      else
+        a.part_o[(split * all_rows + out_row) * a.pool.d + col] = v;
+    }
+    if (lane == 0) {
+      const float lse2 = none ? -INFINITY : mm + log2f(total);
+      if (a.splits > 1)
+        a.part_lse[split * all_rows + out_row] = lse2;
+      else if (a.lse != nullptr)
+        a.lse[out_row] = lse2 * 0.693147180559945309f;
+    }
+  }
+}
+
+// out = sum_i w_i o_i / sum_i w_i, w_i = 2^(lse_i - max): a warp per row.
+template <typename T>
+__global__ void __launch_bounds__(128) cache_attention_join_kernel(const CacheAttentionArgs a) {
+  const long long all_rows = static_cast<long long>(a.batch) * a.seq * a.q_heads;
+  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= all_rows) return;
+  const int head = static_cast<int>(row % a.q_heads);
+  const long long bs = row / a.q_heads;
+  const int s = static_cast<int>(bs % a.seq), b = static_cast<int>(bs / a.seq);
+  float top = -INFINITY;
+  for (int i = lane; i < a.splits; i += 32) top = fmaxf(top, a.part_lse[i * all_rows + row]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float base = top == -INFINITY ? 0.0f : top;
+  float total = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < a.splits; ++i) {
+    const float lse = a.part_lse[i * all_rows + row];
+    if (lse == -INFINITY) continue;  // that part saw nothing
+    const float w = exp2_fast(lse - base);
+    total += w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (lane + 32 * j < a.pool.d) v[j] += w * a.part_o[(i * all_rows + row) * a.pool.d + lane + 32 * j];
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  T* out = static_cast<T*>(a.out.p) + b * a.out.sb + s * a.out.ss + head * a.out.sh;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (lane + 32 * j < a.pool.d) out[lane + 32 * j] = from_f32<T>(total == 0.0f ? 0.0f : v[j] * inv);
+  if (lane == 0 && a.lse != nullptr)
+    a.lse[row] = total == 0.0f ? -INFINITY : (base + log2f(total)) * 0.693147180559945309f;
+}
+
+template <typename T>
+cudaError_t launch_few(const CacheAttentionArgs& a, cudaStream_t s) {
+  const long long blocks = static_cast<long long>(a.batch) * a.row_tiles * a.pool.heads * a.splits;
+  cache_attention_few_kernel<T><<<static_cast<unsigned>(blocks), kFewWarps * 32, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_join(const CacheAttentionArgs& a, cudaStream_t s) {
+  const long long rows = static_cast<long long>(a.batch) * a.seq * a.q_heads;
+  cache_attention_join_kernel<T><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attention_few(const CacheAttentionArgs& a, int dtype, cudaStream_t s) {
+  return dtype == QKV_CTE_DTYPE_BF16 ? launch_few<__nv_bfloat16>(a, s) : launch_few<__half>(a, s);
+}
+
+cudaError_t launch_cache_attention_join(const CacheAttentionArgs& a, int dtype, cudaStream_t s) {
+  return dtype == QKV_CTE_DTYPE_BF16 ? launch_join<__nv_bfloat16>(a, s) : launch_join<__half>(a, s);
+}
+
+}  // namespace qkvcte
