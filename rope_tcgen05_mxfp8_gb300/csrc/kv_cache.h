@@ -50,21 +50,23 @@ struct CacheAttentionArgs {
   const int* lengths;    // [batch]
   const int* counts;     // [batch] or null (seq)
   int batch, seq, q_heads, group;  // group: query heads per key head
-  int row_tiles;         // tiles of seq * group rows per (batch, key head)
+  int row_tiles;         // tiles of the seq * group rows of a (batch, key head): of 16, or pairs of 128
   int splits;            // parts of the keys
   float scale_log2;      // softmax scale * log2(e)
   int causal, window;    // window 0: none
-  int wide;              // rows of q start on 16-byte boundaries
+  int wide, wide_out;    // rows of q, of out start on 16-byte boundaries
   float* part_o;         // splits > 1: [splits][batch * seq * q_heads][d], each part normalised
   float* part_lse;       // splits > 1: [splits][batch * seq * q_heads], base 2
   uint32_t* status;
   uint32_t flags;
 };
 
-// Rows of a tile of the form for few queries.
+// Rows a block takes: of the form for few queries, of the form on the tensor cores.
 constexpr int kCacheFewRows = 16;
+constexpr int kCachePairRows = 256;
 
 cudaError_t launch_cache_attention_few(const CacheAttentionArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_cache_attention_tiles(const CacheAttentionArgs& a, int dtype, cudaStream_t s);
 // Joins the parts of the keys.
 cudaError_t launch_cache_attention_join(const CacheAttentionArgs& a, int dtype, cudaStream_t s);
 

@@ -165,6 +165,7 @@ int copy_call(qkv_cte_cache_plan_t plan, const qkv_cte_cache_pages* pages, Heads
 
 // How an attention call is divided.
 struct AttentionShape {
+  bool few;
   int row_tiles, splits;
 };
 
@@ -173,9 +174,11 @@ AttentionShape attention_shape(const qkv_cte_cache_desc& d, int64_t batch, int64
   AttentionShape s;
   if (max_length > kMaxPositions) max_length = kMaxPositions;
   const int64_t rows = seq * (n_q_heads / d.n_kv_heads);
-  s.row_tiles = static_cast<int>((rows + kCacheFewRows - 1) / kCacheFewRows);
+  s.few = rows <= kCacheFewRows;
+  const int per = s.few ? kCacheFewRows : kCachePairRows;
+  s.row_tiles = static_cast<int>((rows + per - 1) / per);
   const int64_t items = batch * d.n_kv_heads * s.row_tiles;
-  int64_t splits = (608 + items - 1) / (items > 0 ? items : 1);
+  int64_t splits = s.few ? (608 + items - 1) / (items > 0 ? items : 1) : 152 / (items > 0 ? items : 1);
   const int64_t most = (max_length + 255) / 256;
   if (splits > most) splits = most;
   s.splits = static_cast<int>(splits < 1 ? 1 : splits > kMaxSplits ? kMaxSplits : splits);
@@ -336,6 +339,7 @@ int qkv_cte_cache_attention(qkv_cte_cache_plan_t plan, const qkv_cte_cache_pages
   a.causal = causal;
   a.window = window;
   a.wide = wide_rows(a.q, e);
+  a.wide_out = wide_rows(a.out, e);
   a.status = status;
   a.flags = plan->d.flags;
   if (s.splits > 1) {
@@ -343,7 +347,7 @@ int qkv_cte_cache_attention(qkv_cte_cache_plan_t plan, const qkv_cte_cache_pages
     a.part_lse = a.part_o + static_cast<size_t>(s.splits) * rows * plan->d.d_head;
   }
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  cudaError_t err = launch_cache_attention_few(a, dtype, cs);
+  cudaError_t err = s.few ? launch_cache_attention_few(a, dtype, cs) : launch_cache_attention_tiles(a, dtype, cs);
   if (err == cudaSuccess && s.splits > 1) err = launch_cache_attention_join(a, dtype, cs);
   if (err != cudaSuccess) return fail(QKV_CTE_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(err));
   return ok();
