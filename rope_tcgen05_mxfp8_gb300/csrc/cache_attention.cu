@@ -4,17 +4,21 @@
 // with c = scale log2(e) and a running reference m per row: one pass over the keys, nothing
 // of the score matrix leaves the SM.
 //
-// A CTA owns two tiles of 128 query rows (a row is a token and one of the query heads that
-// share the key head) and walks the keys 128 at a time:
+// A pair of CTAs owns two tiles of 256 query rows (a row is a token and one of the query heads
+// that share the key head), 128 rows of each tile per CTA, and walks the keys 128 at a time:
 //   conversion warps read the codes of K and V, turn them into fp16 (exact: e4m3 is a subset)
-//     and store them swizzled for the tensor cores, a tile ahead;
-//   one thread issues S = Q K^T (both in shared memory) and O += P V (P in tensor memory);
-//   two groups of four softmax warps, a thread per row, take S out of tensor memory, and put
-//     P back over it as fp16.
+//     and store them swizzled for the tensor cores, a tile ahead. Each CTA converts half: 64 of
+//     the keys of K, half of the lanes of V;
+//   one thread of the leading CTA issues S = Q K^T (both in shared memory) and O += P V (P in
+//     tensor memory) as M = 256 instructions over the pair, which read each half where it is;
+//   two groups of four softmax warps per CTA, a thread per row, take S out of tensor memory,
+//     and put P back over it as fp16.
 // The two row tiles take turns: while one is in its softmax the tensor cores work on the
 // other. Codes cannot feed the tensor cores as they are, because both operands of an 8-bit
 // product would have to be 8-bit, and weights and queries rounded to three digits are not
-// attention; the conversion is shared by 256 rows.
+// attention; the conversion is shared by 512 rows. A CTA by itself would need 128 bytes of
+// shared memory a clock for Q K^T alone, all there is (measured: 94 to 113 clocks for an
+// instruction of 64), and its codes in flight would not fit the L1 that its buffers leave.
 //
 // Scales. A key's block scale multiplies its score in fp32. A value's block scale multiplies
 // its weight before the rounding to fp16, relative to the largest value scale so far (an
@@ -35,19 +39,24 @@ namespace qkvcte {
 
 namespace {
 
-constexpr int kTileRows = 128;
+constexpr int kTileRows = 128;     // of a row tile, per CTA
 constexpr int kTileKeys = 128;
+constexpr int kPairRows = kCacheTileRows;
+static_assert(kPairRows == 4 * kTileRows, "two CTAs, two row tiles");
 constexpr int kAttnThreads = 512;  // 2 x 4 softmax warps, 4 conversion warps, the issuing warp and three idle
 constexpr int kStages = 2;
 constexpr int kMetaSlots = 4;
-constexpr int kHalfBytes = kTileKeys * 128;       // 128 rows of 64 fp16
-constexpr int kTileBytes = 2 * kHalfBytes;
+constexpr int kQHalf = kTileRows * 128;           // 128 rows of 64 fp16
+constexpr int kQBytes = 2 * kQHalf;
+constexpr int kKHalf = kTileKeys / 2 * 128;       // this CTA's 64 keys, 64 lanes of them
+constexpr int kKBytes = 2 * kKHalf;
+constexpr int kVBytes = kTileKeys * 128;          // 128 keys, this CTA's lanes of them (64 at most)
 constexpr int kBias = 7;                          // weights are held 2^7 above their value
 constexpr float kGrowth = 8.0f;                   // binary orders the maximum may grow before a rescale
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kSCol = 0, kOCol = 256;        // TMEM columns: S (and P) of both tiles, then O
-// Registers per thread and role: 8 x 176 + 4 x 104 + 4 x 56 = 16 x 128, what the launch has.
-constexpr int kSoftmaxRegs = 176, kConvertRegs = 104, kIssueRegs = 56;
+// Registers per thread and role: 8 x 192 + 4 x 72 + 4 x 56 = 16 x 128, what the launch has.
+constexpr int kSoftmaxRegs = 192, kConvertRegs = 72, kIssueRegs = 56;
 static_assert(8 * kSoftmaxRegs + 4 * kConvertRegs + 4 * kIssueRegs == 16 * 128, "register split");
 
 // What the softmax warps need to know about a tile of keys, by groups of 16.
@@ -70,7 +79,7 @@ struct Smem {
   TileMeta meta[kMetaSlots];
 };
 
-constexpr size_t kSmemBytes = 1024 + 2 * kTileBytes + 2 * kStages * kTileBytes + sizeof(Smem);
+constexpr size_t kSmemBytes = 1024 + 2 * kQBytes + kStages * (kKBytes + kVBytes) + sizeof(Smem);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 template <int kRegs>
@@ -82,32 +91,36 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+// Issued by one lane of a warp that is together, so that descriptors stay in uniform registers:
+// in a branch of one lane every operand is moved there anew (1000 instead of 750 clocks for
+// eight instructions of 64).
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-
-// fp16 x fp16 -> fp32, M = 128; B K-major, or N-major (the values: rows of keys, lanes contiguous).
-__device__ __forceinline__ uint32_t idesc_f16(int n, bool b_n_major) {
-  return (1u << 4) | (b_n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+// Arrive on both CTAs' barrier at this offset when that lane's products so far are done.
+__device__ __forceinline__ void commit_both(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
 }
 
-// An N-major operand in 128-byte swizzled rows of 64 lanes: the next 64 lanes are one half
-// away (leading byte offset), the next 8 keys 1024 bytes (stride byte offset).
-__device__ __forceinline__ uint64_t smem_desc_n_major(uint32_t saddr) {
-  uint64_t d = smem_desc_sw128(saddr);
-  d |= static_cast<uint64_t>(kHalfBytes >> 4) << 16;
-  return d;
+// fp16 x fp16 -> fp32, M = 256; B K-major, or N-major (the values: rows of keys, lanes contiguous).
+__device__ __forceinline__ uint32_t idesc_f16(int n, bool b_n_major) {
+  return (1u << 4) | (b_n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (16u << 24);
 }
 
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t* r) {
@@ -118,11 +131,16 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));  // 2 ulp
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // 2 ulp; below 2^-126 zero (one instruction, not four)
   return y;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -131,16 +149,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-__device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
 __device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// What a CTA works on; every thread finds the same.
+// What a pair of CTAs works on; every thread finds the same.
 struct Work {
   int split, pair, h, b;
 
@@ -159,10 +172,10 @@ struct Work {
 
   __device__ __forceinline__ void plan(const CacheAttentionArgs& a, const Visible& v) {
     rows = a.seq * a.group;
-    r0 = pair * 2 * kTileRows;
-    two = rows - r0 > kTileRows;
+    r0 = pair * kPairRows;
+    two = rows - r0 > kPairRows / 2;
     const int s_first = r0 / a.group;
-    int s_last = (rows - r0 < 2 * kTileRows ? rows - 1 : r0 + 2 * kTileRows - 1) / a.group;
+    int s_last = (rows - r0 < kPairRows ? rows - 1 : r0 + kPairRows - 1) / a.group;
     if (s_last > v.count - 1) s_last = v.count - 1;
     const int lo = v.lo(a, s_first), hi = s_first > s_last ? 0 : v.hi(a, s_last);
     const int t0 = lo / kTileKeys, t1 = hi > lo ? (hi + kTileKeys - 1) / kTileKeys : t0;
@@ -172,89 +185,129 @@ struct Work {
   }
 };
 
-// Every role's waits: bounded, and given up when another role has failed.
+// Every role's waits: bounded, and given up when another role of the CTA has failed.
+__device__ __forceinline__ bool try_wait_held(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(100000)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Smem* sm, uint32_t* status, uint32_t code) {
-  if (mbar_wait_bounded(smem_u32(bar), parity, &sm->abort, kWaitNs)) return true;
+  const uint32_t at = smem_u32(bar);
+  if (try_wait_held(at, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  do {
+    if (try_wait_held(at, parity)) return true;
+  } while (*reinterpret_cast<volatile int*>(&sm->abort) == 0 && globaltimer_ns() - t0 < kWaitNs);
   atomicOr(status, code);
   *reinterpret_cast<volatile int*>(&sm->abort) = 1;
   return false;
 }
 
-// ---------------------------------------------------------------------------------------
-// Conversion: 128 threads; in step i a thread has row 16 i + tid / 8, codes 16 (tid % 8) ...
-// ---------------------------------------------------------------------------------------
-struct CodeTile {
-  uint4 c[8];
+// Arrive on the leading CTA's barrier at this offset. What it announces is read by the tensor
+// cores alone, where it lies, and has been fenced towards them; a release at cluster scope
+// would wait for the thread's loads in flight as well (6000 instead of 3000 clocks a tile).
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0)) : "memory");
+}
 
-  // `limit`: rows from it on are zeros.
-  __device__ __forceinline__ void load(const CachePool& p, const uint8_t* codes, int page, int h, int key0, int tid,
-                                       int pieces, int limit) {
-    const int piece = tid & 7;
+// ---------------------------------------------------------------------------------------
+// Conversion: 128 threads with four pieces of 16 codes of K and of V each. Eight lanes that
+// store together have the same piece of eight rows, which the swizzle spreads over all banks.
+// ---------------------------------------------------------------------------------------
+struct CodePieces {
+  uint4 c[4];
+
+  // Piece i lies in the page that lane group0 + step i has (-1: zeros), `slot` rows on.
+  // `codes`: the pool from this thread's head, row and piece on. Zeros where row + rows i >= limit.
+  template <int kRows>
+  __device__ __forceinline__ void load(const CachePool& p, const uint8_t* codes, int page, int group0, int row,
+                                       int first_slot, int limit) {
+    const uint32_t page_bytes = static_cast<uint32_t>(p.heads * p.d) << p.log_bt;  // < 2^30
+    const int mask = (1 << p.log_bt) - 1;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int pg = __shfl_sync(0xffffffffu, page, i);
-      const int row = 16 * i + (tid >> 3);
-      c[i] = make_uint4(0, 0, 0, 0);
-      if (pg >= 0 && piece < pieces && row < limit) {
-        const int slot = (key0 + row) & ((1 << p.log_bt) - 1);
-        const long long at = ((static_cast<long long>(pg) * p.heads + h) << p.log_bt) + slot;
-        c[i] = ld_codes(codes + at * p.d + 16 * piece);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int pg = __shfl_sync(0xffffffffu, page, group0 + kRows / 16 * i);
+      c[i] = ld_codes_if(codes + static_cast<uint64_t>(static_cast<uint32_t>(pg)) * page_bytes +
+                             static_cast<uint32_t>(((first_slot + kRows * i) & mask) * p.d),
+                         pg >= 0 && row + kRows * i < limit);
     }
   }
-  // 16 codes become two 16-byte chunks of a row; which goes first alternates so that eight
-  // lanes of a row hit all banks.
-  __device__ __forceinline__ void store(uint32_t tile, int tid, int pieces) const {
-    const int piece = tid & 7;
-    if (piece >= pieces) return;
-    const int first = piece >> 2;
+  // To two 16-byte chunks of a row, kRows rows apart.
+  template <int kRows>
+  __device__ __forceinline__ void store(uint32_t at) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = 16 * i + (tid >> 3);
-      const uint32_t base = tile + (piece >> 2) * kHalfBytes + row * 128;
-      const uint32_t lo[4] = {codes_to_half2(c[i].x), codes_hi_to_half2(c[i].x), codes_to_half2(c[i].y),
-                              codes_hi_to_half2(c[i].y)};
-      const uint32_t hi[4] = {codes_to_half2(c[i].z), codes_hi_to_half2(c[i].z), codes_to_half2(c[i].w),
-                              codes_hi_to_half2(c[i].w)};
-      const uint32_t chunk = 2 * (piece & 3);
-      const uint32_t at0 = base + (((chunk + first) ^ (row & 7)) << 4);
-      const uint32_t at1 = base + (((chunk + 1 - first) ^ (row & 7)) << 4);
-      st_shared16(at0, first ? hi[0] : lo[0], first ? hi[1] : lo[1], first ? hi[2] : lo[2], first ? hi[3] : lo[3]);
-      st_shared16(at1, first ? lo[0] : hi[0], first ? lo[1] : hi[1], first ? lo[2] : hi[2], first ? lo[3] : hi[3]);
+    for (int i = 0; i < 4; ++i) {
+      st_shared16(at + 128 * kRows * i, codes_to_half2(c[i].x), codes_hi_to_half2(c[i].x), codes_to_half2(c[i].y),
+                  codes_hi_to_half2(c[i].y));
+      st_shared16((at ^ 16) + 128 * kRows * i, codes_to_half2(c[i].z), codes_hi_to_half2(c[i].z),
+                  codes_to_half2(c[i].w), codes_hi_to_half2(c[i].w));
     }
   }
 };
 
 __device__ __forceinline__ void convert_role(const CacheAttentionArgs& a, const Work& w, const Visible& vis, Smem* sm,
-                                             uint32_t s_k, uint32_t s_v) {
+                                             uint32_t s_k, uint32_t s_v, int rank) {
   const int tid = threadIdx.x - 256, lane = tid & 31;
-  const int pieces = a.pool.d >> 4;
   if ((a.flags & QKV_CTE_FLAG_TEST_STALL) != 0) return;  // test hook: hand out nothing
-  // lane i < 8 keeps the page of a tile's i-th group of 16 keys
-  auto find = [&](int j) -> int {
+  // K: rows krow + 16 i of this CTA's 64 keys, piece kp of 8. V: rows vrow + 32 i of the 128
+  // keys, piece vp of this CTA's half of the lanes (of d rounded up to 32). Threads beyond the
+  // lanes store zeros where nothing that counts is read.
+  const int pieces = a.pool.d >> 4;
+  const int krow = (tid & 7) + ((tid >> 2) & 8), kp = ((tid >> 3) & 3) + ((tid >> 4) & 4);
+  const int vrow = (tid & 7) + 8 * (tid >> 5), vp = (tid >> 3) & 3;
+  const int half = (pieces + 1) >> 1;
+  const int vpiece = rank * half + vp;
+  const bool k_mine = kp < pieces, v_mine = vp < half && vpiece < pieces;
+  const int bt = 1 << a.pool.log_bt;
+  const long long head_row = static_cast<long long>(w.h) << a.pool.log_bt;
+  const uint8_t* k_codes = a.pool.k + (head_row + (krow & (bt - 1))) * a.pool.d + 16 * kp;
+  const uint8_t* v_codes = a.pool.v + (head_row + (vrow & 15)) * a.pool.d + 16 * vpiece;
+  const uint32_t k_at = s_k + (kp >> 2) * kKHalf + krow * 128 + (((2 * (kp & 3)) ^ (krow & 7)) << 4);
+  const uint32_t v_at = s_v + vrow * 128 + (((2 * vp) ^ (vrow & 7)) << 4);
+  const int vgroup = tid >> 6;
+  // Lane i < 8 keeps the page of a tile's i-th group of 16 keys. Every load is issued an
+  // iteration before its use: table entries two tiles ahead, scales and codes one.
+  auto entry = [&](int j) -> int {
     const int key = (w.key_tile0 + j) * kTileKeys + 16 * lane;
     if (j >= w.n || lane >= 8 || key >= vis.length) return -1;
-    return static_cast<int>(cache_page(a.pool, w.b, key >> a.pool.log_bt));
+    return cache_entry(a.pool, w.b, key >> a.pool.log_bt);
   };
-  CodeTile k, v;
-  int page = find(0), next = find(1);
-  auto limit = [&](int j) { return vis.length - (w.key_tile0 + j) * kTileKeys; };
-  k.load(a.pool, a.pool.k, page, w.h, w.key_tile0 * kTileKeys, tid, pieces, kTileKeys);
-  v.load(a.pool, a.pool.v, page, w.h, w.key_tile0 * kTileKeys, tid, pieces, limit(0));
+  auto checked = [&](int e) { return e >= 0 && e < a.pool.pages ? e : -1; };
+  int ek = 0, ev = 0;
+  auto scales = [&](int page) {
+    ek = ev = 0;
+    if (page >= 0 && tid < 32) {
+      const size_t ph = static_cast<size_t>(page) * a.pool.heads + w.h;
+      ek = __ldg(a.pool.k_sf + ph);
+      ev = __ldg(a.pool.v_sf + ph);
+    }
+  };
+  // keys past the sequence's end may hold anything: as values they count as zeros
+  CodePieces k, v;
+  auto load_k = [&](int page) { k.load<16>(a.pool, k_codes, page, 4 * rank, krow, 64 * rank, k_mine ? kTileKeys : 0); };
+  auto load_v = [&](int page, int j) {
+    v.load<32>(a.pool, v_codes, page, vgroup, vrow, 16 * vgroup,
+               v_mine ? vis.length - (w.key_tile0 + j) * kTileKeys : 0);
+  };
+  int page = checked(entry(0)), ahead = entry(1);
+  scales(page);
+  load_k(page);
+  load_v(page, 0);
   for (int j = 0; j < w.n; ++j) {
     const int st = j & 1;
     const uint32_t ph = (j >> 1) & 1;
+    const int next = checked(ahead);
+    ahead = entry(j + 2);
     if (!__all_sync(0xffffffffu, wait_for(&sm->k_empty[st], ph ^ 1u, sm, a.status, kErrProducerEmptyWait))) return;
     if (tid < 32) {
       // the slot's last readers have handed in their weights: the issue of the scores that
       // freed this stage came after them
       TileMeta& m = sm->meta[j & (kMetaSlots - 1)];
-      int ek = 0, ev = 0;
-      if (page >= 0) {
-        const size_t at = static_cast<size_t>(page) * a.pool.heads + w.h;
-        ek = __ldg(a.pool.k_sf + at);
-        ev = __ldg(a.pool.v_sf + at);
-      }
       const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
       const uint32_t vnan = __ballot_sync(0xffffffffu, ev == kScaleNan);
       if (ev == kScaleNan) ev = 0;
@@ -271,67 +324,82 @@ __device__ __forceinline__ void convert_role(const CacheAttentionArgs& a, const 
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm->meta_full[j & (kMetaSlots - 1)]));
     }
-    k.store(s_k + st * kTileBytes, tid, pieces);
+    k.store<16>(k_at + st * kKBytes);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sm->k_full[st]));
-    const int key0 = (w.key_tile0 + j + 1) * kTileKeys;
-    k.load(a.pool, a.pool.k, next, w.h, key0, tid, pieces, kTileKeys);
+    if (lane == 0) arrive_leader(&sm->k_full[st]);
+    scales(next);
+    load_k(next);
     if (!__all_sync(0xffffffffu, wait_for(&sm->v_empty[st], ph ^ 1u, sm, a.status, kErrProducerEmptyWait))) return;
-    v.store(s_v + st * kTileBytes, tid, pieces);
+    v.store<32>(v_at + st * kVBytes);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sm->v_full[st]));
-    v.load(a.pool, a.pool.v, next, w.h, key0, tid, pieces, limit(j + 1));
+    if (lane == 0) arrive_leader(&sm->v_full[st]);
+    load_v(next, j + 1);
     page = next;
-    next = find(j + 2);
   }
 }
 
 // ---------------------------------------------------------------------------------------
-// Issue: one thread
+// Issue: one thread of the leading CTA
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ bool issue_all(const CacheAttentionArgs& a, const Work& w, Smem* sm, uint32_t s_q,
-                                          uint32_t s_k, uint32_t s_v, uint32_t tmem) {
-  const int tiles = w.two ? 2 : 1;
+                                          uint32_t s_k, uint32_t s_v) {
+  const uint32_t tmem = 0;  // all columns are this CTA's
+  const int tiles = __shfl_sync(0xffffffffu, w.two ? 2 : 1, 0);
+  const int n = __shfl_sync(0xffffffffu, w.n, 0);
   const int steps = a.pool.d >> 4;
   const uint32_t id_s = idesc_f16(kTileKeys, false);
-  const uint32_t id_o = idesc_f16(a.pool.d > 64 ? 128 : 64, true);
+  const uint32_t id_o = idesc_f16((a.pool.d + 31) & ~31, true);
+  const uint64_t q_desc = smem_desc_sw128(s_q), k_desc = smem_desc_sw128(s_k), v_desc = smem_desc_sw128(s_v);
+  // Straight lines of eight: with a condition around each instruction the scores were wrong
+  // (nvcc 13.0).
   auto scores = [&](int x, int st) {
-    for (int ks = 0; ks < steps; ++ks) {
-      const uint32_t off = (ks >> 2) * kHalfBytes + (ks & 3) * 32;
-      mma_f16_ss(tmem + kSCol + x * 128, smem_desc_sw128(s_q + x * kTileBytes + off),
-                 smem_desc_sw128(s_k + st * kTileBytes + off), id_s, ks > 0 ? 1u : 0u);
+    const uint64_t qd = q_desc + (x * kQBytes >> 4), kd = k_desc + (st * kKBytes >> 4);
+    const uint32_t to = tmem + kSCol + x * 128;
+    auto step = [&](int ks) {
+      mma_f16_ss(to, qd + (((ks >> 2) * kQHalf + (ks & 3) * 32) >> 4), kd + (((ks >> 2) * kKHalf + (ks & 3) * 32) >> 4),
+                 id_s, ks > 0 ? 1u : 0u);
+    };
+    if (steps == 8) {
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) step(ks);
+    } else {
+#pragma unroll 1
+      for (int ks = 0; ks < steps; ++ks) step(ks);
     }
-    tc_commit(smem_u32(&sm->s_full[x]));
+    commit_both(&sm->s_full[x]);
   };
-  if (!wait_for(&sm->k_full[0], 0, sm, a.status, kErrMmaFullWait)) return false;
-  for (int x = 0; x < tiles; ++x) {
-    if (!wait_for(&sm->q_full[x], 0, sm, a.status, kErrMmaFullWait)) return false;
+  // (a wait that one lane gives up, all give up)
+  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
+    const bool ok = __all_sync(0xffffffffu, wait_for(bar, parity, sm, a.status, code));
     tc_fence_after();
+    return ok;
+  };
+  if (!wait(&sm->k_full[0], 0, kErrMmaFullWait)) return false;
+  for (int x = 0; x < tiles; ++x) {
+    if (!wait(&sm->q_full[x], 0, kErrMmaFullWait)) return false;
     scores(x, 0);
   }
-  tc_commit(smem_u32(&sm->k_empty[0]));
-  for (int j = 0; j < w.n; ++j) {
+  commit_both(&sm->k_empty[0]);
+  for (int j = 0; j < n; ++j) {
     const int st = j & 1, st1 = st ^ 1;
-    if (!wait_for(&sm->v_full[st], (j >> 1) & 1, sm, a.status, kErrMmaFullWait)) return false;
+    if (!wait(&sm->v_full[st], (j >> 1) & 1, kErrMmaFullWait)) return false;
     for (int x = 0; x < tiles; ++x) {
-      if (!wait_for(&sm->p_full[x], j & 1, sm, a.status, kErrMmaTmemEmptyWait)) return false;
-      tc_fence_after();
+      if (!wait(&sm->p_full[x], j & 1, kErrMmaTmemEmptyWait)) return false;
+      const uint64_t vd = v_desc + (st * kVBytes >> 4);
+#pragma unroll
       for (int ks = 0; ks < kTileKeys / 16; ++ks)
-        mma_f16_ts(tmem + kOCol + x * 128, tmem + kSCol + x * 128 + 8 * ks,
-                   smem_desc_n_major(s_v + st * kTileBytes + ks * 2048), id_o, (j | ks) != 0 ? 1u : 0u);
-      if (x == tiles - 1) tc_commit(smem_u32(&sm->v_empty[st]));
-      if (j + 1 == w.n) {
-        tc_commit(smem_u32(&sm->o_full[x]));
+        mma_f16_ts(tmem + kOCol + x * 128, tmem + kSCol + x * 128 + 8 * ks, vd + (ks * 2048 >> 4), id_o,
+                   ks > 0 || j > 0 ? 1u : 0u);
+      if (x == tiles - 1) commit_both(&sm->v_empty[st]);
+      if (j + 1 == n) {
+        commit_both(&sm->o_full[x]);
         continue;
       }
-      if (x == 0) {
-        if (!wait_for(&sm->k_full[st1], ((j + 1) >> 1) & 1, sm, a.status, kErrMmaFullWait)) return false;
-        tc_fence_after();
-      }
+      if (x == 0 && !wait(&sm->k_full[st1], ((j + 1) >> 1) & 1, kErrMmaFullWait)) return false;
       scores(x, st1);
-      if (x == tiles - 1) tc_commit(smem_u32(&sm->k_empty[st1]));
+      if (x == tiles - 1) commit_both(&sm->k_empty[st1]);
     }
   }
   return true;
@@ -342,9 +410,10 @@ __device__ __forceinline__ bool issue_all(const CacheAttentionArgs& a, const Wor
 // ---------------------------------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const Work& w, const Visible& vis, Smem* sm,
-                                             uint32_t s_q, uint32_t tmem, int x) {
+                                             uint32_t s_q, uint32_t tmem, int x, int rank) {
   const int row = threadIdx.x & 127;                   // of the tile: also its TMEM lane
-  const int r = w.r0 + x * kTileRows + row;
+  const int first_row = w.r0 + (2 * x + rank) * kTileRows;
+  const int r = first_row + row;
   const int s = r / a.group, head = w.h * a.group + r % a.group;
   const bool inside = r < w.rows;
   const bool live = inside && s < vis.count;
@@ -380,7 +449,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     const int f = query_factor_field(__float_as_uint(unpack_pair<T>(top).x) & 0x7FFFFFFFu);
     const float up = scale_value(f);
     coef = a.scale_log2 * scale_value(254 - f);
-    const uint32_t base = s_q + x * kTileBytes + row * 128;
+    const uint32_t base = s_q + x * kQBytes + row * 128;
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
       uint32_t h[4];
@@ -389,14 +458,16 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
         const float2 v = unpack_pair<T>(q[4 * c + i]);
         h[i] = pack_pair<__half>(make_float2(v.x * up, v.y * up));
       }
-      st_shared16(base + (c >> 3) * kHalfBytes + (((c & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+      st_shared16(base + (c >> 3) * kQHalf + (((c & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
     }
     fence_proxy_async_smem();
-    mbar_arrive(smem_u32(&sm->q_full[x]));
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) arrive_leader(&sm->q_full[x]);
   }
 
-  // keys of [all_lo, all_hi) are seen by every live row of the tile
-  const int first_row = w.r0 + x * kTileRows;
+  // keys of [all_lo, all_hi) are seen by every live row of the tile; without a live row it
+  // does not matter what the scores are
+  const bool dead = first_row >= w.rows || first_row / a.group >= vis.count;
   const int last_row = w.rows - first_row < kTileRows ? w.rows - 1 : first_row + kTileRows - 1;
   const int s_last = last_row / a.group < vis.count - 1 ? last_row / a.group : vis.count - 1;
   const int all_lo = vis.lo(a, s_last < 0 ? 0 : s_last), all_hi = vis.hi(a, first_row / a.group);
@@ -410,46 +481,13 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     if (!__all_sync(0xffffffffu, ok)) return;
     tc_fence_after();
     const TileMeta& meta = sm->meta[slot];
-    float z[kTileKeys];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32 * c, reinterpret_cast<uint32_t*>(z + 32 * c));
-    tmem_ld_wait();
-
     const int key0 = (w.key_tile0 + j) * kTileKeys;
-    const bool whole = key0 >= all_lo && key0 + kTileKeys <= all_hi && meta.there == 0xFFu;
-    // bit i of word c: key 32 c + i is seen
-    uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-    if (!whole) {
-      const uint32_t there = meta.there;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int from = lo - key0 - 32 * c, to = hi - key0 - 32 * c;
-        uint32_t bits = to <= 0 ? 0u : to >= 32 ? ~0u : (1u << to) - 1u;
-        bits &= from <= 0 ? ~0u : from >= 32 ? 0u : ~((1u << from) - 1u);
-        if (!(there >> (2 * c) & 1)) bits &= 0xFFFF0000u;
-        if (!(there >> (2 * c) & 2)) bits &= 0x0000FFFFu;
-        seen[c] = bits;
-      }
-#pragma unroll
-      for (int i = 0; i < kTileKeys; ++i)
-        if (!(seen[i >> 5] >> (i & 31) & 1)) z[i] = -INFINITY;
-    }
-    float c16[8];
-    float top = -INFINITY;
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      c16[g] = coef * meta.ck[g];
-      float t = max3(z[16 * g], z[16 * g + 1], z[16 * g + 2]);
-#pragma unroll
-      for (int i = 3; i < 15; i += 2) t = max3(t, z[16 * g + i], z[16 * g + i + 1]);
-      t = fmaxf(t, z[16 * g + 15]);
-      top = fmaxf(top, t * c16[g]);
-    }
-    const int top_ev = meta.top_ev;
-    if (__any_sync(0xffffffffu, top > m + kGrowth) || top_ev > ref) {
+    // the reference and the sums follow a tile's maximum and largest value scale
+    auto follow = [&](float top) {
+      const int top_ev = meta.top_ev;
+      if (!__any_sync(0xffffffffu, top > m + kGrowth) && top_ev <= ref) return;
       const float now = fmaxf(m, top);
-      const float use = now == -INFINITY ? 0.0f : now;
-      const float keep = exp2_fast(m - use);
+      const float keep = exp2_fast(m - (now == -INFINITY ? 0.0f : now));
       const int newref = max(ref, top_ev);
       if (j > 0) {
         const float f = keep * scale_value(max(127 - (newref - ref), 1));
@@ -465,42 +503,108 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
       l *= keep;
       m = now;
       ref = newref;
-    }
-    const float use = m == -INFINITY ? 0.0f : m;
-    const uint32_t vnan = meta.vnan;
+    };
+    if (dead || (key0 >= all_lo && key0 + kTileKeys <= all_hi && meta.there == 0xFFu && meta.vnan == 0)) {
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float z[32];
+        tmem_ld_32x32b_x32(t_s + 32 * c, reinterpret_cast<uint32_t*>(z));
+        const float2 ck = *reinterpret_cast<const float2*>(&meta.ck[2 * c]);
+        tmem_ld_wait();
+        float t[2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t pk[16];
+        for (int g = 0; g < 2; ++g) {
+          t[g] = max3(z[16 * g], z[16 * g + 1], z[16 * g + 2]);
 #pragma unroll
-      for (int gg = 0; gg < 2; ++gg) {
-        const int g = 2 * c + gg;
-        const int lf = max(meta.ev[g] - ref + kBias, -40);  // further down fp16 holds nothing
-        const float add = static_cast<float>(lf) - use;
-        const float2 cc = make_float2(c16[g], c16[g]), aa = make_float2(add, add);
-        float2 sum = make_float2(0.0f, 0.0f);
+          for (int i = 3; i < 15; i += 2) t[g] = max3(t[g], z[16 * g + i], z[16 * g + i + 1]);
+          t[g] = fmaxf(t[g], z[16 * g + 15]);
+        }
+        top = max3(top, t[0] * (coef * ck.x), t[1] * (coef * ck.y));
+      }
+      follow(top);
+      const float use = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float z[32];
+        uint32_t pk[16];
+        tmem_ld_32x32b_x32(t_s + 32 * c, reinterpret_cast<uint32_t*>(z));
+        const float2 ck = *reinterpret_cast<const float2*>(&meta.ck[2 * c]);
+        const int2 ev = *reinterpret_cast<const int2*>(&meta.ev[2 * c]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int lf = max((g == 0 ? ev.x : ev.y) - ref + kBias, -40);  // further down fp16 holds nothing
+          const float add = static_cast<float>(lf) - use, mul = coef * (g == 0 ? ck.x : ck.y);
+          const float2 cc = make_float2(mul, mul), aa = make_float2(add, add);
+          float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float2 e = ffma2(make_float2(z[16 * g + 2 * i], z[16 * g + 2 * i + 1]), cc, aa);
+            e.x = exp2_fast(e.x);
+            e.y = exp2_fast(e.y);
+            sum = fadd2(sum, e);
+            pk[8 * g + i] = pack_pair<__half>(e);
+          }
+          l = fmaf(sum.x + sum.y, scale_value(127 - lf), l);
+        }
+        tmem_st_32x32b_x16(t_s + 16 * c, pk);
+      }
+    } else {
+      // Masked, or with a NaN among the value scales: 16 keys at a time, scores read twice.
+      // Bit i of `seen`: the row sees key i of the group.
+      const uint32_t there = meta.there, vnan = meta.vnan;
+      auto seen_bits = [&](int g) {
+        const int from = lo - key0 - 16 * g, to = hi - key0 - 16 * g;
+        uint32_t bits = to <= 0 ? 0u : to >= 16 ? 0xFFFFu : (1u << to) - 1u;
+        bits &= from <= 0 ? 0xFFFFu : from >= 16 ? 0u : ~((1u << from) - 1u);
+        return (there >> g & 1) != 0 ? bits : 0u;
+      };
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int g = 0; g < 8; ++g) {
+        uint32_t z[16];
+        tmem_ld_32x32b_x16(t_s + 16 * g, z);
+        tmem_ld_wait();
+        const uint32_t seen = seen_bits(g);
+        float t = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t = fmaxf(t, (seen >> i & 1) ? __uint_as_float(z[i]) : -INFINITY);
+        top = fmaxf(top, t * (coef * meta.ck[g]));
+      }
+      follow(top);
+      const float use = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
+      for (int g = 0; g < 8; ++g) {
+        uint32_t z[16], pk[8];
+        tmem_ld_32x32b_x16(t_s + 16 * g, z);
+        tmem_ld_wait();
+        const uint32_t seen = seen_bits(g);
+        const int lf = max(meta.ev[g] - ref + kBias, -40);
+        const float add = static_cast<float>(lf) - use, mul = coef * meta.ck[g];
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float2 e = ffma2(make_float2(z[16 * g + 2 * i], z[16 * g + 2 * i + 1]), cc, aa);
-          e.x = exp2_fast(e.x);
-          e.y = exp2_fast(e.y);
-          if (!whole) {  // (a scale that is NaN shows where it is seen)
-            if (!(seen[c] >> (16 * gg + 2 * i) & 1)) e.x = 0.0f;
-            if (!(seen[c] >> (16 * gg + 2 * i + 1) & 1)) e.y = 0.0f;
+          float2 e = make_float2(exp2_fast(fmaf(__uint_as_float(z[2 * i]), mul, add)),
+                                 exp2_fast(fmaf(__uint_as_float(z[2 * i + 1]), mul, add)));
+          const bool sx = seen >> (2 * i) & 1, sy = seen >> (2 * i + 1) & 1;
+          e.x = sx ? e.x : 0.0f;
+          e.y = sy ? e.y : 0.0f;
+          sum += e.x + e.y;
+          if (vnan >> g & 1) {  // shows where it is seen
+            if (sx) e.x = scale_value(kScaleNan);
+            if (sy) e.y = scale_value(kScaleNan);
           }
-          sum = fadd2(sum, e);
-          if (vnan != 0 && (vnan >> g & 1)) {
-            if (seen[c] >> (16 * gg + 2 * i) & 1) e.x = scale_value(kScaleNan);
-            if (seen[c] >> (16 * gg + 2 * i + 1) & 1) e.y = scale_value(kScaleNan);
-          }
-          pk[8 * gg + i] = pack_pair<__half>(e);
+          pk[i] = pack_pair<__half>(e);
         }
-        l = fmaf(sum.x + sum.y, scale_value(127 - lf), l);
+        l = fmaf(sum, scale_value(127 - lf), l);
+        tmem_st_32x32b_x8(t_s + 8 * g, pk);
       }
-      tmem_st_32x32b_x16(t_s + 16 * c, pk);
     }
     tmem_st_wait();
     tc_fence_before();
-    mbar_arrive(smem_u32(&sm->p_full[x]));
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) arrive_leader(&sm->p_full[x]);
   }
 
   // the row's result
@@ -550,24 +654,25 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kAttnThreads, 1) cache_attention_kernel(const CacheAttentionArgs a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1) cache_attention_kernel(const CacheAttentionArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t s_q = smem_u32(smem), s_k = s_q + 2 * kTileBytes, s_v = s_k + kStages * kTileBytes;
-  Smem* sm = reinterpret_cast<Smem*>(smem + 2 * kTileBytes + 2 * kStages * kTileBytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t s_q = smem_u32(smem), s_k = s_q + 2 * kQBytes, s_v = s_k + kStages * kKBytes;
+  Smem* sm = reinterpret_cast<Smem*>(smem + 2 * kQBytes + kStages * (kKBytes + kVBytes));
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  const int rank = static_cast<int>(cluster_ctarank());
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sm->q_full[i]), kTileRows);
+      mbar_init(smem_u32(&sm->q_full[i]), 8);  // a warp's arrival each: four of either CTA
       mbar_init(smem_u32(&sm->s_full[i]), 1);
-      mbar_init(smem_u32(&sm->p_full[i]), kTileRows);
+      mbar_init(smem_u32(&sm->p_full[i]), 8);
       mbar_init(smem_u32(&sm->o_full[i]), 1);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&sm->k_full[i]), 4);
+      mbar_init(smem_u32(&sm->k_full[i]), 8);
       mbar_init(smem_u32(&sm->k_empty[i]), 1);
-      mbar_init(smem_u32(&sm->v_full[i]), 4);
+      mbar_init(smem_u32(&sm->v_full[i]), 8);
       mbar_init(smem_u32(&sm->v_empty[i]), 1);
     }
     for (int i = 0; i < kMetaSlots; ++i) mbar_init(smem_u32(&sm->meta_full[i]), 1);
@@ -576,39 +681,41 @@ __global__ void __launch_bounds__(kAttnThreads, 1) cache_attention_kernel(const 
     fence_barrier_init();
   }
   if (warp == 12) {
-    tmem_alloc(smem_u32(&sm->tmem), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(&sm->tmem), 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tmem = sm->tmem;
 
-  Work w(a, blockIdx.x);
+  Work w(a, blockIdx.x >> 1);
   const Visible vis(a, w.b);
   w.plan(a, vis);
 
   if (warp < 8) {
     regs_up<kSoftmaxRegs>();
     const int x = warp >> 2;
-    if (x == 0 || w.two) softmax_role<T>(a, w, vis, sm, s_q, tmem, x);
+    if (x == 0 || w.two) softmax_role<T>(a, w, vis, sm, s_q, tmem, x, rank);
   } else if (warp < 12) {
     regs_down<kConvertRegs>();
-    convert_role(a, w, vis, sm, s_k, s_v);
+    convert_role(a, w, vis, sm, s_k, s_v, rank);
   } else {
     regs_down<kIssueRegs>();
-    if (warp == 12 && lane == 0 && w.n > 0 && !issue_all(a, w, sm, s_q, s_k, s_v, tmem)) {
+    if (warp == 12 && rank == 0 && w.n > 0 && !issue_all(a, w, sm, s_q, s_k, s_v)) {
       // what was issued reads shared memory and writes tensor memory: let it end
-      tc_commit(smem_u32(&sm->drain));
+      commit_both(&sm->drain);
       if (!mbar_wait_bounded(smem_u32(&sm->drain), 0, nullptr, kWaitNs)) atomicOr(a.status, kErrDrainWait);
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // nothing of the pair reads the other's memory any more
   if (warp == 12) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -617,7 +724,7 @@ cudaError_t launch_tiles(const CacheAttentionArgs& a, cudaStream_t s) {
   auto k = cache_attention_kernel<T>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
   if (e != cudaSuccess) return e;
-  const long long blocks = static_cast<long long>(a.batch) * a.row_tiles * a.pool.heads * a.splits;
+  const long long blocks = 2ll * a.batch * a.row_tiles * a.pool.heads * a.splits;
   k<<<static_cast<unsigned>(blocks), kAttnThreads, kSmemBytes, s>>>(a);
   return cudaGetLastError();
 }

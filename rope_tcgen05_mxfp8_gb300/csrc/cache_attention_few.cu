@@ -47,16 +47,8 @@ __device__ __forceinline__ void mma_16816(float* c, const uint32_t* a, uint32_t 
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));  // 2 ulp
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // 2 ulp; below 2^-126 zero (one instruction, not four)
   return y;
-}
-
-__device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
 }
 
 __device__ __forceinline__ float quad_max(float v) {
@@ -166,7 +158,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
 
   KeyGroup now[2], next[2];
   uint4 kr[4][2], vr[2][4];
-  const uint4 zero = make_uint4(0, 0, 0, 0);
   auto find = [&](KeyGroup (&kg)[2], int c) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -181,9 +172,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
     for (int n = 0; n < 4; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        kr[n][i] = kg[n >> 1].row >= 0 && 4 * i + t < pieces
-                       ? ld_codes(a.pool.k + (kg[n >> 1].row + 8 * (n & 1) + g) * a.pool.d + 64 * i + 16 * t)
-                       : zero;
+        kr[n][i] = ld_codes_if(a.pool.k + (kg[n >> 1].row + 8 * (n & 1) + g) * a.pool.d + 64 * i + 16 * t,
+                               kg[n >> 1].row >= 0 && 4 * i + t < pieces);
   };
   // rows of V past the sequence's end may hold anything: they count as zeros
   auto load_v = [&](const KeyGroup (&kg)[2], int c) {
@@ -192,9 +182,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         const int slot = 2 * t + (n & 1) + 8 * (n >> 1);
-        vr[i][n] = kg[i].row >= 0 && g < pieces && c * kFewKeys + 16 * i + slot < vis.length
-                       ? ld_codes(a.pool.v + (kg[i].row + slot) * a.pool.d + 16 * g)
-                       : zero;
+        vr[i][n] = ld_codes_if(a.pool.v + (kg[i].row + slot) * a.pool.d + 16 * g,
+                               kg[i].row >= 0 && g < pieces && c * kFewKeys + 16 * i + slot < vis.length);
       }
   };
 

@@ -11,12 +11,17 @@ namespace qkvcte {
 
 constexpr int kScaleNan = 255;  // UE8M0: a page and head that hold a value that is not finite
 
-// Page of block `blk` of sequence b, or -1: behind the table, or a hole (an entry that is no
-// page of the pool). Every access to the pool goes through here.
-__device__ __forceinline__ long long cache_page(const CachePool& p, int b, long long blk) {
+// The table's entry for block `blk` of sequence b, -1 behind the table. (Without a table
+// b * max_blocks + blk < pages, which fits.)
+__device__ __forceinline__ int cache_entry(const CachePool& p, int b, long long blk) {
   if (blk < 0 || blk >= p.max_blocks) return -1;
-  const long long page = p.table != nullptr ? static_cast<long long>(__ldg(p.table + b * p.table_stride + blk))
-                                            : static_cast<long long>(b) * p.max_blocks + blk;
+  return p.table != nullptr ? __ldg(p.table + b * p.table_stride + blk) : b * p.max_blocks + static_cast<int>(blk);
+}
+
+// The page of that block, or -1: also for a hole (an entry that is no page of the pool). Every
+// access to the pool is by a page that was checked so.
+__device__ __forceinline__ long long cache_page(const CachePool& p, int b, long long blk) {
+  const int page = cache_entry(p, b, blk);
   return page >= 0 && page < p.pages ? page : -1;
 }
 
@@ -33,6 +38,19 @@ __device__ __forceinline__ int scale_exponent(uint32_t abs_bits) {
   if (abs_bits >= 0x7F800000u) return kScaleNan;
   const int e = static_cast<int>(abs_bits >> 23) - 8 + ((abs_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return e < 1 ? 1 : e;
+}
+
+// 16 codes, zeros without `live` (nothing is read then). One predicated instruction: a branch
+// around each load made the next ones wait for it.
+__device__ __forceinline__ uint4 ld_codes_if(const uint8_t* p, bool live) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@q ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"(static_cast<int>(live)));
+  return v;
 }
 
 // Two e4m3 codes (the low 16 bits) as fp16, exactly.

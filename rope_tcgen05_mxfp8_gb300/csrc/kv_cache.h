@@ -50,7 +50,7 @@ struct CacheAttentionArgs {
   const int* lengths;    // [batch]
   const int* counts;     // [batch] or null (seq)
   int batch, seq, q_heads, group;  // group: query heads per key head
-  int row_tiles;         // tiles of the seq * group rows of a (batch, key head): of 16, or pairs of 128
+  int row_tiles;         // tiles of the seq * group rows of a (batch, key head): of 16, or of 512
   int splits;            // parts of the keys
   float scale_log2;      // softmax scale * log2(e)
   int causal, window;    // window 0: none
@@ -61,9 +61,9 @@ struct CacheAttentionArgs {
   uint32_t flags;
 };
 
-// Rows a block takes: of the form for few queries, of the form on the tensor cores.
+// Rows a block takes of the form for few queries, a pair of blocks of the form on tcgen05.
 constexpr int kCacheFewRows = 16;
-constexpr int kCachePairRows = 256;
+constexpr int kCacheTileRows = 512;
 
 cudaError_t launch_cache_attention_few(const CacheAttentionArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_cache_attention_tiles(const CacheAttentionArgs& a, int dtype, cudaStream_t s);

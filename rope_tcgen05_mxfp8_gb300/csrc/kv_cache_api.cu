@@ -175,10 +175,10 @@ AttentionShape attention_shape(const qkv_cte_cache_desc& d, int64_t batch, int64
   if (max_length > kMaxPositions) max_length = kMaxPositions;
   const int64_t rows = seq * (n_q_heads / d.n_kv_heads);
   s.few = rows <= kCacheFewRows;
-  const int per = s.few ? kCacheFewRows : kCachePairRows;
+  const int per = s.few ? kCacheFewRows : kCacheTileRows;
   s.row_tiles = static_cast<int>((rows + per - 1) / per);
   const int64_t items = batch * d.n_kv_heads * s.row_tiles;
-  int64_t splits = s.few ? (608 + items - 1) / (items > 0 ? items : 1) : 152 / (items > 0 ? items : 1);
+  int64_t splits = s.few ? (608 + items - 1) / (items > 0 ? items : 1) : 76 / (items > 0 ? items : 1);
   const int64_t most = (max_length + 255) / 256;
   if (splits > most) splits = most;
   s.splits = static_cast<int>(splits < 1 ? 1 : splits > kMaxSplits ? kMaxSplits : splits);
@@ -320,7 +320,7 @@ int qkv_cte_cache_attention(qkv_cte_cache_plan_t plan, const qkv_cte_cache_pages
     for (int j = 0; j < (i == 0 ? 2 : 3); ++j)  // q and out: above
       if ((rc = disjoint(outs[i], ins[j], who)) != QKV_CTE_OK) return rc;
   }
-  if (batch * plan->d.n_kv_heads * s.row_tiles > INT32_MAX / s.splits)
+  if (batch * plan->d.n_kv_heads * s.row_tiles > INT32_MAX / 2 / s.splits)
     return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: more than INT32_MAX tiles", who);
   DeviceInfo dev;
   if ((rc = check_device(&dev)) != QKV_CTE_OK) return rc;
