@@ -65,23 +65,18 @@ struct KeyGroup {
   long long row;   // (page * heads + head) * block_tokens + slot, or -1
   int ek, ev;
 
-  __device__ __forceinline__ void find(const CachePool& p, int b, int h, int key) {
-    const long long page = cache_page(p, b, key >> p.log_bt);
+  // `entry`: the table's, loaded an iteration earlier
+  __device__ __forceinline__ void find(const CachePool& p, int entry, int h, int key) {
     row = -1;
     ek = ev = 1;
-    if (page >= 0) {
-      const long long ph = page * p.heads + h;
+    if (entry >= 0 && entry < p.pages) {
+      const long long ph = static_cast<long long>(entry) * p.heads + h;
       row = (ph << p.log_bt) + (key & ((1 << p.log_bt) - 1));
       ek = __ldg(p.k_sf + ph);
       ev = __ldg(p.v_sf + ph);
     }
   }
 };
-
-template <typename T>
-__device__ __forceinline__ float query_elem(const T* p) {
-  return to_f32(*p);
-}
 
 template <typename T>
 __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(const CacheAttentionArgs a) {
@@ -128,12 +123,32 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
     float x[32];
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+      const T* e = p + 64 * i + 16 * t;
+      const bool there = live && 4 * i + t < pieces;
+      if (a.wide) {
+        Vec<T, 8> v[2];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        x[16 * i + j] = live && 4 * i + t < pieces ? query_elem(p + 64 * i + 16 * t + j) : 0.0f;
-        top = max(top, __float_as_uint(x[16 * i + j]) & 0x7FFFFFFFu);
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[k].w[j] = 0;
+        if (there) {
+          v[0] = *reinterpret_cast<const Vec<T, 8>*>(e);
+          v[1] = *reinterpret_cast<const Vec<T, 8>*>(e + 8);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 f = v[j >> 2].pair(j & 3);
+          x[16 * i + 2 * j] = f.x;
+          x[16 * i + 2 * j + 1] = f.y;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[16 * i + j] = there ? to_f32(e[j]) : 0.0f;
       }
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int f = query_factor_field(top);
@@ -158,14 +173,18 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
 
   KeyGroup now[2], next[2];
   uint4 kr[4][2], vr[2][4];
-  auto find = [&](KeyGroup (&kg)[2], int c) {
+  // table entries are loaded two chunks ahead, scales and codes one
+  int ahead[2];
+  auto entries = [&](int c) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      kg[i].row = -1;
-      kg[i].ek = kg[i].ev = 1;
       const int key = c * kFewKeys + 16 * i;
-      if (c < c1 && key < hi) kg[i].find(a.pool, b, h, key);
+      ahead[i] = c < c1 && key < hi ? cache_entry(a.pool, b, key >> a.pool.log_bt) : -1;
     }
+  };
+  auto find = [&](KeyGroup (&kg)[2], int c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) kg[i].find(a.pool, ahead[i], h, c * kFewKeys + 16 * i);
   };
   auto load_k = [&](const KeyGroup (&kg)[2]) {
 #pragma unroll
@@ -188,11 +207,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
   };
 
   int c = c0 + warp;
+  entries(c);
   find(now, c);
+  entries(c + kFewWarps);
   load_k(now);
   load_v(now, c);
   for (; c < c1; c += kFewWarps) {
     find(next, c + kFewWarps);
+    entries(c + 2 * kFewWarps);
     // scores
     float z[4][4];
 #pragma unroll

@@ -1,7 +1,7 @@
 // C-ABI front end of the 8-bit key/value cache (qkv_cte_cache_*, documented in qkv_cte.h):
 // argument checks, the choice of an attention's form, launches.
+#include <algorithm>
 #include <climits>
-#include <cmath>
 #include <new>
 
 #include "api_common.h"
@@ -178,10 +178,22 @@ AttentionShape attention_shape(const qkv_cte_cache_desc& d, int64_t batch, int64
   const int per = s.few ? kCacheFewRows : kCacheTileRows;
   s.row_tiles = static_cast<int>((rows + per - 1) / per);
   const int64_t items = batch * d.n_kv_heads * s.row_tiles;
-  int64_t splits = s.few ? (608 + items - 1) / (items > 0 ? items : 1) : 76 / (items > 0 ? items : 1);
-  const int64_t most = (max_length + 255) / 256;
-  if (splits > most) splits = most;
-  s.splits = static_cast<int>(splits < 1 ? 1 : splits > kMaxSplits ? kMaxSplits : splits);
+  // Parts of the keys: the fewest waves of blocks, weighed by what a block costs beside its
+  // keys (in the time of 1024 keys) and by the joining.
+  const int64_t slots = s.few ? 304 : 76;  // two blocks on each of 152 SMs; pairs of blocks
+  const double fixed = s.few ? 0.25 : 0.5, join = 0.25;
+  const double traffic = static_cast<double>(batch * seq * n_q_heads) * d.d_head * 8 / 1.3e8;  // of one part: written, read
+  const int64_t most = std::min<int64_t>((max_length + 511) / 512, kMaxSplits);
+  double best = 0;
+  s.splits = 1;
+  for (int64_t k = 1; k <= most; ++k) {
+    const double waves = static_cast<double>((items * k + slots - 1) / slots);
+    const double cost = waves * (static_cast<double>(max_length) / (1024.0 * k) + fixed) + (k > 1 ? join + traffic * k : 0.0);
+    if (k == 1 || cost < best) {
+      best = cost;
+      s.splits = static_cast<int>(k);
+    }
+  }
   return s;
 }
 

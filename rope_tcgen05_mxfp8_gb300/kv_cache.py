@@ -6,7 +6,7 @@ Argument marshalling only, with the rules of block_ops.py.
 from __future__ import annotations
 
 import ctypes
-import functools
+import math
 
 import torch
 
@@ -16,6 +16,8 @@ from .qkv_cte import (QKV_CTE_ERR_UNSUPPORTED, QkvCteError, _check, _cleared, _e
 
 _QUERY = (torch.bfloat16, torch.float16)
 _I32 = (torch.int32,)
+_increment_version = torch.autograd.graph.increment_version
+_NONE = (None, 0, 0, 0)
 
 
 class qkv_cte_cache_desc(ctypes.Structure):
@@ -68,7 +70,14 @@ def _lib() -> ctypes.CDLL:
 
 
 def _heads(name: str, t, dtypes, device, heads, d, shape=None):
-    """(address, batch, row and head stride), batch and seq of [B, S, heads, d] or [S, heads, d]."""
+    """(address, batch, row and head stride), batch and seq of [B, S, heads, d] or [S, heads, d].
+    What is right is tested first, with as few calls into torch as will do."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == device:
+        s = t.shape
+        if len(s) == 4 and s[3] == d and (heads is None or s[2] == heads) and (shape is None or s == shape):
+            b, r, h, one = t.stride()
+            if one == 1:
+                return (t.data_ptr(), b, r, h), s[0], s[1]
     _tensor(name, t, dtypes, device)
     s, st = t.shape, t.stride()
     if len(s) not in (3, 4) or s[-1] != d or (heads is not None and s[-2] != heads):
@@ -78,8 +87,6 @@ def _heads(name: str, t, dtypes, device, heads, d, shape=None):
         raise ValueError(f"{name}: shape {tuple(s)} is not {tuple(shape)}")
     if st[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    if len(s) == 4:
-        return (t.data_ptr(), st[0], st[1], st[2]), s[0], s[1]
     return (t.data_ptr(), 0, st[0], st[1]), 1, s[0]
 
 
@@ -138,7 +145,7 @@ class QkvCteCache:
                 self._own.append(t)
             elif not isinstance(t, torch.Tensor) or t.dim() != len(shape):
                 raise ValueError(f"{name}: expected a tensor of shape {shape}")
-            _vector(name, t, (torch.uint8,), dev, functools.reduce(lambda a, b: a * b, shape))
+            _vector(name, t, (torch.uint8,), dev, math.prod(shape))
             if tuple(t.shape) != shape:
                 raise ValueError(f"{name}: shape {tuple(t.shape)} is not {shape}")
             return t
@@ -149,11 +156,18 @@ class QkvCteCache:
         self._own.append(self._status)
         self._base = (self.k.data_ptr(), self.k_sf.data_ptr(), self.v.data_ptr(), self.v_sf.data_ptr())
         self._needs = {}  # workspace bytes by sizes
+        self._status_at = self._status.data_ptr()
+        # version counters (inference tensors have none)
+        self._k_counted, self._v_counted = ([t for t in pair if not t.is_inference()]
+                                            for pair in ((self.k, self.k_sf), (self.v, self.v_sf)))
 
     def _pages(self, table, batch):
         """The table as the library takes it, and its positions per sequence."""
         if table is None:
             p, stride, blocks = None, 0, self.pages // batch if batch else 1
+        elif (isinstance(table, torch.Tensor) and table.dtype is torch.int32 and table.device == self.device
+              and len(table.shape) == 2 and table.shape[0] == batch > 1 and table.stride(1) == 1 and table.stride(0)):
+            p, stride, blocks = table.data_ptr(), table.stride(0), table.shape[1]
         else:
             _tensor("table", table, _I32, self.device)
             if table.dim() not in (1, 2) or (table.dim() == 2 and table.shape[0] != batch):
@@ -186,16 +200,16 @@ class QkvCteCache:
         if not isinstance(first, torch.Tensor):
             raise TypeError("k, v: expected a torch.Tensor")
         dt, n, d = first.dtype, self.n_kv_heads, self.d_head
-        none = (None, 0, 0, 0)
-        sizes = _heads("k" if k is not None else "v", first, _DTYPE, self.device, n, d)[1:]
-        ak = _heads("k", k, (dt,), self.device, n, d, first.shape)[0] if k is not None else none
-        av = _heads("v", v, (dt,), self.device, n, d, first.shape)[0] if v is not None else none
-        batch, seq = sizes
+        ak, batch, seq = _heads("k" if k is not None else "v", first, _DTYPE, self.device, n, d)
+        if k is None:
+            ak, av = _NONE, ak
+        else:
+            av = _heads("v", v, (dt,), self.device, n, d, first.shape)[0] if v is not None else _NONE
         pages, _ = self._pages(table, batch)
         ps, pc = self._index("starts", starts, batch), self._index("counts", counts, batch)
         _launch(_lib().qkv_cte_cache_write, self.device, self._stream(stream), self.plan, ctypes.byref(pages), *ak, *av,
                 batch, seq, ps, pc, _DTYPE[dt])
-        _written(*((self.k, self.k_sf) if k is not None else ()), *((self.v, self.v_sf) if v is not None else ()))
+        _increment_version((self._k_counted if k is not None else []) + (self._v_counted if v is not None else []))
 
     def read(self, starts, seq: int, lengths, table=None, dtype=torch.bfloat16, k=None, v=None, stream=None):
         """(k, v) [B, seq, n_kv_heads, d_head]: tokens starts[b] + s; zeros from lengths[b] on.
@@ -212,24 +226,24 @@ class QkvCteCache:
             if dtype not in _DTYPE:
                 raise TypeError(f"dtype: {dtype} not in {tuple(_DTYPE)}")
             k, v = (_empty(side, (batch, seq, n, d), dtype, self.device) for _ in range(2))
+            ak, av = ((t.data_ptr(), seq * n * d, n * d, d) for t in (k, v))
         else:
             given = k, v
             dtype = (k if k is not None else v).dtype
-        none = (None, 0, 0, 0)
-        full = (batch, seq, n, d)
-        args = []
-        for name, t in (("k", k), ("v", v)):
-            if t is None:
-                args.append(none)
-                continue
-            a, b_, s_ = _heads(name, t, (dtype,) if dtype in _DTYPE else _DTYPE, self.device, n, d)
-            if (b_, s_) != (batch, seq):
-                raise ValueError(f"{name}: shape {tuple(t.shape)} is not {full}")
-            args.append(a)
+            args = []
+            for name, t in (("k", k), ("v", v)):
+                if t is None:
+                    args.append(_NONE)
+                    continue
+                at, b, rows = _heads(name, t, (dtype,) if dtype in _DTYPE else _DTYPE, self.device, n, d)
+                if (b, rows) != (batch, seq):
+                    raise ValueError(f"{name}: shape {tuple(t.shape)} is not {(batch, seq, n, d)}")
+                args.append(at)
+            ak, av = args
         pages, _ = self._pages(table, batch)
         ps, pl = self._index("starts", starts, batch), self._index("lengths", lengths, batch)
-        _launch(_lib().qkv_cte_cache_read, self.device, self._stream(stream), self.plan, ctypes.byref(pages), *args[0],
-                *args[1], batch, seq, ps, pl, _DTYPE[dtype])
+        _launch(_lib().qkv_cte_cache_read, self.device, self._stream(stream), self.plan, ctypes.byref(pages), *ak, *av,
+                batch, seq, ps, pl, _DTYPE[dtype])
         if given is not None:
             _written(*given)
         return k, v
@@ -237,16 +251,17 @@ class QkvCteCache:
     def attention_workspace(self, batch: int, seq: int, heads: int, max_length: int) -> int:
         """Workspace bytes of an attention call (a function of the sizes alone)."""
         key = batch, seq, heads, max_length
-        if key not in self._needs:
-            if len(self._needs) >= 256:
-                self._needs.clear()
+        need = self._needs.get(key)
+        if need is None:
             _fits("heads", heads)
             for name, v in (("batch", batch), ("seq", seq), ("max_length", max_length)):
                 _fits(name, v, 63)
             n = ctypes.c_size_t()
             _check(_lib().qkv_cte_cache_attention_workspace(self.plan, *key, ctypes.byref(n)))
-            self._needs[key] = n.value
-        return self._needs[key]
+            if len(self._needs) >= 256:
+                self._needs.clear()
+            self._needs[key] = need = n.value
+        return need
 
     def attention(self, q, lengths, counts=None, table=None, causal: bool = False, window: int = 0, scale=None,
                   out=None, lse=None, stats: bool = False, max_length=None, workspace=None, stream=None):
@@ -271,7 +286,9 @@ class QkvCteCache:
         given = None if out is None and lse is None else (out, lse)
         if out is None:
             out = torch.empty(shape, dtype=dt, device=dev) if side is None else _empty(side, shape, dt, dev)
-        ao = _heads("out", out, (dt,), dev, heads, d, shape)[0]
+            ao = (out.data_ptr(), seq * heads * d, heads * d, d)
+        else:
+            ao = _heads("out", out, (dt,), dev, heads, d, shape)[0]
         if stats and lse is None:
             lse = _empty(side, shape[:-1], torch.float32, dev)
         pe = None
@@ -287,7 +304,7 @@ class QkvCteCache:
             pw = _vector("workspace", workspace, (torch.uint8,), dev, need)
         _launch(_lib().qkv_cte_cache_attention, dev, self._stream(stream), self.plan, ctypes.byref(pages), *aq, *ao, pe,
                 batch, seq, heads, pl, pc, max_length, d ** -0.5 if scale is None else scale, 1 if causal else 0, window,
-                _DTYPE[dt], pw, need, self._status.data_ptr())
+                _DTYPE[dt], pw, need, self._status_at)
         if given:
             _written(*given)
         return out, lse
