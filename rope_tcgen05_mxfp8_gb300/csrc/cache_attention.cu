@@ -43,7 +43,7 @@ constexpr int kTileRows = 128;     // of a row tile, per CTA
 constexpr int kTileKeys = 128;
 constexpr int kPairRows = kCacheTileRows;
 static_assert(kPairRows == 4 * kTileRows, "two CTAs, two row tiles");
-constexpr int kAttnThreads = 512;  // 2 x 4 softmax warps, 4 conversion warps, the issuing warp and three idle
+constexpr int kAttnThreads = 416;  // 2 x 4 softmax warps, 4 conversion warps, the issuing warp
 constexpr int kStages = 2;
 constexpr int kMetaSlots = 4;
 constexpr int kQHalf = kTileRows * 128;           // 128 rows of 64 fp16
@@ -55,10 +55,6 @@ constexpr int kBias = 7;                          // weights are held 2^7 above 
 constexpr float kGrowth = 8.0f;                   // binary orders the maximum may grow before a rescale
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kSCol = 0, kOCol = 256;        // TMEM columns: S (and P) of both tiles, then O
-// Registers per thread and role: 8 x 192 + 4 x 72 + 4 x 56 = 16 x 128, what the launch has.
-constexpr int kSoftmaxRegs = 192, kConvertRegs = 72, kIssueRegs = 56;
-static_assert(8 * kSoftmaxRegs + 4 * kConvertRegs + 4 * kIssueRegs == 16 * 128, "register split");
-
 // What the softmax warps need to know about a tile of keys, by groups of 16.
 struct TileMeta {
   float ck[8];      // key scale (NaN: 255)
@@ -81,15 +77,6 @@ struct Smem {
 
 constexpr size_t kSmemBytes = 1024 + 2 * kQBytes + kStages * (kKBytes + kVBytes) + sizeof(Smem);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-
-template <int kRegs>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
 
 // Issued by one lane of a warp that is together, so that descriptors stay in uniform registers:
 // in a branch of one lane every operand is moved there anew (1000 instead of 750 clocks for
@@ -210,7 +197,8 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Smem* s
 
 // Arrive on the leading CTA's barrier at this offset. What it announces is read by the tensor
 // cores alone, where it lies, and has been fenced towards them; a release at cluster scope
-// would wait for the thread's loads in flight as well (6000 instead of 3000 clocks a tile).
+// would wait for the thread's loads in flight as well (5900 instead of 5050 clocks a tile of
+// keys).
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0)) : "memory");
 }
@@ -695,15 +683,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1) cac
   w.plan(a, vis);
 
   if (warp < 8) {
-    regs_up<kSoftmaxRegs>();
     const int x = warp >> 2;
     if (x == 0 || w.two) softmax_role<T>(a, w, vis, sm, s_q, tmem, x, rank);
   } else if (warp < 12) {
-    regs_down<kConvertRegs>();
     convert_role(a, w, vis, sm, s_k, s_v, rank);
   } else {
-    regs_down<kIssueRegs>();
-    if (warp == 12 && rank == 0 && w.n > 0 && !issue_all(a, w, sm, s_q, s_k, s_v)) {
+    if (rank == 0 && w.n > 0 && !issue_all(a, w, sm, s_q, s_k, s_v)) {
       // what was issued reads shared memory and writes tensor memory: let it end
       commit_both(&sm->drain);
       if (!mbar_wait_bounded(smem_u32(&sm->drain), 0, nullptr, kWaitNs)) atomicOr(a.status, kErrDrainWait);
