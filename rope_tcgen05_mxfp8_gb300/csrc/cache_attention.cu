@@ -16,9 +16,17 @@
 // The two row tiles take turns: while one is in its softmax the tensor cores work on the
 // other. Codes cannot feed the tensor cores as they are, because both operands of an 8-bit
 // product would have to be 8-bit, and weights and queries rounded to three digits are not
-// attention; the conversion is shared by 512 rows. A CTA by itself would need 128 bytes of
-// shared memory a clock for Q K^T alone, all there is (measured: 94 to 113 clocks for an
-// instruction of 64), and its codes in flight would not fit the L1 that its buffers leave.
+// attention; the conversion is shared by 512 rows.
+//
+// What bounds it (972 x 4096, 38 heads of 128: 77.5 us, 1.00 PFLOP/s, 0.53 of the measured rate;
+// 32760 keys 0.52): a tile of 128 keys takes some 4700 clocks for 2048 of products. An
+// instruction with A from shared memory takes 86 to 95 clocks instead of 64 by itself, and each
+// row tile goes round a chain of softmax (2000), arrival from the other CTA, O += P V and the
+// next S. Tried: a CTA by itself (twice the conversion per SM: 700 TFLOP/s), P through shared
+// memory so that S is free sooner (870), two softmax threads per row (590, held by the three
+// conversion warps that were left room for), one row tile per pair and two blocks per SM (830).
+// Short key ranges are bound by what comes before and after: 32760 queries over 128 keys take 466
+// us, 14 a block, so that over 512 keys (673) more than half is not products.
 //
 // Scales. A key's block scale multiplies its score in fp32. A value's block scale multiplies
 // its weight before the rounding to fp16, relative to the largest value scale so far (an

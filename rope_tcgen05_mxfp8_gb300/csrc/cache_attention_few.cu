@@ -4,13 +4,20 @@
 // with c = scale log2(e) and m the running maximum: one pass over the keys.
 //
 // With a few query rows per key head (a token of each sequence, times the query heads that
-// share a key head) the cache is read once and the read is all that counts. A warp takes 32
-// keys at a time and multiplies them with up to 16 rows by warp-level tensor instructions
+// share a key head) the cache is read once and the read is what counts. A warp takes 32 keys
+// at a time and multiplies them with up to 16 rows by warp-level tensor instructions
 // (m16n8k16, fp16 in, fp32 out): the codes become fp16 exactly, and the instruction wants
 // them in registers, where the global loads put them. No shared memory, no barrier and no
 // conversion pass stands between memory and the product. tcgen05 would want the same codes
 // converted and stored to shared memory first, for a tile whose 128 rows would be mostly
-// padding.
+// padding (17 rows over 4096 keys, 40 heads: 27 us here, 56 there).
+//
+// What bounds it: 4 sequences of 32760 tokens, 40 heads of 128, one row each (1.34 GB) take 278 us,
+// 4.8 TB/s of 6.8: the warps' chains of product, maximum, exponential and product, about 400
+// instructions per 8 KB. More warps did not help (8 rows a tile in 168 or 128 registers: 276 and
+// 295 us), nor did integer operations in place of the conversion instructions (321). One token
+// over 512 keys takes 9.7 us, latencies alone. Keys are divided among blocks by waves (see the
+// host's attention_shape) and the parts joined by a second, small kernel.
 //
 // Layouts. Lane 4g + t holds column g of the B operand and rows g, g + 8 of A and C.
 //   Scores: B's column g is key g; a lane reads 16-byte pieces t, t + 4 of its key's row, so

@@ -21,6 +21,17 @@ namespace {
 
 constexpr int kMaxDHead = 128;
 constexpr int kMaxSplits = 64;
+// Query rows per key head up to which the form for few queries is taken, in tiles of 16 rows that
+// read the keys again (from L2); beyond, pairs of blocks on tcgen05, for which fewer than 256
+// rows leave part of every product empty. us a call in a captured graph, few rows' form / tcgen05,
+// 40 key heads of 128:
+//   rows  over 512 keys  over 4096     4 x 32760
+//   17    11.6 / 13.8    26.6 / 55.5
+//   32    11.5 / 13.9    27.8 / 56.1   575 / 1275
+//   64    13.7 / 14.2    50.3 / 58.3   1067 / 1296
+//   96                   57.9 / 60.8
+//   128   22.9 / 15.9    94.9 / 63.9
+constexpr int64_t kFewMaxRows = 64;
 constexpr int64_t kMaxPositions = INT32_MAX - 1024;  // positions rounded up to tiles stay inside 32 bits
 
 size_t elem_size(int dtype) { return dtype == QKV_CTE_DTYPE_FP32 ? 4 : 2; }
@@ -174,7 +185,7 @@ AttentionShape attention_shape(const qkv_cte_cache_desc& d, int64_t batch, int64
   AttentionShape s;
   if (max_length > kMaxPositions) max_length = kMaxPositions;
   const int64_t rows = seq * (n_q_heads / d.n_kv_heads);
-  s.few = rows <= kCacheFewRows;
+  s.few = rows <= kFewMaxRows;
   const int per = s.few ? kCacheFewRows : kCacheTileRows;
   s.row_tiles = static_cast<int>((rows + per - 1) / per);
   const int64_t items = batch * d.n_kv_heads * s.row_tiles;

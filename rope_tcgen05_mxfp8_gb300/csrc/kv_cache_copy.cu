@@ -122,7 +122,8 @@ struct CopyItem {
   }
 };
 
-// kThreadsMax 32: a warp per item, several items per block; else a block per item.
+// kWarp: a warp per item, several items per block (pages of up to 2048 elements per head); else
+// a block per item.
 template <typename T, bool kWarp>
 __global__ void __launch_bounds__(256) cache_write_kernel(const CacheCopyArgs a, long long items) {
   __shared__ uint32_t warp_max[8];

@@ -108,6 +108,12 @@ def test_lengths(S, causal):
     Case([0, 1, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 515], S=S, causal=causal).run_and_check()
 
 
+@pytest.mark.parametrize("S,nq", [(8, 2), (9, 2), (16, 2), (17, 2), (32, 2), (33, 2), (63, 1), (64, 1), (65, 1), (128, 1),
+                                  (129, 1), (255, 1), (256, 1), (257, 1), (511, 1), (512, 1), (513, 1), (1030, 1)])
+def test_rows_at_the_edges_of_tiles_and_forms(S, nq):
+    Case([1100, 140], S=S, nq=nq, nkv=1, d=64, bt=32, causal=True).run_and_check()
+
+
 @pytest.mark.parametrize("bt", [16, 32, 64, 128])
 @pytest.mark.parametrize("d", [16, 32, 48, 64, 80, 96, 112, 128])
 @pytest.mark.parametrize("S", [3, 50])
