@@ -62,7 +62,8 @@ constexpr int kVBytes = kTileKeys * 128;          // 128 keys, this CTA's lanes 
 constexpr int kBias = 7;                          // weights are held 2^7 above their value
 constexpr float kGrowth = 8.0f;                   // binary orders the maximum may grow before a rescale
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr uint32_t kSCol = 0, kOCol = 256;        // TMEM columns: S (and P) of both tiles, then O
+// TMEM columns: S (and P) of both tiles, then O. The block has all 512, so they count from 0.
+constexpr uint32_t kSCol = 0, kOCol = 256;
 // What the softmax warps need to know about a tile of keys, by groups of 16.
 struct TileMeta {
   float ck[8];      // key scale (NaN: 255)
@@ -144,6 +145,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+__device__ __forceinline__ void ld_global32(uint32_t* w, const void* p) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
 __device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -203,6 +209,16 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Smem* s
   return false;
 }
 
+// Every warp passes here once, when its first loads are on their way: barriers and tensor memory
+// of both CTAs are ready behind it.
+__device__ __forceinline__ void start_pair() {
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+}
+
 // Arrive on the leading CTA's barrier at this offset. What it announces is read by the tensor
 // cores alone, where it lies, and has been fenced towards them; a release at cluster scope
 // would wait for the thread's loads in flight as well (5900 instead of 5050 clocks a tile of
@@ -249,7 +265,10 @@ struct CodePieces {
 __device__ __forceinline__ void convert_role(const CacheAttentionArgs& a, const Work& w, const Visible& vis, Smem* sm,
                                              uint32_t s_k, uint32_t s_v, int rank) {
   const int tid = threadIdx.x - 256, lane = tid & 31;
-  if ((a.flags & QKV_CTE_FLAG_TEST_STALL) != 0) return;  // test hook: hand out nothing
+  if ((a.flags & QKV_CTE_FLAG_TEST_STALL) != 0) {  // test hook: hand out nothing
+    start_pair();
+    return;
+  }
   // K: rows krow + 16 i of this CTA's 64 keys, piece kp of 8. V: rows vrow + 32 i of the 128
   // keys, piece vp of this CTA's half of the lanes (of d rounded up to 32). Threads beyond the
   // lanes store zeros where nothing that counts is read.
@@ -294,6 +313,7 @@ __device__ __forceinline__ void convert_role(const CacheAttentionArgs& a, const 
   scales(page);
   load_k(page);
   load_v(page, 0);
+  start_pair();
   for (int j = 0; j < w.n; ++j) {
     const int st = j & 1;
     const uint32_t ph = (j >> 1) & 1;
@@ -341,7 +361,6 @@ __device__ __forceinline__ void convert_role(const CacheAttentionArgs& a, const 
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ bool issue_all(const CacheAttentionArgs& a, const Work& w, Smem* sm, uint32_t s_q,
                                           uint32_t s_k, uint32_t s_v) {
-  const uint32_t tmem = 0;  // all columns are this CTA's
   const int tiles = __shfl_sync(0xffffffffu, w.two ? 2 : 1, 0);
   const int n = __shfl_sync(0xffffffffu, w.n, 0);
   const int steps = a.pool.d >> 4;
@@ -352,7 +371,7 @@ __device__ __forceinline__ bool issue_all(const CacheAttentionArgs& a, const Wor
   // (nvcc 13.0).
   auto scores = [&](int x, int st) {
     const uint64_t qd = q_desc + (x * kQBytes >> 4), kd = k_desc + (st * kKBytes >> 4);
-    const uint32_t to = tmem + kSCol + x * 128;
+    const uint32_t to = kSCol + x * 128;
     auto step = [&](int ks) {
       mma_f16_ss(to, qd + (((ks >> 2) * kQHalf + (ks & 3) * 32) >> 4), kd + (((ks >> 2) * kKHalf + (ks & 3) * 32) >> 4),
                  id_s, ks > 0 ? 1u : 0u);
@@ -386,7 +405,7 @@ __device__ __forceinline__ bool issue_all(const CacheAttentionArgs& a, const Wor
       const uint64_t vd = v_desc + (st * kVBytes >> 4);
 #pragma unroll
       for (int ks = 0; ks < kTileKeys / 16; ++ks)
-        mma_f16_ts(tmem + kOCol + x * 128, tmem + kSCol + x * 128 + 8 * ks, vd + (ks * 2048 >> 4), id_o,
+        mma_f16_ts(kOCol + x * 128, kSCol + x * 128 + 8 * ks, vd + (ks * 2048 >> 4), id_o,
                    ks > 0 || j > 0 ? 1u : 0u);
       if (x == tiles - 1) commit_both(&sm->v_empty[st]);
       if (j + 1 == n) {
@@ -406,7 +425,7 @@ __device__ __forceinline__ bool issue_all(const CacheAttentionArgs& a, const Wor
 // ---------------------------------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const Work& w, const Visible& vis, Smem* sm,
-                                             uint32_t s_q, uint32_t tmem, int x, int rank) {
+                                             uint32_t s_q, int x, int rank) {
   const int row = threadIdx.x & 127;                   // of the tile: also its TMEM lane
   const int first_row = w.r0 + (2 * x + rank) * kTileRows;
   const int r = first_row + row;
@@ -415,7 +434,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
   const bool live = inside && s < vis.count;
   const int lo = live ? vis.lo(a, s) : 0, hi = live ? vis.hi(a, s) : 0;
   const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
-  const uint32_t t_s = tmem + lanes + kSCol + x * 128, t_o = tmem + lanes + kOCol + x * 128;
+  const uint32_t t_s = lanes + kSCol + x * 128, t_o = lanes + kOCol + x * 128;
   const int d = a.pool.d;
   float coef;
 
@@ -424,21 +443,23 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     const T* p = static_cast<const T*>(a.q.p) + w.b * a.q.sb + s * a.q.ss + head * a.q.sh;
     uint32_t q[64];
     uint32_t top = 0;
+    // a lane's row is its own, so an access is a sector of 32 bytes per lane: with 16 bytes each
+    // sector is asked for twice
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
+    for (int c = 0; c < 8; ++c) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q[4 * c + i] = 0;
-      if (live && 8 * c < d) {
-        if (a.wide) {
-          const uint4 v = *reinterpret_cast<const uint4*>(p + 8 * c);
-          q[4 * c] = v.x, q[4 * c + 1] = v.y, q[4 * c + 2] = v.z, q[4 * c + 3] = v.w;
+      for (int i = 0; i < 8; ++i) q[8 * c + i] = 0;
+      if (live && 16 * c < d) {
+        if (a.wide32) {
+          ld_global32(q + 8 * c, p + 16 * c);
         } else {
-          const uint16_t* e = reinterpret_cast<const uint16_t*>(p + 8 * c);
+          const uint16_t* e = reinterpret_cast<const uint16_t*>(p + 16 * c);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) q[4 * c + i] = e[2 * i] | static_cast<uint32_t>(e[2 * i + 1]) << 16;
+          for (int i = 0; i < 8; ++i) q[8 * c + i] = e[2 * i] | static_cast<uint32_t>(e[2 * i + 1]) << 16;
         }
       }
     }
+    start_pair();
 #pragma unroll
     for (int i = 0; i < 64; ++i) top = __vmaxu2(top, q[i] & 0x7FFF7FFFu);
     top = max(top & 0xFFFFu, top >> 16);
@@ -629,12 +650,11 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         reinterpret_cast<float4*>(part + 16 * c)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else if (a.wide_out) {
+    } else if (a.wide32_out) {
       uint32_t pk[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) pk[i] = pack_pair<T>(make_float2(v[2 * i], v[2 * i + 1]));
-      reinterpret_cast<uint4*>(out + 16 * c)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-      reinterpret_cast<uint4*>(out + 16 * c)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+      st_global_v8_b32(out + 16 * c, pk);
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) out[16 * c + i] = from_f32<T>(v[i]);
@@ -658,44 +678,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1) cac
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int rank = static_cast<int>(cluster_ctarank());
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sm->q_full[i]), 8);  // a warp's arrival each: four of either CTA
-      mbar_init(smem_u32(&sm->s_full[i]), 1);
-      mbar_init(smem_u32(&sm->p_full[i]), 8);
-      mbar_init(smem_u32(&sm->o_full[i]), 1);
-    }
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&sm->k_full[i]), 8);
-      mbar_init(smem_u32(&sm->k_empty[i]), 1);
-      mbar_init(smem_u32(&sm->v_full[i]), 8);
-      mbar_init(smem_u32(&sm->v_empty[i]), 1);
-    }
-    for (int i = 0; i < kMetaSlots; ++i) mbar_init(smem_u32(&sm->meta_full[i]), 1);
-    mbar_init(smem_u32(&sm->drain), 1);
-    sm->abort = 0;
-    fence_barrier_init();
-  }
-  if (warp == 12) {
-    tmem_alloc_pair(smem_u32(&sm->tmem), 512);
-    tmem_relinquish_pair();
-  }
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();  // both CTAs' barriers are ready
-  tc_fence_after();
-  const uint32_t tmem = sm->tmem;
-
   Work w(a, blockIdx.x >> 1);
   const Visible vis(a, w.b);
   w.plan(a, vis);
 
   if (warp < 8) {
     const int x = warp >> 2;
-    if (x == 0 || w.two) softmax_role<T>(a, w, vis, sm, s_q, tmem, x, rank);
+    if (x == 0 || w.two)
+      softmax_role<T>(a, w, vis, sm, s_q, x, rank);
+    else
+      start_pair();
   } else if (warp < 12) {
     convert_role(a, w, vis, sm, s_k, s_v, rank);
   } else {
+    if ((threadIdx.x & 31) == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&sm->q_full[i]), 8);  // a warp's arrival each: four of either CTA
+        mbar_init(smem_u32(&sm->s_full[i]), 1);
+        mbar_init(smem_u32(&sm->p_full[i]), 8);
+        mbar_init(smem_u32(&sm->o_full[i]), 1);
+      }
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(smem_u32(&sm->k_full[i]), 8);
+        mbar_init(smem_u32(&sm->k_empty[i]), 1);
+        mbar_init(smem_u32(&sm->v_full[i]), 8);
+        mbar_init(smem_u32(&sm->v_empty[i]), 1);
+      }
+      for (int i = 0; i < kMetaSlots; ++i) mbar_init(smem_u32(&sm->meta_full[i]), 1);
+      mbar_init(smem_u32(&sm->drain), 1);
+      sm->abort = 0;
+      fence_barrier_init();
+    }
+    __syncwarp();
+    tmem_alloc_pair(smem_u32(&sm->tmem), 512);
+    tmem_relinquish_pair();
+    start_pair();
     if (rank == 0 && w.n > 0 && !issue_all(a, w, sm, s_q, s_k, s_v)) {
       // what was issued reads shared memory and writes tensor memory: let it end
       commit_both(&sm->drain);
@@ -708,7 +725,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1) cac
   cluster_sync();  // nothing of the pair reads the other's memory any more
   if (warp == 12) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc_pair(sm->tmem, 512);
   }
 }
 

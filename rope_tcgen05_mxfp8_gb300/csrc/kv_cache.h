@@ -54,7 +54,8 @@ struct CacheAttentionArgs {
   int splits;            // parts of the keys
   float scale_log2;      // softmax scale * log2(e)
   int causal, window;    // window 0: none
-  int wide, wide_out;    // rows of q, of out start on 16-byte boundaries
+  int wide;              // rows of q start on 16-byte boundaries
+  int wide32, wide32_out;  // rows of q, of out start on 32-byte boundaries
   float* part_o;         // splits > 1: [splits][batch * seq * q_heads][d], each part normalised
   float* part_lse;       // splits > 1: [splits][batch * seq * q_heads], base 2
   uint32_t* status;

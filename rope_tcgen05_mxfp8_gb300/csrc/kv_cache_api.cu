@@ -109,10 +109,10 @@ HeadsTensor as_args(const HeadsView& t) {
   return HeadsTensor{const_cast<void*>(t.p), t.batch > 1 ? t.sb : 0, t.seq > 1 ? t.ss : 0, t.heads > 1 ? t.sh : 0};
 }
 
-// Whether every row of heads starts on a 16-byte boundary (16-byte groups of lanes).
-bool wide_rows(const HeadsTensor& t, size_t elem) {
-  const int64_t n = 16 / static_cast<int64_t>(elem);
-  return aligned(t.p, 16) && t.sb % n == 0 && t.ss % n == 0 && t.sh % n == 0;
+// Whether every row of heads starts on a boundary of `bytes` (16, 32).
+bool wide_rows(const HeadsTensor& t, size_t elem, size_t bytes = 16) {
+  const int64_t n = static_cast<int64_t>(bytes / elem);
+  return aligned(t.p, bytes) && t.sb % n == 0 && t.ss % n == 0 && t.sh % n == 0;
 }
 
 // Writing and reading back share all but the direction.
@@ -362,7 +362,8 @@ int qkv_cte_cache_attention(qkv_cte_cache_plan_t plan, const qkv_cte_cache_pages
   a.causal = causal;
   a.window = window;
   a.wide = wide_rows(a.q, e);
-  a.wide_out = wide_rows(a.out, e);
+  a.wide32 = wide_rows(a.q, e, 32);
+  a.wide32_out = wide_rows(a.out, e, 32);
   a.status = status;
   a.flags = plan->d.flags;
   if (s.splits > 1) {
