@@ -606,7 +606,7 @@ int qkv_cte_cache_read(qkv_cte_cache_plan_t plan, const qkv_cte_cache_pages* pag
  *             share it.
  * status    : a device word, zero before its first use, which a call sets but never clears
  *             when a bounded wait runs out: qkv_cte_status(status, stream) reads it
- * Returns 0, -1, -2, -3 or -4. */
+ * At most 2^31 - 1025 rows [batch, seq, n_q_heads]. Returns 0, -1, -2, -3 or -4. */
 int qkv_cte_cache_attention(qkv_cte_cache_plan_t plan, const qkv_cte_cache_pages* pages, const void* q,
                             int64_t q_batch_stride, int64_t q_row_stride, int64_t q_head_stride, void* out,
                             int64_t out_batch_stride, int64_t out_row_stride, int64_t out_head_stride, float* lse,

@@ -98,8 +98,8 @@ struct Visible {
   }
   __device__ __forceinline__ int lo(const CacheAttentionArgs& a, int s) const {
     if (a.window == 0) return 0;
-    const int first = first_pos + s - a.window + 1;
-    return first > 0 ? first : 0;
+    const long long first = static_cast<long long>(first_pos) + s - a.window + 1;
+    return first > 0 ? static_cast<int>(first) : 0;
   }
 };
 

@@ -32,7 +32,7 @@ constexpr int kMaxSplits = 64;
 //   96                   57.9 / 60.8
 //   128   22.9 / 15.9    94.9 / 63.9
 constexpr int64_t kFewMaxRows = 64;
-constexpr int64_t kMaxPositions = INT32_MAX - 1024;  // positions rounded up to tiles stay inside 32 bits
+constexpr int64_t kMaxPositions = INT32_MAX - 1024;  // positions and rows rounded up to tiles stay inside 32 bits
 
 size_t elem_size(int dtype) { return dtype == QKV_CTE_DTYPE_FP32 ? 4 : 2; }
 
@@ -93,8 +93,8 @@ int check_pool(qkv_cte_cache_plan_t plan, const qkv_cte_cache_pages* pages, int6
 
 int check_counts(int64_t batch, int64_t seq, int64_t heads, const char* who) {
   if (batch < 0 || seq < 0) return fail(QKV_CTE_ERR_INVALID, "%s: batch and seq must be >= 0", who);
-  if (batch > INT32_MAX || seq > kMaxPositions || (seq > 0 && batch > INT32_MAX / heads / seq))
-    return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: more than INT32_MAX rows of heads", who);
+  if (batch > INT32_MAX || seq > kMaxPositions || (seq > 0 && batch > kMaxPositions / heads / seq))
+    return fail(QKV_CTE_ERR_UNSUPPORTED, "%s: more than INT32_MAX - 1024 rows of heads", who);
   return QKV_CTE_OK;
 }
 

@@ -143,7 +143,7 @@ LONG = dict(table=68 * MB, stride=4096, blocks=4096, longest=131072, batch=1, se
     (dict(kc=None), -1), (dict(vc=64 * MB + 1), -2), (dict(blocks=0), -1), (dict(table=None, blocks=5), -1),
     (dict(heads=0), -1), (dict(heads=3), -1), (dict(heads=-2), -1), (dict(longest=-1), -1),
     (dict(batch=-1), -1), (dict(seq=-1), -1), (dict(batch=0), 0), (dict(seq=0), 0),
-    (dict(seq=2 ** 31 - 1), -2), (dict(heads=2 ** 30), -2),
+    (dict(seq=2 ** 31 - 1), -2), (dict(heads=2 ** 30), -2), (dict(batch=1, seq=(2 ** 31 - 1024) // 4), -2),
     (dict(dtype=2), -2), (dict(dtype=3), -1),
     (dict(scale=0.0), -1), (dict(scale=-1.0), -1), (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1),
     (dict(causal=2), -1), (dict(window=-1), -1), (dict(window=5), -1),

@@ -127,7 +127,7 @@ def test_shared_heads(nq, nkv, S):
     Case([200, 65], S=S, nq=nq, nkv=nkv, d=64, causal=True, dt="fp16").run_and_check()
 
 
-@pytest.mark.parametrize("window", [1, 2, 16, 63, 100, 1000])
+@pytest.mark.parametrize("window", [1, 2, 16, 63, 100, 1000, 2 ** 31 - 1])
 @pytest.mark.parametrize("S", [1, 4, 200])
 def test_window(window, S):
     Case([400, 201, 64, 3], S=S, causal=True, window=window, bt=32).run_and_check()
