@@ -9,7 +9,7 @@
 //   conversion warps read the codes of K and V, turn them into fp16 (exact: e4m3 is a subset)
 //     and store them swizzled for the tensor cores, a tile ahead. Each CTA converts half: 64 of
 //     the keys of K, half of the lanes of V;
-//   one thread of the leading CTA issues S = Q K^T (both in shared memory) and O += P V (P in
+//   one warp of the leading CTA issues S = Q K^T (both in shared memory) and O += P V (P in
 //     tensor memory) as M = 256 instructions over the pair, which read each half where it is;
 //   two groups of four softmax warps per CTA, a thread per row, take S out of tensor memory,
 //     and put P back over it as fp16.
@@ -18,15 +18,15 @@
 // product would have to be 8-bit, and weights and queries rounded to three digits are not
 // attention; the conversion is shared by 512 rows.
 //
-// What bounds it (972 x 4096, 38 heads of 128: 77.5 us, 1.00 PFLOP/s, 0.53 of the measured rate;
+// What bounds it (972 x 4096, 38 heads of 128: 76 to 78 us, 1.0 PFLOP/s, 0.53 of the measured rate;
 // 32760 keys 0.52): a tile of 128 keys takes some 4700 clocks for 2048 of products. An
 // instruction with A from shared memory takes 86 to 95 clocks instead of 64 by itself, and each
 // row tile goes round a chain of softmax (2000), arrival from the other CTA, O += P V and the
 // next S. Tried: a CTA by itself (twice the conversion per SM: 700 TFLOP/s), P through shared
 // memory so that S is free sooner (870), two softmax threads per row (590, held by the three
 // conversion warps that were left room for), one row tile per pair and two blocks per SM (830).
-// Short key ranges are bound by what comes before and after: 32760 queries over 128 keys take 466
-// us, 14 a block, so that over 512 keys (673) more than half is not products.
+// Short key ranges are bound by what comes before and after: 32760 queries over 128 keys take 375
+// us, 11 a pair of blocks, so that over 512 keys (582) more than half is not products.
 //
 // Scales. A key's block scale multiplies its score in fp32. A value's block scale multiplies
 // its weight before the rounding to fp16, relative to the largest value scale so far (an
@@ -357,7 +357,7 @@ __device__ __forceinline__ void convert_role(const CacheAttentionArgs& a, const 
 }
 
 // ---------------------------------------------------------------------------------------
-// Issue: one thread of the leading CTA
+// Issue: one warp of the leading CTA
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ bool issue_all(const CacheAttentionArgs& a, const Work& w, Smem* sm, uint32_t s_q,
                                           uint32_t s_k, uint32_t s_v) {
