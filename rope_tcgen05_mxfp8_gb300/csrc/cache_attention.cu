@@ -18,8 +18,8 @@
 // product would have to be 8-bit, and weights and queries rounded to three digits are not
 // attention; the conversion is shared by 512 rows.
 //
-// What bounds it (972 x 4096, 38 heads of 128: 76 to 78 us, 1.0 PFLOP/s, 0.53 of the measured rate;
-// 32760 keys 0.52): a tile of 128 keys takes some 4700 clocks for 2048 of products. An
+// What bounds it (972 x 4096, 38 heads of 128: 70 us, 1.11 PFLOP/s, 0.59 of the measured rate; 4680 x
+// 32760, 40 heads 0.54): a tile of 128 keys takes some 4300 clocks for 2048 of products. An
 // instruction with A from shared memory takes 86 to 95 clocks instead of 64 by itself, and each
 // row tile goes round a chain of softmax (2000), arrival from the other CTA, O += P V and the
 // next S. Tried: a CTA by itself (twice the conversion per SM: 700 TFLOP/s), P through shared
@@ -64,6 +64,7 @@ constexpr float kGrowth = 8.0f;                   // binary orders the maximum m
 constexpr uint64_t kWaitNs = 2000000000ull;
 // TMEM columns: S (and P) of both tiles, then O. The block has all 512, so they count from 0.
 constexpr uint32_t kSCol = 0, kOCol = 256;
+
 // What the softmax warps need to know about a tile of keys, by groups of 16.
 struct TileMeta {
   float ck[8];      // key scale (NaN: 255)
@@ -186,7 +187,9 @@ struct Work {
   }
 };
 
-// Every role's waits: bounded, and given up when another role of the CTA has failed.
+// Every role's waits: bounded, and given up when another role of the CTA has failed. The
+// hardware is asked to hold a waiting warp for up to 100 us at a time: warps that poll take
+// issue slots from those that work (5050 instead of 4800 clocks a tile of keys).
 __device__ __forceinline__ bool try_wait_held(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -321,8 +324,8 @@ __device__ __forceinline__ void convert_role(const CacheAttentionArgs& a, const 
     ahead = entry(j + 2);
     if (!__all_sync(0xffffffffu, wait_for(&sm->k_empty[st], ph ^ 1u, sm, a.status, kErrProducerEmptyWait))) return;
     if (tid < 32) {
-      // the slot's last readers have handed in their weights: the issue of the scores that
-      // freed this stage came after them
+      // the slot's last readers (of tile j - 4) have handed in their weights: the scores that freed
+      // this stage, of tile j - 2, were issued behind the weights of tile j - 3
       TileMeta& m = sm->meta[j & (kMetaSlots - 1)];
       const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
       const uint32_t vnan = __ballot_sync(0xffffffffu, ev == kScaleNan);
@@ -367,8 +370,8 @@ __device__ __forceinline__ bool issue_all(const CacheAttentionArgs& a, const Wor
   const uint32_t id_s = idesc_f16(kTileKeys, false);
   const uint32_t id_o = idesc_f16((a.pool.d + 31) & ~31, true);
   const uint64_t q_desc = smem_desc_sw128(s_q), k_desc = smem_desc_sw128(s_k), v_desc = smem_desc_sw128(s_v);
-  // Straight lines of eight: with a condition around each instruction the scores were wrong
-  // (nvcc 13.0).
+  // Straight lines of eight: what stands between two instructions is added to their 64 clocks
+  // (and with a condition around each one the scores were wrong, nvcc 13.0).
   auto scores = [&](int x, int st) {
     const uint64_t qd = q_desc + (x * kQBytes >> 4), kd = k_desc + (st * kKBytes >> 4);
     const uint32_t to = kSCol + x * 128;
@@ -523,7 +526,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     };
     if (dead || (key0 >= all_lo && key0 + kTileKeys <= all_hi && meta.there == 0xFFu && meta.vnan == 0)) {
       float top = -INFINITY;
-#pragma unroll 1
+#pragma unroll 2
       for (int c = 0; c < 4; ++c) {
         float z[32];
         tmem_ld_32x32b_x32(t_s + 32 * c, reinterpret_cast<uint32_t*>(z));
@@ -541,7 +544,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
       }
       follow(top);
       const float use = m == -INFINITY ? 0.0f : m;
-#pragma unroll 1
+#pragma unroll 2
       for (int c = 0; c < 4; ++c) {
         float z[32];
         uint32_t pk[16];

@@ -265,6 +265,24 @@ def test_long(S):
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("S", [1, 200])
+def test_far_pages(S):
+    """Codes past 2^32 bytes of the pool give what the same codes near its start give."""
+    n, d, bt, T = 40, 128, 64, 1900
+    pages = (1 << 32) // (n * d * bt) + 40
+    far = lib.QkvCteCache(pages, n, d, block_tokens=bt, k=torch.empty(pages, n, bt, d, dtype=torch.uint8, device=DEV),
+                          v=torch.empty(pages, n, bt, d, dtype=torch.uint8, device=DEV))
+    near = lib.QkvCteCache(30, n, d, block_tokens=bt)
+    table = torch.arange(pages - 1, pages - 31, -1, dtype=torch.int32, device=DEV)[None]
+    k, v = torch.randn(2, 1, T, n, d, device=DEV).bfloat16()
+    q = torch.randn(1, S, n, d, device=DEV).bfloat16()
+    far.write(k, v, _i32([0]), table=table)
+    near.write(k, v, _i32([0]))
+    a = far.attention(q, _i32([T]), table=table, causal=True, max_length=T)[0]
+    b = near.attention(q, _i32([T]), causal=True, max_length=T)[0]
+    assert torch.equal(a, b)
+
+
 def test_lengths_beyond_the_table():
     c = Case([128, 128], S=2, bt=64)
     want, _ = c.run()
