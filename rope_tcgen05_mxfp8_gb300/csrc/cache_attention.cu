@@ -636,7 +636,8 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     tc_fence_after();
   }
   const bool none = l == 0.0f || !live;  // no key seen, or a row of padding: zeros
-  const float f = none ? 0.0f : scale_value(max(ref - kBias, 0)) / l;
+  const float f = none ? 0.0f : 0x1p-7f / l, unit = scale_value(ref);  // in turn: 2^(ref - 134) need not be normal
+  static_assert(kBias == 7, "2^-7");
   T* out = static_cast<T*>(a.out.p) + w.b * a.out.sb + s * a.out.ss + head * a.out.sh;
   float* part = a.splits > 1 ? a.part_o + (w.split * all_rows + out_row) * d : nullptr;
   for (int c = 0; c < d / 16; ++c) {
@@ -648,7 +649,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     if (!inside) continue;
     float v[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = none ? 0.0f : __uint_as_float(o[i]) * f;
+    for (int i = 0; i < 16; ++i) v[i] = none ? 0.0f : __uint_as_float(o[i]) * f * unit;
     if (part != nullptr) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
