@@ -1,8 +1,8 @@
 // Attention of many queries over the 8-bit cache on the tensor cores.
 //
-//   z_t = c q . k_t,  p_t = 2^(z_t - m),  o = sum_t p_t v_t / sum_t p_t
-// with c = scale log2(e) and a running reference m per row: one pass over the keys, nothing
-// of the score matrix leaves the SM.
+//   z_t = c q . k_t,  o = sum_t 2^z_t v_t / sum_t 2^z_t
+// with c = scale log2(e) and running references per row: one pass over the keys, nothing of
+// the score matrix leaves the SM.
 //
 // A pair of CTAs owns two tiles of 256 query rows (a row is a token and one of the query heads
 // that share the key head), 128 rows of each tile per CTA, and walks the keys 128 at a time:
@@ -28,14 +28,22 @@
 // Short key ranges are bound by what comes before and after: 32760 queries over 128 keys take 375
 // us, 11 a pair of blocks, so that over 512 keys (582) more than half is not products.
 //
-// Scales. A key's block scale multiplies its score in fp32. A value's block scale multiplies
-// its weight before the rounding to fp16, relative to the largest value scale so far (an
-// exact power of two), 2^7 above: with weights of at most 2^8 (below) that fills fp16's
-// range from the top, so 28 binary orders keep their digits.
+// Scales. A key's block scale multiplies its score in fp32. A value's block scale 2^x_t multiplies
+// its weight before the rounding to fp16 (the products take no more digits at this rate; by 2^-11
+// at most, an eighth of what a result's rounding to bf16 may cost and as much as one to fp16, and
+// it averages out over the keys), so what is rounded is 2^(z_t + x_t - m), with m the row's own maximum of z_t + x_t over the keys it sees: neither a
+// key that it does not see nor one whose weight makes its large values negligible takes digits from
+// the others. References are whole numbers, so that every change of one is exact. With 2^7 above,
+// the row's largest weight is 2^6 or more: down to 2^-20 of it weights keep fp16's digits, and
+// what is 2^-31 of it is lost.
+// The sum of the 2^z_t has a reference n of its own. As long as the value scales met lie within
+// 2^60 of one another its terms are the weights without their 2^x_t, one exponential for both,
+// and n is m less the first tile's largest x. Beyond (a page of zeros has the least scale there
+// is) the terms are taken by themselves, as 2^(z_t - n), in the path that masked tiles take.
 //
-// The reference m follows the maximum lazily: O in tensor memory is rescaled only when the
-// maximum has grown by more than 2^8 (or a larger value scale has come), which after the
-// first tiles is hardly ever; weights then reach 2^8 instead of 1, which costs nothing.
+// m follows its maximum lazily: O in tensor memory is rescaled only when that has grown by more
+// than 2^8, which after the first tiles is hardly ever; weights then reach 2^15 instead of 2^7,
+// which costs nothing.
 #include "fp32x2.cuh"
 #include "internal.h"
 #include "kv_cache.cuh"
@@ -61,21 +69,26 @@ constexpr int kKBytes = 2 * kKHalf;
 constexpr int kVBytes = kTileKeys * 128;          // 128 keys, this CTA's lanes of them (64 at most)
 constexpr int kBias = 7;                          // weights are held 2^7 above their value
 constexpr float kGrowth = 8.0f;                   // binary orders the maximum may grow before a rescale
+constexpr int kNear = 60;                         // binary orders of value scales that share an exponential
 constexpr uint64_t kWaitNs = 2000000000ull;
 // TMEM columns: S (and P) of both tiles, then O. The block has all 512, so they count from 0.
 constexpr uint32_t kSCol = 0, kOCol = 256;
 
 // What the softmax warps need to know about a tile of keys, by groups of 16.
 struct TileMeta {
-  float ck[8];      // key scale (NaN: 255)
-  int ev[8];        // exponent of the value scale (of an absent or NaN group: 0)
+  float2 kx[8];     // key scale (NaN: 255), exponent of the value scale (of an absent or NaN group: origin)
+  float back[8];    // a weight without its value scale and 2^7, in the unit of the sum
   uint32_t there;   // groups with a page and tokens
   uint32_t vnan;    // groups whose value scale is NaN
-  int top_ev;
-  int pad;
+  int origin;       // exponent of the first tile's largest value scale (0 without one)
+  int apart;        // value scales more than 2^60 apart have been met
 };
+static_assert(sizeof(TileMeta) % 16 == 0, "pairs of kx in one access");
 
-struct Smem {
+// 2^x for a whole number x <= 0 (and minus infinity; 2^-127 is the least).
+__device__ __forceinline__ float pow2_down(float x) { return scale_value(max(127 + __float2int_rz(x), 0)); }
+
+struct alignas(16) Smem {
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t meta_full[kMetaSlots];
@@ -296,7 +309,7 @@ __device__ __forceinline__ void convert_role(const CacheAttentionArgs& a, const 
     return cache_entry(a.pool, w.b, key >> a.pool.log_bt);
   };
   auto checked = [&](int e) { return e >= 0 && e < a.pool.pages ? e : -1; };
-  int ek = 0, ev = 0;
+  int ek = 0, ev = 0, least = kScaleNan, most = -1, origin = 127;
   auto scales = [&](int page) {
     ek = ev = 0;
     if (page >= 0 && tid < 32) {
@@ -329,16 +342,24 @@ __device__ __forceinline__ void convert_role(const CacheAttentionArgs& a, const 
       TileMeta& m = sm->meta[j & (kMetaSlots - 1)];
       const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
       const uint32_t vnan = __ballot_sync(0xffffffffu, ev == kScaleNan);
-      if (ev == kScaleNan) ev = 0;
-      const int top = __reduce_max_sync(0xffffffffu, ev);
+      const bool counts = page >= 0 && ev != kScaleNan;
+      least = min(least, __reduce_min_sync(0xffffffffu, counts ? ev : kScaleNan));
+      most = max(most, __reduce_max_sync(0xffffffffu, counts ? ev : -1));
+      if (j == 0) {
+        if (most < 0) most = 127;
+        least = min(least, most);
+        origin = most;
+      }
       if (lane < 8) {
-        m.ck[lane] = scale_value(ek);
-        m.ev[lane] = ev;
+        const int x = counts ? ev : origin;
+        m.kx[lane] = make_float2(scale_value(ek), static_cast<float>(x - 127));
+        m.back[lane] = scale_value(min(max(127 - kBias + origin - x, 0), 254));
       }
       if (lane == 0) {
         m.there = there;
         m.vnan = vnan;
-        m.top_ev = top;
+        m.origin = origin - 127;
+        m.apart = most - least > kNear;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm->meta_full[j & (kMetaSlots - 1)]));
@@ -492,8 +513,10 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
   const int s_last = last_row / a.group < vis.count - 1 ? last_row / a.group : vis.count - 1;
   const int all_lo = vis.lo(a, s_last < 0 ? 0 : s_last), all_hi = vis.hi(a, first_row / a.group);
 
-  float m = -INFINITY, l = 0.0f;
-  int ref = 1;
+  // references of the weights and (where scales lie apart) of the sum, minus infinity before a key
+  // is seen; the sum
+  float m = -INFINITY, n = -INFINITY, l = 0.0f;
+  bool apart = false;
   for (int j = 0; j < w.n; ++j) {
     const int slot = j & (kMetaSlots - 1);
     bool ok = wait_for(&sm->meta_full[slot], (j / kMetaSlots) & 1, sm, a.status, kErrEpilogueTmemFullWait);
@@ -502,35 +525,34 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     tc_fence_after();
     const TileMeta& meta = sm->meta[slot];
     const int key0 = (w.key_tile0 + j) * kTileKeys;
-    // the reference and the sums follow a tile's maximum and largest value scale
+    if (meta.apart != 0 && !apart) {
+      apart = true;
+      n = m - static_cast<float>(meta.origin);
+    }
+    // the weights' reference follows the tile's maximum of z + x
     auto follow = [&](float top) {
-      const int top_ev = meta.top_ev;
-      if (!__any_sync(0xffffffffu, top > m + kGrowth) && top_ev <= ref) return;
-      const float now = fmaxf(m, top);
-      const float keep = exp2_fast(m - (now == -INFINITY ? 0.0f : now));
-      const int newref = max(ref, top_ev);
-      if (j > 0) {
-        const float f = keep * scale_value(max(127 - (newref - ref), 1));
-        for (int c = 0; c < (d > 64 ? 8 : 4); ++c) {
-          uint32_t o[16];
-          tmem_ld_32x32b_x16(t_o + 16 * c, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st_32x32b_x16(t_o + 16 * c, o);
-        }
-      }
-      l *= keep;
+      if (!__any_sync(0xffffffffu, top > m + kGrowth)) return;
+      const float now = fmaxf(m, ceilf(top));
+      const float f = pow2_down(m - now);
       m = now;
-      ref = newref;
+      if (!apart) l *= f;
+      if (j == 0) return;
+      for (int c = 0; c < (d > 64 ? 8 : 4); ++c) {
+        uint32_t o[16];
+        tmem_ld_32x32b_x16(t_o + 16 * c, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tmem_st_32x32b_x16(t_o + 16 * c, o);
+      }
     };
-    if (dead || (key0 >= all_lo && key0 + kTileKeys <= all_hi && meta.there == 0xFFu && meta.vnan == 0)) {
+    if (dead || (key0 >= all_lo && key0 + kTileKeys <= all_hi && meta.there == 0xFFu && meta.vnan == 0 && !apart)) {
       float top = -INFINITY;
 #pragma unroll 2
       for (int c = 0; c < 4; ++c) {
         float z[32];
         tmem_ld_32x32b_x32(t_s + 32 * c, reinterpret_cast<uint32_t*>(z));
-        const float2 ck = *reinterpret_cast<const float2*>(&meta.ck[2 * c]);
+        const float4 kx = *reinterpret_cast<const float4*>(&meta.kx[2 * c]);
         tmem_ld_wait();
         float t[2];
 #pragma unroll
@@ -540,22 +562,21 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
           for (int i = 3; i < 15; i += 2) t[g] = max3(t[g], z[16 * g + i], z[16 * g + i + 1]);
           t[g] = fmaxf(t[g], z[16 * g + 15]);
         }
-        top = max3(top, t[0] * (coef * ck.x), t[1] * (coef * ck.y));
+        top = max3(top, fmaf(t[0], coef * kx.x, kx.y), fmaf(t[1], coef * kx.z, kx.w));
       }
       follow(top);
-      const float use = m == -INFINITY ? 0.0f : m;
+      const float up = kBias - (m == -INFINITY ? 0.0f : m);
 #pragma unroll 2
       for (int c = 0; c < 4; ++c) {
         float z[32];
         uint32_t pk[16];
         tmem_ld_32x32b_x32(t_s + 32 * c, reinterpret_cast<uint32_t*>(z));
-        const float2 ck = *reinterpret_cast<const float2*>(&meta.ck[2 * c]);
-        const int2 ev = *reinterpret_cast<const int2*>(&meta.ev[2 * c]);
+        const float4 kx = *reinterpret_cast<const float4*>(&meta.kx[2 * c]);
+        const float2 back = *reinterpret_cast<const float2*>(&meta.back[2 * c]);
         tmem_ld_wait();
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const int lf = max((g == 0 ? ev.x : ev.y) - ref + kBias, -40);  // further down fp16 holds nothing
-          const float add = static_cast<float>(lf) - use, mul = coef * (g == 0 ? ck.x : ck.y);
+          const float add = (g == 0 ? kx.y : kx.w) + up, mul = coef * (g == 0 ? kx.x : kx.z);
           const float2 cc = make_float2(mul, mul), aa = make_float2(add, add);
           float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -566,12 +587,12 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
             sum = fadd2(sum, e);
             pk[8 * g + i] = pack_pair<__half>(e);
           }
-          l = fmaf(sum.x + sum.y, scale_value(127 - lf), l);
+          l = fmaf(sum.x + sum.y, g == 0 ? back.x : back.y, l);
         }
         tmem_st_32x32b_x16(t_s + 16 * c, pk);
       }
     } else {
-      // Masked, or with a NaN among the value scales: 16 keys at a time, scores read twice.
+      // Masked, with a NaN among the value scales, or with scales far apart: 16 keys at a time.
       // Bit i of `seen`: the row sees key i of the group.
       const uint32_t there = meta.there, vnan = meta.vnan;
       auto seen_bits = [&](int g) {
@@ -580,7 +601,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
         bits &= from <= 0 ? 0xFFFFu : from >= 16 ? 0u : ~((1u << from) - 1u);
         return (there >> g & 1) != 0 ? bits : 0u;
       };
-      float top = -INFINITY;
+      float top = -INFINITY, top_z = -INFINITY;
 #pragma unroll 1
       for (int g = 0; g < 8; ++g) {
         uint32_t z[16];
@@ -590,18 +611,25 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
         float t = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 16; ++i) t = fmaxf(t, (seen >> i & 1) ? __uint_as_float(z[i]) : -INFINITY);
-        top = fmaxf(top, t * (coef * meta.ck[g]));
+        t *= coef * meta.kx[g].x;
+        top_z = fmaxf(top_z, t);
+        top = fmaxf(top, t + meta.kx[g].y);
       }
       follow(top);
-      const float use = m == -INFINITY ? 0.0f : m;
+      const float up = kBias - (m == -INFINITY ? 0.0f : m);
+      if (apart) {
+        const float now = fmaxf(n, ceilf(top_z));
+        l *= pow2_down(n - now);
+        n = now;
+      }
+      const float up_n = n == -INFINITY ? 0.0f : -n;
 #pragma unroll 1
       for (int g = 0; g < 8; ++g) {
         uint32_t z[16], pk[8];
         tmem_ld_32x32b_x16(t_s + 16 * g, z);
         tmem_ld_wait();
         const uint32_t seen = seen_bits(g);
-        const int lf = max(meta.ev[g] - ref + kBias, -40);
-        const float add = static_cast<float>(lf) - use, mul = coef * meta.ck[g];
+        const float add = meta.kx[g].y + up, mul = coef * meta.kx[g].x;
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -617,8 +645,16 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
           }
           pk[i] = pack_pair<__half>(e);
         }
-        l = fmaf(sum, scale_value(127 - lf), l);
         tmem_st_32x32b_x8(t_s + 8 * g, pk);
+        if (apart) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float e = exp2_fast(fmaf(__uint_as_float(z[i]), mul, up_n));
+            l += (seen >> i & 1) ? e : 0.0f;
+          }
+        } else {
+          l = fmaf(sum, meta.back[g], l);
+        }
       }
     }
     tmem_st_wait();
@@ -634,10 +670,12 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     const bool ok = wait_for(&sm->o_full[x], 0, sm, a.status, kErrEpilogueTmemFullWait);
     if (!__all_sync(0xffffffffu, ok)) return;
     tc_fence_after();
+    if (!apart) n = m - static_cast<float>(sm->meta[(w.n - 1) & (kMetaSlots - 1)].origin);
   }
   const bool none = l == 0.0f || !live;  // no key seen, or a row of padding: zeros
-  const float f = none ? 0.0f : 0x1p-7f / l, unit = scale_value(ref);  // in turn: 2^(ref - 134) need not be normal
-  static_assert(kBias == 7, "2^-7");
+  // O times 2^(m - n - 7) / l, in two factors: the power need not be normal
+  const int unit = __float2int_rz(m - n) - kBias, half_unit = unit >> 1;
+  const float f1 = none ? 0.0f : scale_value(127 + half_unit) / l, f2 = scale_value(127 + unit - half_unit);
   T* out = static_cast<T*>(a.out.p) + w.b * a.out.sb + s * a.out.ss + head * a.out.sh;
   float* part = a.splits > 1 ? a.part_o + (w.split * all_rows + out_row) * d : nullptr;
   for (int c = 0; c < d / 16; ++c) {
@@ -649,7 +687,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     if (!inside) continue;
     float v[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = none ? 0.0f : __uint_as_float(o[i]) * f * unit;
+    for (int i = 0; i < 16; ++i) v[i] = none ? 0.0f : __uint_as_float(o[i]) * f1 * f2;
     if (part != nullptr) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -665,7 +703,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     }
   }
   if (inside) {
-    const float lse2 = none ? -INFINITY : m + log2f(l);
+    const float lse2 = none ? -INFINITY : n + log2f(l);
     if (a.splits > 1)
       a.part_lse[w.split * all_rows + out_row] = lse2;
     else if (a.lse != nullptr)

@@ -11,6 +11,7 @@ from test_gpu_cache_attention import DEV, Case
 
 pytestmark = pytest.mark.gpu
 BOTH_FORMS = pytest.mark.parametrize("S", [1, 20, 65, 300])
+MANY_ROWS = pytest.mark.parametrize("S", [65, 300])
 
 
 class Apart(Case):
@@ -58,6 +59,17 @@ def _case(scales, S, **kw):
     return c
 
 
+def _towards(c, page, exponent):
+    """The page's keys along all queries (which become positive), or against them for a negative
+    exponent: scores of about +-2^|exponent|."""
+    c.q = c.q.abs() + 0.5
+    p = c.table[0][page]
+    k = c.codes[0, p]
+    c.codes[0, p] = torch.where((k & 127) == 127, k, (k & 127) | (0x80 if exponent < 0 else 0))
+    # |code| about 80 and d lanes of about 1.3: the sum is about 104 d
+    c.sf[0, p] = 127 + round(abs(exponent) - math.log2(104 * c.d * c.scale))
+
+
 @pytest.mark.parametrize("scales", [range(1, 11), [1] * 10, [6] * 10, [7] * 10, [3, 8] * 5, [4, 20, 1, 9]])
 @BOTH_FORMS
 def test_least_scales(S, scales):
@@ -67,3 +79,91 @@ def test_least_scales(S, scales):
     out, lse = c.run()
     c.check(out, lse)
     assert bool((out != 0).any())
+
+
+@pytest.mark.parametrize("above", [24, 34, 45, 60, 110])
+@MANY_ROWS
+def test_hidden_page_of_large_values(S, above):
+    """A page 2^above larger behind the causal edge of the earlier rows, and one before every row's
+    window, in the tiles of keys that the rows walk."""
+    scales = [120 + j % 3 for j in range(30)]
+    c = _case(scales, S, causal=True, length=470)
+    c.sf[1, c.table[0][29]] = 121 + above        # seen by the last rows alone (or by all there are)
+    c.upload()
+    c.run_and_check()
+    n = min(S, 120)                              # rows from position 470 - n on, which see 33 keys back
+    c = _case(scales, n, causal=True, window=33, length=470)
+    before = (470 - n - 33) // 16 - 1
+    for j in range(before - 3, before + 1):
+        c.sf[1, c.table[0][j]] = 121 + above
+    c.upload()
+    out, lse = c.run()
+    c.check(out, lse)
+    c.sf[1, :] = c.sf[1, :].clamp(max=122)       # the hidden pages like the rest: nothing changes
+    c.upload()
+    like, like_lse = c.run()
+    c.check(like, like_lse)
+    assert torch.allclose(out.float(), like.float(), rtol=2.0 ** -7, atol=2.0 ** -9 * float(like.abs().max()))
+
+
+@pytest.mark.parametrize("above,score", [(30, 6), (34, 7), (45, 7), (60, 8), (110, 8), (126, 9)])
+@pytest.mark.parametrize("page", [0, 3, 11])
+@MANY_ROWS
+def test_large_values_of_negligible_weight(S, above, score, page):
+    """The page of large values stands 2^score away from the queries: its weight times its values is
+    next to nothing, and the other pages' values come out."""
+    c = _case([119 + j % 2 for j in range(12)], S)
+    _towards(c, page, -score)
+    c.sf[1, c.table[0][page]] = 120 + above
+    c.upload()
+    ref, _, _, _ = c.reference()
+    with_small = float(ref.abs().max())
+    assert with_small < 2.0 ** 6                 # (the large page's share is below that)
+    c.run_and_check()
+
+
+@pytest.mark.parametrize("least", [1, 30, 70, 100])
+@pytest.mark.parametrize("score", [4, 5, 6, 7])
+@pytest.mark.parametrize("page", [0, 5, 9])
+@MANY_ROWS
+def test_least_values_of_nearly_all_weight(S, page, score, least):
+    """The other way round: a page of small values (of zeros, at the least scale) takes nearly all
+    of the weight, and what is left of the others is the answer."""
+    c = _case([150 + j % 3 for j in range(10)], S)
+    _towards(c, page, score)
+    p = c.table[0][page]
+    c.sf[1, p] = least
+    if least == 1:
+        k = c.codes[1, p]
+        c.codes[1, p] = torch.where((k & 127) == 127, k, torch.zeros_like(k))
+    c.upload()
+    c.run_and_check()
+
+
+@pytest.mark.parametrize("seed", range(6))
+@pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 50)])
+@MANY_ROWS
+def test_scales_of_the_whole_range(S, seed, causal, window):
+    g = torch.Generator().manual_seed(seed)
+    least, most = ((1, 230), (100, 160), (60, 200), (1, 60), (180, 230), (1, 230))[seed]
+    c = _case([120] * 30, S, causal=causal, window=window, length=470, seed=seed, gain=(1.0, 8.0)[seed & 1])
+    c.sf[1][c.sf[1] != 255] = torch.randint(least, most + 1, (int((c.sf[1] != 255).sum()),), generator=g, dtype=torch.uint8)
+    if seed == 5:                                # a page of zeros now and then
+        for j in range(0, 30, 4):
+            p = c.table[0][j]
+            k = c.codes[1, p]
+            c.codes[1, p] = torch.where((k & 127) == 127, k, torch.zeros_like(k))
+            c.sf[1, p] = 1
+    c.upload()
+    c.run_and_check()
+
+
+@MANY_ROWS
+@pytest.mark.parametrize("nan_pages", [8, 9, 29, 30])
+def test_nan_pages_before_any_other(S, nan_pages):
+    """Pages of NaN values first: the rows that see one are NaN, their log-sums are not."""
+    c = _case([150] * 30, S, causal=True, window=200, length=470)
+    for j in range(nan_pages):
+        c.sf[1, c.table[0][j]] = 255
+    c.upload()
+    Case.check(c, *c.run())
