@@ -85,9 +85,6 @@ struct TileMeta {
 };
 static_assert(sizeof(TileMeta) % 16 == 0, "pairs of kx in one access");
 
-// 2^x for a whole number x <= 0 (and minus infinity; 2^-127 is the least).
-__device__ __forceinline__ float pow2_down(float x) { return scale_value(max(127 + __float2int_rz(x), 0)); }
-
 struct alignas(16) Smem {
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];

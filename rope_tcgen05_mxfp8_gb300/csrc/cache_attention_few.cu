@@ -1,7 +1,7 @@
 // Attention of few queries over the 8-bit cache, and the joining of the keys' parts.
 //
-//   z_t = c q . k_t,  p_t = 2^(z_t - m),  o = sum_t p_t v_t / sum_t p_t
-// with c = scale log2(e) and m the running maximum: one pass over the keys.
+//   z_t = c q . k_t,  o = sum_t 2^z_t v_t / sum_t 2^z_t
+// with c = scale log2(e) and running references per row: one pass over the keys.
 //
 // With a few query rows per key head (a token of each sequence, times the query heads that
 // share a key head) the cache is read once and the read is what counts. A warp takes 32 keys
@@ -12,12 +12,12 @@
 // converted and stored to shared memory first, for a tile whose 128 rows would be mostly
 // padding (17 rows over 4096 keys, 40 heads: 27 us here, 56 there).
 //
-// What bounds it: 4 sequences of 32760 tokens, 40 heads of 128, one row each (1.34 GB) take 278 us,
-// 4.8 TB/s of 6.8: the warps' chains of product, maximum, exponential and product, about 400
+// What bounds it: 4 sequences of 32760 tokens, 40 heads of 128, one row each (1.34 GB) take 289 us,
+// 4.6 TB/s of 6.8: the warps' chains of product, maximum, exponential and product, about 400
 // instructions per 8 KB. More warps did not help (8 rows a tile in 168 or 128 registers: 276 and
-// 295 us), nor did integer operations in place of the conversion instructions (321). One token
-// over 512 keys takes 9.7 us, latencies alone. Keys are divided among blocks by waves (see the
-// host's attention_shape) and the parts joined by a second, small kernel.
+// 295 us against 278 at the time), nor did integer operations in place of the conversion
+// instructions (321). One token over 512 keys takes 9.7 us, latencies alone. Keys are divided among
+// blocks by waves (see the host's attention_shape) and the parts joined by a second, small kernel.
 //
 // Layouts. Lane 4g + t holds column g of the B operand and rows g, g + 8 of A and C.
 //   Scores: B's column g is key g; a lane reads 16-byte pieces t, t + 4 of its key's row, so
@@ -29,8 +29,15 @@
 //
 // Numerics. Queries are fp16 after a power of two per row (exact but for what is 2^-28 of the
 // row's largest), codes are exact, products and sums fp32. Each key's block scales multiply
-// its score and its weight in fp32. Weights are rounded to fp16 (2^-11) relative to the
-// largest value scale so far, 2^14 above, so that 28 binary orders below it keep their digits.
+// its score and its weight in fp32; weights are rounded to fp16 (by 2^-11 at most; the product takes
+// no more digits) with their value scale 2^x_t. While the value scales met lie within 2^12 of
+// one another, a weight is 2^(z_t - m + x_t - x), m the row's maximum of z_t and x the largest
+// x_t. Beyond, that would take the digits of weights that matter, for the sake of large values that
+// the row does not see or whose weight is negligible: a weight is then 2^(z_t + x_t - m), m the row's
+// own maximum of that over the keys it sees, and the sum of the 2^z_t has a reference and exponentials
+// of its own (13 % slower: 327 us for the 289 above, were it done all the time). Held 2^14 above,
+// the row's largest weight is 2 or more: down to 2^-15 of it weights keep fp16's digits, and what is
+// 2^-26 of it is lost. References are whole numbers, so that every change of one is exact.
 #include "kv_cache.cuh"
 #include "qkv_cte.h"
 #include "vec_io.cuh"
@@ -42,6 +49,7 @@ namespace {
 constexpr int kFewWarps = 4;
 constexpr int kFewKeys = 32;       // keys a warp takes at a time
 constexpr int kWeightBias = 14;    // weights are held 2^14 above their value
+constexpr int kFewNear = 12;       // binary orders of value scales that share a reference
 constexpr int kPitch = 132;        // floats per row of the warps' partial outputs (banks)
 
 __device__ __forceinline__ void mma_16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -88,8 +96,7 @@ struct KeyGroup {
 template <typename T>
 __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(const CacheAttentionArgs a) {
   __shared__ float s_o[kFewWarps][kCacheFewRows][kPitch];
-  __shared__ float s_m[kFewWarps][kCacheFewRows], s_l[kFewWarps][kCacheFewRows];
-  __shared__ int s_ev[kFewWarps];
+  __shared__ float s_m[kFewWarps][kCacheFewRows], s_mz[kFewWarps][kCacheFewRows], s_l[kFewWarps][kCacheFewRows];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   long long item = blockIdx.x;
@@ -175,8 +182,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
   for (int j = 0; j < 16; ++j)
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[j][k] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-  int ref = 1;  // exponent of the largest value scale so far
+  // references, minus infinity before a key is seen: m of the weights (without the largest value
+  // scale while scales lie near), mz of the sum where they lie apart; the sum
+  float m[2] = {-INFINITY, -INFINITY}, mz[2], l[2] = {0.0f, 0.0f};
+  int most = 1, least = kScaleNan;  // exponents of the largest and the least value scale so far
+  bool apart = false;
 
   KeyGroup now[2], next[2];
   uint4 kr[4][2], vr[2][4];
@@ -242,7 +252,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
     // scale, mask, maximum
     const int key0 = c * kFewKeys;
     const bool whole = key0 >= all_lo && key0 + kFewKeys <= all_hi && now[0].row >= 0 && now[1].row >= 0;
-    float top[2] = {m[0], m[1]};
+    float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const float sk = scale_value(now[n >> 1].ek);
@@ -254,44 +264,86 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
         top[k >> 1] = fmaxf(top[k >> 1], z[n][k]);
       }
     }
-    int newref = ref;
+    int newmost = most;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (now[i].row >= 0 && now[i].ev != kScaleNan) newref = max(newref, now[i].ev);
-    float use[2];
+      if (now[i].row >= 0 && now[i].ev != kScaleNan) {
+        newmost = max(newmost, now[i].ev);
+        least = min(least, now[i].ev);
+      }
+    if (!apart && newmost - least > kFewNear) {
+      apart = true;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      top[k] = quad_max(top[k]);
-      use[k] = top[k] == -INFINITY ? 0.0f : top[k];
-      const float keep = exp2_fast(m[k] - use[k]);
-      m[k] = top[k];
-      l[k] *= keep;
-      const float ko = keep * scale_value(max(127 - (newref - ref), 1));
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        o[j][2 * k] *= ko;
-        o[j][2 * k + 1] *= ko;
+      for (int k = 0; k < 2; ++k) {
+        mz[k] = m[k];
+        m[k] += static_cast<float>(most - 127);
       }
     }
-    ref = newref;
+    // the scores become weights
+    float keep[2];
+    if (!apart) {
+      float use[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        top[k] = fmaxf(m[k], ceilf(quad_max(top[k])));
+        use[k] = top[k] == -INFINITY ? 0.0f : top[k];
+        const float f = exp2_fast(m[k] - use[k]);
+        m[k] = top[k];
+        l[k] *= f;
+        keep[k] = f * scale_value(max(127 - (newmost - most), 1));
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float fv = scale_value(max(127 + kWeightBias + now[n >> 1].ev - newmost, 1));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float e = exp2_fast(z[n][k] - use[k >> 1]);
+          l[k >> 1] += e;
+          z[n][k] = !whole && z[n][k] == -INFINITY ? 0.0f : e * fv;  // (a scale that is NaN shows where it is seen)
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float x[2], t[2] = {-INFINITY, -INFINITY};  // of the groups: value scale, largest score
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          x[i] = now[i].ev == kScaleNan ? 0.0f : static_cast<float>(now[i].ev - 127);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t[i] = fmaxf(t[i], z[2 * i + (j >> 1)][2 * k + (j & 1)]);
+        }
+        const float to = fmaxf(m[k], ceilf(quad_max(fmaxf(t[0] + x[0], t[1] + x[1]))));
+        const float to_z = fmaxf(mz[k], ceilf(quad_max(fmaxf(t[0], t[1]))));
+        const float use = to == -INFINITY ? 0.0f : to, use_z = to_z == -INFINITY ? 0.0f : to_z;
+        keep[k] = exp2_fast(m[k] - use);
+        m[k] = to;
+        l[k] *= exp2_fast(mz[k] - use_z);
+        mz[k] = to_z;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float& w = z[j >> 1][2 * k + (j & 1)];
+          const bool nan = now[j >> 2].ev == kScaleNan && (whole || w != -INFINITY);
+          l[k] += exp2_fast(w - use_z);
+          w = nan ? scale_value(kScaleNan) : exp2_fast(w + (x[j >> 2] + kWeightBias - use));
+        }
+      }
+    }
+    most = newmost;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        o[j][2 * k] *= keep[k];
+        o[j][2 * k + 1] *= keep[k];
+      }
     // weights and values
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float fv = now[i].ev == kScaleNan ? scale_value(kScaleNan)
-                                              : scale_value(max(127 + kWeightBias + now[i].ev - ref, 1));
       uint32_t pa[4];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        float p[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float zz = z[2 * i + n][k];
-          const float e = exp2_fast(zz - use[k >> 1]);
-          l[k >> 1] += e;
-          p[k] = !whole && zz == -INFINITY ? 0.0f : e * fv;  // (a scale that is NaN shows where it is seen)
-        }
-        pa[2 * n] = pack_pair<__half>(make_float2(p[0], p[1]));
-        pa[2 * n + 1] = pack_pair<__half>(make_float2(p[2], p[3]));
+        pa[2 * n] = pack_pair<__half>(make_float2(z[2 * i + n][0], z[2 * i + n][1]));
+        pa[2 * n + 1] = pack_pair<__half>(make_float2(z[2 * i + n][2], z[2 * i + n][3]));
       }
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
@@ -316,54 +368,56 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     l[k] = quad_sum(l[k]);
+    if (!apart) {
+      mz[k] = m[k];
+      m[k] += static_cast<float>(most - 127);
+    }
     if (t == 0) {
       s_m[warp][g + 8 * k] = m[k];
+      s_mz[warp][g + 8 * k] = mz[k];
       s_l[warp][g + 8 * k] = l[k];
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j)
       *reinterpret_cast<float2*>(&s_o[warp][g + 8 * k][8 * j + 2 * t]) = make_float2(o[j][2 * k], o[j][2 * k + 1]);
   }
-  if (lane == 0) s_ev[warp] = ref;
   __syncthreads();
-  int top_ev = s_ev[0];
-#pragma unroll
-  for (int w = 1; w < kFewWarps; ++w) top_ev = max(top_ev, s_ev[w]);
   const int n_rows = rows - r0 < kCacheFewRows ? rows - r0 : kCacheFewRows;
   const long long all_rows = static_cast<long long>(a.batch) * a.seq * a.q_heads;
   for (int r = warp; r < n_rows; r += kFewWarps) {
     const int s = (r0 + r) / a.group;
     const int head = h * a.group + (r0 + r) % a.group;
-    float mm = s_m[0][r];
+    float top = s_m[0][r], top_z = s_mz[0][r];
 #pragma unroll
-    for (int w = 1; w < kFewWarps; ++w) mm = fmaxf(mm, s_m[w][r]);
-    const float base = mm == -INFINITY ? 0.0f : mm;
+    for (int w = 1; w < kFewWarps; ++w) {
+      top = fmaxf(top, s_m[w][r]);
+      top_z = fmaxf(top_z, s_mz[w][r]);
+    }
     float wt[kFewWarps], total = 0.0f;
 #pragma unroll
     for (int w = 0; w < kFewWarps; ++w) {
-      const float e = exp2_fast(s_m[w][r] - base);
-      total += s_l[w][r] * e;
-      wt[w] = e * scale_value(max(127 - (top_ev - s_ev[w]), 1));
+      total += s_l[w][r] * pow2_down(s_mz[w][r] - top_z);
+      wt[w] = pow2_down(s_m[w][r] - top);
     }
     const bool none = total == 0.0f || s >= vis.count;  // no key seen, or a row of padding: zeros
-    const float inv = none ? 0.0f : 1.0f / total;
+    // the warps' values times 2^(top - top_z - 14) / total, in two factors: the power need not be normal
+    const int unit = __float2int_rz(top - top_z) - kWeightBias, half_unit = unit >> 1;
+    const float f1 = none ? 0.0f : scale_value(127 + half_unit) / total, f2 = scale_value(127 + unit - half_unit);
     const long long out_row = (static_cast<long long>(b) * a.seq + s) * a.q_heads + head;
-    const float unit = scale_value(top_ev), unbias = 0x1p-14f;
-    static_assert(kWeightBias == 14, "unbias");
     T* out = static_cast<T*>(a.out.p) + b * a.out.sb + s * a.out.ss + head * a.out.sh;
     for (int col = lane; col < a.pool.d; col += 32) {
       const int at = 8 * (col & 15) + (col >> 4);
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < kFewWarps; ++w) v += s_o[w][r][at] * wt[w];
-      v = none ? 0.0f : v * inv * unbias * unit;
+      v = none ? 0.0f : v * f1 * f2;
       if (a.splits == 1)
         out[col] = from_f32<T>(v);
       else
         a.part_o[(split * all_rows + out_row) * a.pool.d + col] = v;
     }
     if (lane == 0) {
-      const float lse2 = none ? -INFINITY : mm + log2f(total);
+      const float lse2 = none ? -INFINITY : top_z + log2f(total);
       if (a.splits > 1)
         a.part_lse[split * all_rows + out_row] = lse2;
       else if (a.lse != nullptr)
