@@ -426,7 +426,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
   }
 }
 
-// out = sum_i w_i o_i / sum_i w_i, w_i = 2^(lse_i - max): a warp per row.
+// out = sum_i w_i o_i / sum_i w_i, w_i = 2^(lse_i - max): a warp per row. A weight is applied as its
+// root twice: by itself it may be less than fp32 holds where its values are so large that they count.
 template <typename T>
 __global__ void __launch_bounds__(128) cache_attention_join_kernel(const CacheAttentionArgs a) {
   const long long all_rows = static_cast<long long>(a.batch) * a.seq * a.q_heads;
@@ -445,11 +446,11 @@ __global__ void __launch_bounds__(128) cache_attention_join_kernel(const CacheAt
   for (int i = 0; i < a.splits; ++i) {
     const float lse = a.part_lse[i * all_rows + row];
     if (lse == -INFINITY) continue;  // that part saw nothing
-    const float w = exp2_fast(lse - base);
-    total += w;
+    const float root = exp2_fast(0.5f * (lse - base));
+    total += root * root;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (lane + 32 * j < a.pool.d) v[j] += w * a.part_o[(i * all_rows + row) * a.pool.d + lane + 32 * j];
+      if (lane + 32 * j < a.pool.d) v[j] += root * (root * a.part_o[(i * all_rows + row) * a.pool.d + lane + 32 * j]);
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   T* out = static_cast<T*>(a.out.p) + b * a.out.sb + s * a.out.ss + head * a.out.sh;

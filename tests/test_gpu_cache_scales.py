@@ -167,3 +167,19 @@ def test_nan_pages_before_any_other(S, nan_pages):
         c.sf[1, c.table[0][j]] = 255
     c.upload()
     Case.check(c, *c.run())
+
+
+@pytest.mark.parametrize("lead", [4, 6, 7])
+@pytest.mark.parametrize("S", [1, 70])
+def test_scales_far_apart_over_parts(S, lead):
+    """Keys divided among blocks: one part holds zeros that take nearly all the weight, another the
+    large values, joined from parts that are far apart in both."""
+    c = _case([127 + 100 if j > 30 else 127 for j in range(64)], S, nq=1, nkv=1, bt=128)
+    p = c.table[0][2]
+    _towards(c, 2, lead)
+    c.sf[1, p] = 1
+    c.codes[1, p] = 0
+    c.upload()
+    out, lse = c.run()
+    c.check(out, lse)
+    c.check(*c.run(max_length=1))
