@@ -591,10 +591,11 @@ int qkv_cte_cache_read(qkv_cte_cache_plan_t plan, const qkv_cte_cache_pages* pag
  * row s < counts[b] stands at position lengths[b] - counts[b] + s. It sees every t <
  * lengths[b]; with causal = 1 only t <= its position, and of these with window > 0 only the
  * last `window`. A row that sees nothing, and rows from counts[b] on, become zeros with an lse
- * of -infinity. Products and statistics are fp32, out is rounded once. Before they multiply the
- * codes, weights are rounded to fp16 with their value scale, as p_t 2^(sf_t - 127): each by
- * 2^-11 of itself, or by 2^-26 of the row's largest such product over the tokens that it sees where
- * that is more (pages so much smaller than another that the row attends to are lost beside it).
+ * of -infinity; a row that sees a token and has an element of q that is not finite becomes NaN.
+ * Products and statistics are fp32, out is rounded once. Before they multiply the codes,
+ * weights are rounded to fp16 with their value scale, as p_t 2^(sf_t - 127): each by 2^-11 of
+ * itself, or by 2^-26 of the row's largest such product over the tokens that it sees where that is
+ * more (pages so much smaller than another that the row attends to are lost beside it).
  *
  * q, out    : dtype (bf16 or fp16) [batch, seq, n_q_heads, d_head] with strides in elements,
  *             lanes contiguous; out's elements are distinct and overlap nothing else (column

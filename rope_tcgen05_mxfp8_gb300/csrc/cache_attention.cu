@@ -484,9 +484,10 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
 #pragma unroll
     for (int i = 0; i < 64; ++i) top = __vmaxu2(top, q[i] & 0x7FFF7FFFu);
     top = max(top & 0xFFFFu, top >> 16);
-    const int f = query_factor_field(__float_as_uint(unpack_pair<T>(top).x) & 0x7FFFFFFFu);
+    top = __float_as_uint(unpack_pair<T>(top).x) & 0x7FFFFFFFu;
+    const int f = query_factor_field(top);
     const float up = scale_value(f);
-    coef = a.scale_log2 * scale_value(254 - f);
+    coef = query_coef(top, f, a.scale_log2);
     const uint32_t base = s_q + x * kQBytes + row * 128;
 #pragma unroll
     for (int c = 0; c < 16; ++c) {

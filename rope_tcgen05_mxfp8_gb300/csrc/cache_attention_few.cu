@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int f = query_factor_field(top);
     const float up = scale_value(f);
-    coef[k] = a.scale_log2 * scale_value(254 - f);
+    coef[k] = query_coef(top, f, a.scale_log2);
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
       qf[n][k] = pack_pair<__half>(make_float2(x[4 * n] * up, x[4 * n + 1] * up));

@@ -113,5 +113,10 @@ __device__ __forceinline__ int query_factor_field(uint32_t abs_bits) {
   const int f = 268 - static_cast<int>(abs_bits >> 23);
   return f > 253 ? 253 : f;
 }
+// What brings a row's products back and scales them; NaN for a row with an element that is not
+// finite: infinite scores alone, all of one sign, would pass for a row that sees nothing.
+__device__ __forceinline__ float query_coef(uint32_t abs_bits, int field, float scale_log2) {
+  return scale_log2 * scale_value(abs_bits >= 0x7F800000u ? kScaleNan : 254 - field);
+}
 
 }  // namespace qkvcte

@@ -183,3 +183,23 @@ def test_scales_far_apart_over_parts(S, lead):
     out, lse = c.run()
     c.check(out, lse)
     c.check(*c.run(max_length=1))
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@BOTH_FORMS
+def test_queries_that_are_not_finite(S, dt, value):
+    """Where every score is an infinity of one sign, too; rows that see nothing stay empty."""
+    c = Case([40, 40], S=S, nq=2, nkv=2, d=32, bt=16, dt=dt, causal=True)
+    live = (c.codes[0] & 127) != 127
+    c.codes[0] = torch.where(live, (c.codes[0] & 0x7F).clamp(min=8), c.codes[0])   # positive, not zero
+    c.upload()
+    want, want_lse = c.run()
+    c.check(want, want_lse)
+    c.q[0, S // 2, 1, 7] = value
+    out, lse = c.run()
+    sees = S - 1 - S // 2 < 40
+    bad = torch.zeros(2, S, 2, dtype=torch.bool, device=DEV)
+    bad[0, S // 2, 1] = sees
+    assert torch.equal(torch.isnan(out), bad[..., None].expand_as(out)) and torch.equal(torch.isnan(lse), bad)
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], want_lse[~bad])
