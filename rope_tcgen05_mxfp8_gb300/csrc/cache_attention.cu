@@ -77,10 +77,9 @@ constexpr uint32_t kSCol = 0, kOCol = 256;
 // What the softmax warps need to know about a tile of keys, by groups of 16.
 struct TileMeta {
   float2 kx[8];     // key scale (NaN: 255), exponent of the value scale (of an absent or NaN group: origin)
-  float back[8];    // a weight without its value scale and 2^7, in the unit of the sum
   uint32_t there;   // groups with a page and tokens
   uint32_t vnan;    // groups whose value scale is NaN
-  int origin;       // exponent of the first tile's largest value scale (0 without one)
+  float origin;     // exponent of the first tile's largest value scale (0 without one)
   int apart;        // value scales more than 2^60 apart have been met
 };
 static_assert(sizeof(TileMeta) % 16 == 0, "pairs of kx in one access");
@@ -350,12 +349,11 @@ __device__ __forceinline__ void convert_role(const CacheAttentionArgs& a, const 
       if (lane < 8) {
         const int x = counts ? ev : origin;
         m.kx[lane] = make_float2(scale_value(ek), static_cast<float>(x - 127));
-        m.back[lane] = scale_value(min(max(127 - kBias + origin - x, 0), 254));
       }
       if (lane == 0) {
         m.there = there;
         m.vnan = vnan;
-        m.origin = origin - 127;
+        m.origin = static_cast<float>(origin - 127);
         m.apart = most - least > kNear;
       }
       __syncwarp();
@@ -525,7 +523,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     const int key0 = (w.key_tile0 + j) * kTileKeys;
     if (meta.apart != 0 && !apart) {
       apart = true;
-      n = m - static_cast<float>(meta.origin);
+      n = m - meta.origin;
     }
     // the weights' reference follows the tile's maximum of z + x
     auto follow = [&](float top) {
@@ -563,14 +561,13 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
         top = max3(top, fmaf(t[0], coef * kx.x, kx.y), fmaf(t[1], coef * kx.z, kx.w));
       }
       follow(top);
-      const float up = kBias - (m == -INFINITY ? 0.0f : m);
+      const float up = kBias - (m == -INFINITY ? 0.0f : m), unit = meta.origin - kBias;
 #pragma unroll 2
       for (int c = 0; c < 4; ++c) {
         float z[32];
         uint32_t pk[16];
         tmem_ld_32x32b_x32(t_s + 32 * c, reinterpret_cast<uint32_t*>(z));
         const float4 kx = *reinterpret_cast<const float4*>(&meta.kx[2 * c]);
-        const float2 back = *reinterpret_cast<const float2*>(&meta.back[2 * c]);
         tmem_ld_wait();
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
@@ -585,7 +582,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
             sum = fadd2(sum, e);
             pk[8 * g + i] = pack_pair<__half>(e);
           }
-          l = fmaf(sum.x + sum.y, g == 0 ? back.x : back.y, l);
+          l = fmaf(sum.x + sum.y, exp2_fast(unit - (g == 0 ? kx.y : kx.w)), l);
         }
         tmem_st_32x32b_x16(t_s + 16 * c, pk);
       }
@@ -614,7 +611,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
         top = fmaxf(top, t + meta.kx[g].y);
       }
       follow(top);
-      const float up = kBias - (m == -INFINITY ? 0.0f : m);
+      const float up = kBias - (m == -INFINITY ? 0.0f : m), unit = meta.origin - kBias;
       if (apart) {
         const float now = fmaxf(n, ceilf(top_z));
         l *= pow2_down(n - now);
@@ -651,7 +648,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
             l += (seen >> i & 1) ? e : 0.0f;
           }
         } else {
-          l = fmaf(sum, meta.back[g], l);
+          l = fmaf(sum, exp2_fast(unit - meta.kx[g].y), l);
         }
       }
     }
@@ -668,12 +665,13 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     const bool ok = wait_for(&sm->o_full[x], 0, sm, a.status, kErrEpilogueTmemFullWait);
     if (!__all_sync(0xffffffffu, ok)) return;
     tc_fence_after();
-    if (!apart) n = m - static_cast<float>(sm->meta[(w.n - 1) & (kMetaSlots - 1)].origin);
+    if (!apart) n = m - sm->meta[(w.n - 1) & (kMetaSlots - 1)].origin;
   }
   const bool none = l == 0.0f || !live;  // no key seen, or a row of padding: zeros
   // O times 2^(m - n - 7) / l, in two factors: the power need not be normal
   const int unit = __float2int_rz(m - n) - kBias, half_unit = unit >> 1;
   const float f1 = none ? 0.0f : scale_value(127 + half_unit) / l, f2 = scale_value(127 + unit - half_unit);
+  const float2 ff1 = make_float2(f1, f1), ff2 = make_float2(f2, f2);
   T* out = static_cast<T*>(a.out.p) + w.b * a.out.sb + s * a.out.ss + head * a.out.sh;
   float* part = a.splits > 1 ? a.part_o + (w.split * all_rows + out_row) * d : nullptr;
   for (int c = 0; c < d / 16; ++c) {
@@ -685,7 +683,11 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     if (!inside) continue;
     float v[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = none ? 0.0f : __uint_as_float(o[i]) * f1 * f2;
+    for (int i = 0; i < 16; i += 2) {
+      const float2 x = fmul2(fmul2(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), ff1), ff2);
+      v[i] = none ? 0.0f : x.x;
+      v[i + 1] = none ? 0.0f : x.y;
+    }
     if (part != nullptr) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
