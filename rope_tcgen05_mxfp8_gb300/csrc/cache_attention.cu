@@ -378,30 +378,23 @@ __device__ __forceinline__ void convert_role(const CacheAttentionArgs& a, const 
 // ---------------------------------------------------------------------------------------
 // Issue: one warp of the leading CTA
 // ---------------------------------------------------------------------------------------
+// kSteps: sixteens of lanes. What stands between two instructions is added to their 64 clocks, so a
+// product's are one straight line, whatever the head size: nothing is decided within it, and the
+// warp is together from its wait (a vote) to its commit, with the same elected lane throughout.
+template <int kSteps>
 __device__ __forceinline__ bool issue_all(const CacheAttentionArgs& a, const Work& w, Smem* sm, uint32_t s_q,
                                           uint32_t s_k, uint32_t s_v) {
   const int tiles = __shfl_sync(0xffffffffu, w.two ? 2 : 1, 0);
   const int n = __shfl_sync(0xffffffffu, w.n, 0);
-  const int steps = a.pool.d >> 4;
   const uint32_t id_s = idesc_f16(kTileKeys, false);
-  const uint32_t id_o = idesc_f16((a.pool.d + 31) & ~31, true);
+  const uint32_t id_o = idesc_f16((16 * kSteps + 31) & ~31, true);
   const uint64_t q_desc = smem_desc_sw128(s_q), k_desc = smem_desc_sw128(s_k), v_desc = smem_desc_sw128(s_v);
-  // Straight lines of eight: what stands between two instructions is added to their 64 clocks
-  // (and with a condition around each one the scores were wrong, nvcc 13.0).
   auto scores = [&](int x, int st) {
     const uint64_t qd = q_desc + (x * kQBytes >> 4), kd = k_desc + (st * kKBytes >> 4);
-    const uint32_t to = kSCol + x * 128;
-    auto step = [&](int ks) {
-      mma_f16_ss(to, qd + (((ks >> 2) * kQHalf + (ks & 3) * 32) >> 4), kd + (((ks >> 2) * kKHalf + (ks & 3) * 32) >> 4),
-                 id_s, ks > 0 ? 1u : 0u);
-    };
-    if (steps == 8) {
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) step(ks);
-    } else {
-#pragma unroll 1
-      for (int ks = 0; ks < steps; ++ks) step(ks);
-    }
+    for (int ks = 0; ks < kSteps; ++ks)
+      mma_f16_ss(kSCol + x * 128, qd + (((ks >> 2) * kQHalf + (ks & 3) * 32) >> 4),
+                 kd + (((ks >> 2) * kKHalf + (ks & 3) * 32) >> 4), id_s, ks > 0 ? 1u : 0u);
     commit_both(&sm->s_full[x]);
   };
   // (a wait that one lane gives up, all give up)
@@ -437,6 +430,20 @@ __device__ __forceinline__ bool issue_all(const CacheAttentionArgs& a, const Wor
     }
   }
   return true;
+}
+
+__device__ __forceinline__ bool issue(const CacheAttentionArgs& a, const Work& w, Smem* sm, uint32_t s_q, uint32_t s_k,
+                                      uint32_t s_v) {
+  switch (a.pool.d >> 4) {
+    case 1: return issue_all<1>(a, w, sm, s_q, s_k, s_v);
+    case 2: return issue_all<2>(a, w, sm, s_q, s_k, s_v);
+    case 3: return issue_all<3>(a, w, sm, s_q, s_k, s_v);
+    case 4: return issue_all<4>(a, w, sm, s_q, s_k, s_v);
+    case 5: return issue_all<5>(a, w, sm, s_q, s_k, s_v);
+    case 6: return issue_all<6>(a, w, sm, s_q, s_k, s_v);
+    case 7: return issue_all<7>(a, w, sm, s_q, s_k, s_v);
+    default: return issue_all<8>(a, w, sm, s_q, s_k, s_v);
+  }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -755,7 +762,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1) cac
     tmem_alloc_pair(smem_u32(&sm->tmem), 512);
     tmem_relinquish_pair();
     start_pair();
-    if (rank == 0 && w.n > 0 && !issue_all(a, w, sm, s_q, s_k, s_v)) {
+    if (rank == 0 && w.n > 0 && !issue(a, w, sm, s_q, s_k, s_v)) {
       // what was issued reads shared memory and writes tensor memory: let it end
       commit_both(&sm->drain);
       if (!mbar_wait_bounded(smem_u32(&sm->drain), 0, nullptr, kWaitNs)) atomicOr(a.status, kErrDrainWait);
