@@ -209,12 +209,25 @@ __device__ __forceinline__ bool try_wait_held(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
+// The same for a barrier on which the other CTA arrives: `acquire_pair` has to follow.
+__device__ __forceinline__ bool try_wait_held_pair(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(100000)
+      : "memory");
+  return done != 0;
+}
+template <bool kPair = false>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Smem* sm, uint32_t* status, uint32_t code) {
   const uint32_t at = smem_u32(bar);
-  if (try_wait_held(at, parity)) return true;
+  auto once = [&]() { return kPair ? try_wait_held_pair(at, parity) : try_wait_held(at, parity); };
+  if (once()) return true;
   const uint64_t t0 = globaltimer_ns();
   do {
-    if (try_wait_held(at, parity)) return true;
+    if (once()) return true;
   } while (*reinterpret_cast<volatile int*>(&sm->abort) == 0 && globaltimer_ns() - t0 < kWaitNs);
   atomicOr(status, code);
   *reinterpret_cast<volatile int*>(&sm->abort) = 1;
@@ -231,12 +244,20 @@ __device__ __forceinline__ void start_pair() {
   tc_fence_after();
 }
 
-// Arrive on the leading CTA's barrier at this offset. What it announces is read by the tensor
-// cores alone, where it lies, and has been fenced towards them; a release at cluster scope
-// would wait for the thread's loads in flight as well (5900 instead of 5050 clocks a tile of
-// keys).
+// Arrive on the leading CTA's barrier at this offset, and what the issuing warp does behind its
+// wait for it. Release and acquire hold for the pair (the tensor cores read operands where either
+// CTA's threads wrote them), but for shared memory alone: tensor memory has fences of its own, and
+// nothing else is handed over. A release of all memory waits for the thread's loads in flight as well
+// (972 x 4096, 38 heads 88 us, with these 71; at CTA scope, which does not reach the other CTA, 68).
+// (What comes the other way are the tensor cores' own arrivals, behind which no thread's writes stand.)
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0)) : "memory");
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0))
+      : "memory");
+}
+__device__ __forceinline__ void acquire_pair() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------------------
@@ -399,7 +420,8 @@ __device__ __forceinline__ bool issue_all(const CacheAttentionArgs& a, const Wor
   };
   // (a wait that one lane gives up, all give up)
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
-    const bool ok = __all_sync(0xffffffffu, wait_for(bar, parity, sm, a.status, code));
+    const bool ok = __all_sync(0xffffffffu, wait_for<true>(bar, parity, sm, a.status, code));
+    acquire_pair();
     tc_fence_after();
     return ok;
   };
