@@ -24,14 +24,23 @@ constexpr int kMaxSplits = 64;
 // Query rows per key head up to which the form for few queries is taken, in tiles of 16 rows that
 // read the keys again (from L2); beyond, pairs of blocks on tcgen05, for which fewer than 256
 // rows leave part of every product empty. us a call in a captured graph, few rows' form / tcgen05,
-// 40 key heads of 128:
-//   rows  over 512 keys  over 4096     4 x 32760
-//   17    11.6 / 13.8    26.6 / 55.5
-//   32    11.5 / 13.9    27.8 / 56.1   575 / 1275
-//   64    13.7 / 14.2    50.3 / 58.3   1067 / 1296
-//   96                   57.9 / 60.8
-//   128   22.9 / 15.9    94.9 / 63.9
+// heads of 128, 40 or 8 key heads:
+//         40: over 512   over 4096     4 x 32760     8: over 512   over 4096    32760
+//   17    12.1 / 13.9    27.4 / 53.0    581 / 1331   12.1 / 14.0   17.4 / 19.2  39.5 / 62.9
+//   32    12.2 / 13.9    29.3 / 53.5    597 / 1331   12.2 / 13.8   16.9 / 18.8  39.0 / 62.6
+//   64    14.6 / 14.0    52.5 / 55.4   1110 / 1351   12.2 / 13.8   19.7 / 19.1  60.5 / 63.1
+//   96    14.9 / 14.2    59.9 / 57.6   1625 / 1367   12.4 / 13.8   22.1 / 20.2  83.0 / 64.3
+//   128   23.7 / 14.4    96.5 / 60.6   2081 / 1383   12.2 / 14.2   24.9 / 20.4   114 / 64.4
 constexpr int64_t kFewMaxRows = 64;
+// Blocks that run at a time: of the form for few rows two on each of 152 SMs, of the other a pair on
+// two SMs. Not the current device's count: the workspace is a function of the sizes alone, asked
+// for where there may be no device (with another count the keys are divided less evenly, no more).
+constexpr int64_t kFewSlots = 2 * 152, kPairSlots = 152 / 2;
+// What a block costs beside its keys, in units of the 17 us that either form's block takes for 1024
+// keys of 128 lanes when all run: a pair's start and end 9 us (32760 rows over 128 keys take 11 a
+// pair, 2 of them for the keys), a block of the few rows' form 4, the launch that joins 4; partial
+// results are written and read at 7.6 TB/s, 1.3e8 bytes in a unit.
+constexpr double kPairFixed = 0.5, kFewFixed = 0.25, kJoinFixed = 0.25, kJoinBytes = 1.3e8;
 constexpr int64_t kMaxPositions = INT32_MAX - 1024;  // positions and rows rounded up to tiles stay inside 32 bits
 
 size_t elem_size(int dtype) { return dtype == QKV_CTE_DTYPE_FP32 ? 4 : 2; }
@@ -189,17 +198,18 @@ AttentionShape attention_shape(const qkv_cte_cache_desc& d, int64_t batch, int64
   const int per = s.few ? kCacheFewRows : kCacheTileRows;
   s.row_tiles = static_cast<int>((rows + per - 1) / per);
   const int64_t items = batch * d.n_kv_heads * s.row_tiles;
-  // Parts of the keys: the fewest waves of blocks, weighed by what a block costs beside its
-  // keys (in the time of 1024 keys) and by the joining.
-  const int64_t slots = s.few ? 304 : 76;  // two blocks on each of 152 SMs; pairs of blocks
-  const double fixed = s.few ? 0.25 : 0.5, join = 0.25;
-  const double traffic = static_cast<double>(batch * seq * n_q_heads) * d.d_head * 8 / 1.3e8;  // of one part: written, read
+  // Parts of the keys: the fewest waves of blocks, weighed by what a block costs beside its keys and by
+  // the joining. (A window is left out, for the workspace does not depend on it either: rows with one
+  // may get more parts than they fill.)
+  const int64_t slots = s.few ? kFewSlots : kPairSlots;
+  const double fixed = s.few ? kFewFixed : kPairFixed;
+  const double traffic = static_cast<double>(batch * seq * n_q_heads) * d.d_head * 8 / kJoinBytes;  // of one part: written, read
   const int64_t most = std::min<int64_t>((max_length + 511) / 512, kMaxSplits);
   double best = 0;
   s.splits = 1;
   for (int64_t k = 1; k <= most; ++k) {
     const double waves = static_cast<double>((items * k + slots - 1) / slots);
-    const double cost = waves * (static_cast<double>(max_length) / (1024.0 * k) + fixed) + (k > 1 ? join + traffic * k : 0.0);
+    const double cost = waves * (static_cast<double>(max_length) / (1024.0 * k) + fixed) + (k > 1 ? kJoinFixed + traffic * k : 0.0);
     if (k == 1 || cost < best) {
       best = cost;
       s.splits = static_cast<int>(k);
