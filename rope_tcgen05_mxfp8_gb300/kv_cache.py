@@ -272,7 +272,8 @@ class QkvCteCache:
         that see nothing, and those from counts[b] on, are zeros. `scale`: 1 / sqrt(d_head) by
         default. The fp32 log-sum lse [..., heads] is written when given or asked for with
         `stats`, else None. `max_length`: a length that no sequence is expected to pass (by
-        default what the table holds); only speed depends on it."""
+        default what the table holds); only speed depends on it. Many rows of q and out want to
+        start on 32-byte boundaries (see the header)."""
         dev, d = self.device, self.d_head
         aq, batch, seq = _heads("q", q, _QUERY, dev, None, d)
         heads, dt, shape = q.shape[-2], q.dtype, q.shape
