@@ -140,6 +140,21 @@ def test_least_values_of_nearly_all_weight(S, page, score, least):
     c.run_and_check()
 
 
+@pytest.mark.parametrize("page", [0, 3, 11])
+@BOTH_FORMS
+def test_zeros_of_all_the_weight(S, page):
+    """A page of zeros 2^300 above the rest in weight: nothing of the rest is left."""
+    c = _case([127] * 12, S)
+    _towards(c, page, 8)
+    k = c.codes[1, c.table[0][page]]
+    c.codes[1, c.table[0][page]] = torch.where((k & 127) == 127, k, torch.zeros_like(k))
+    c.upload()
+    for longest in (None, 1, 10 ** 6):
+        out, lse = c.run(max_length=longest)
+        c.check(out, lse)
+        assert bool((out == 0).all())
+
+
 @pytest.mark.parametrize("seed", range(6))
 @pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 50)])
 @BOTH_FORMS
