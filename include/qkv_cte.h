@@ -517,7 +517,9 @@ int qkv_cte_linear_run(qkv_cte_linear_plan_t plan, const void* A, const float* a
  * Pool. k_codes and v_codes hold [pages, n_kv_heads, block_tokens, d_head] codes (16-byte
  * aligned), k_sf and v_sf [pages, n_kv_heads] UE8M0 scales: a value is code * 2^(sf - 127).
  * A scale of 255 is NaN, and so is every value of that page and head. The pool needs no
- * preparation: a slot is read only where a sequence has a token.
+ * preparation: a slot is read only where a sequence has a token. e4m3's own NaN, codes 0x7F and
+ * 0xFF, is never written; a pool filled by other means must not hold it where a sequence has a token
+ * (in values it could reach rows of queries that do not see that token).
  *
  * Table. Block j of sequence b (its tokens j * block_tokens ...) is page
  * table[b * table_stride + j], j < max_blocks; without a table, page b * max_blocks + j. A
