@@ -33,13 +33,15 @@
 // at most, an eighth of what a result's rounding to bf16 may cost and as much as one to fp16, and
 // it averages out over the keys), so what is rounded is 2^(z_t + x_t - m), with m the row's own maximum of z_t + x_t over the keys it sees: neither a
 // key that it does not see nor one whose weight makes its large values negligible takes digits from
-// the others. References are whole numbers, so that every change of one is exact. With 2^7 above,
-// the row's largest weight is 2^6 or more: down to 2^-20 of it weights keep fp16's digits, and
-// what is 2^-31 of it is lost.
+// the others. With 2^7 above, the row's largest weight is 2^6 or more: down to 2^-20 of it weights
+// keep fp16's digits, and what is 2^-31 of it is lost.
 // The sum of the 2^z_t has a reference n of its own. As long as the value scales met lie within
 // 2^60 of one another its terms are the weights without their 2^x_t, one exponential for both,
 // and n is m less the first tile's largest x. Beyond (a page of zeros has the least scale there
-// is) the terms are taken by themselves, as 2^(z_t - n), in the path that masked tiles take.
+// is) the terms are taken by themselves, as 2^(z_t - n), in the path that masked tiles take, and both
+// references are whole numbers: a difference of two that are large is exact then. (Otherwise m is
+// the maximum itself: a key that is all a row sees has a weight of just 2^7, which fp16 holds, and
+// its value comes out as it is.)
 //
 // m follows its maximum lazily: O in tensor memory is rescaled only when that has grown by more
 // than 2^8, which after the first tiles is hardly ever; weights then reach 2^15 instead of 2^7,
@@ -553,13 +555,15 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     const int key0 = (w.key_tile0 + j) * kTileKeys;
     if (meta.apart != 0 && !apart) {
       apart = true;
-      n = m - meta.origin;
+      const float up = ceilf(m);
+      n = up - meta.origin;
+      if (m != -INFINITY) l *= exp2_fast(m - up);
     }
-    // the weights' reference follows the tile's maximum of z + x
+    // the weights' reference follows the tile's maximum of z + x, and the sum with it
     auto follow = [&](float top) {
-      if (!__any_sync(0xffffffffu, top > m + kGrowth)) return;
-      const float now = fmaxf(m, ceilf(top));
-      const float f = pow2_down(m - now);
+      if (!__any_sync(0xffffffffu, top > m + kGrowth || (apart && m != ceilf(m)))) return;
+      const float now = apart ? fmaxf(ceilf(m), ceilf(top)) : fmaxf(m, top);
+      const float f = exp2_fast(m - (now == -INFINITY ? 0.0f : now));
       m = now;
       if (!apart) l *= f;
       if (j == 0) return;
@@ -644,7 +648,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
       const float up = kBias - (m == -INFINITY ? 0.0f : m), unit = meta.origin - kBias;
       if (apart) {
         const float now = fmaxf(n, ceilf(top_z));
-        l *= pow2_down(n - now);
+        l *= exp2_fast(n - (now == -INFINITY ? 0.0f : now));
         n = now;
       }
       const float up_n = n == -INFINITY ? 0.0f : -n;
@@ -691,15 +695,18 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
   // the row's result
   const long long all_rows = static_cast<long long>(a.batch) * a.seq * a.q_heads;
   const long long out_row = (static_cast<long long>(w.b) * a.seq + s) * a.q_heads + head;
+  int unit = 0;  // O's less the sum's, binary orders
   if (w.n > 0) {
     const bool ok = wait_for(&sm->o_full[x], 0, sm, a.status, kErrEpilogueTmemFullWait);
     if (!__all_sync(0xffffffffu, ok)) return;
     tc_fence_after();
-    if (!apart) n = m - sm->meta[(w.n - 1) & (kMetaSlots - 1)].origin;
+    const float origin = sm->meta[(w.n - 1) & (kMetaSlots - 1)].origin;
+    unit = __float2int_rz(apart ? m - n : origin) - kBias;
+    if (!apart) n = m - origin;
   }
   const bool none = l == 0.0f || !live;  // no key seen, or a row of padding: zeros
-  // O times 2^(m - n - 7) / l, in two factors: the power need not be normal
-  const int unit = __float2int_rz(m - n) - kBias, half_unit = unit >> 1;
+  // O times 2^unit / l, in two factors: the power need not be normal
+  const int half_unit = unit >> 1;
   const float f1 = none ? 0.0f : scale_value(127 + half_unit) / l, f2 = scale_value(127 + unit - half_unit);
   const float2 ff1 = make_float2(f1, f1), ff2 = make_float2(f2, f2);
   T* out = static_cast<T*>(a.out.p) + w.b * a.out.sb + s * a.out.ss + head * a.out.sh;

@@ -35,9 +35,11 @@
 // x_t. Beyond, that would take the digits of weights that matter, for the sake of large values that
 // the row does not see or whose weight is negligible: a weight is then 2^(z_t + x_t - m), m the row's
 // own maximum of that over the keys it sees, and the sum of the 2^z_t has a reference and exponentials
-// of its own (13 % slower: 327 us for the 289 above, were it done all the time). Held 2^14 above,
-// the row's largest weight is 2 or more: down to 2^-15 of it weights keep fp16's digits, and what is
-// 2^-26 of it is lost. References are whole numbers, so that every change of one is exact.
+// of its own (13 % slower: 327 us for the 289 above, were it done all the time); both references are
+// whole numbers then, so that their difference is exact however large they are. Held 2^14 above, the
+// row's largest weight is 2^2 or more: down to 2^-16 of it weights keep fp16's digits, and what is
+// 2^-27 of it is lost. A key that is all a row sees has a weight of just 2^(14 + x_t - x): its value
+// comes out as it is.
 #include "kv_cache.cuh"
 #include "qkv_cte.h"
 #include "vec_io.cuh"
@@ -96,7 +98,7 @@ struct KeyGroup {
 template <typename T>
 __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(const CacheAttentionArgs a) {
   __shared__ float s_o[kFewWarps][kCacheFewRows][kPitch];
-  __shared__ float s_m[kFewWarps][kCacheFewRows], s_mz[kFewWarps][kCacheFewRows], s_l[kFewWarps][kCacheFewRows];
+  __shared__ float s_m[kFewWarps][kCacheFewRows], s_x[kFewWarps][kCacheFewRows], s_l[kFewWarps][kCacheFewRows];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   long long item = blockIdx.x;
@@ -182,8 +184,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
   for (int j = 0; j < 16; ++j)
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[j][k] = 0.0f;
-  // references, minus infinity before a key is seen: m of the weights (without the largest value
-  // scale while scales lie near), mz of the sum where they lie apart; the sum
+  // references, minus infinity before a key is seen: m of the weights (while scales lie near without
+  // the largest of them, and the sum's too), mz of the sum where they lie apart; the sum
   float m[2] = {-INFINITY, -INFINITY}, mz[2], l[2] = {0.0f, 0.0f};
   int most = 1, least = kScaleNan;  // exponents of the largest and the least value scale so far
   bool apart = false;
@@ -275,8 +277,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
       apart = true;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        mz[k] = m[k];
-        m[k] += static_cast<float>(most - 127);
+        mz[k] = ceilf(m[k]);
+        const float f = m[k] == -INFINITY ? 1.0f : exp2_fast(m[k] - mz[k]);
+        l[k] *= f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          o[j][2 * k] *= f;
+          o[j][2 * k + 1] *= f;
+        }
+        m[k] = mz[k] + static_cast<float>(most - 127);
       }
     }
     // the scores become weights
@@ -285,7 +294,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
       float use[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        top[k] = fmaxf(m[k], ceilf(quad_max(top[k])));
+        top[k] = fmaxf(m[k], quad_max(top[k]));
         use[k] = top[k] == -INFINITY ? 0.0f : top[k];
         const float f = exp2_fast(m[k] - use[k]);
         m[k] = top[k];
@@ -368,13 +377,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     l[k] = quad_sum(l[k]);
-    if (!apart) {
-      mz[k] = m[k];
-      m[k] += static_cast<float>(most - 127);
-    }
     if (t == 0) {
-      s_m[warp][g + 8 * k] = m[k];
-      s_mz[warp][g + 8 * k] = mz[k];
+      s_m[warp][g + 8 * k] = apart ? mz[k] : m[k];
+      s_x[warp][g + 8 * k] = !apart ? static_cast<float>(most - 127) : mz[k] == -INFINITY ? 0.0f : m[k] - mz[k];
       s_l[warp][g + 8 * k] = l[k];
     }
 #pragma unroll
@@ -387,21 +392,23 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
   for (int r = warp; r < n_rows; r += kFewWarps) {
     const int s = (r0 + r) / a.group;
     const int head = h * a.group + (r0 + r) % a.group;
-    float top = s_m[0][r], top_z = s_mz[0][r];
+    // sums are in units of 2^s_m, values of 2^(s_m + s_x), s_x whole
+    float top = s_m[0][r];
 #pragma unroll
-    for (int w = 1; w < kFewWarps; ++w) {
-      top = fmaxf(top, s_m[w][r]);
-      top_z = fmaxf(top_z, s_mz[w][r]);
-    }
-    float wt[kFewWarps], total = 0.0f;
+    for (int w = 1; w < kFewWarps; ++w) top = fmaxf(top, s_m[w][r]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float wt[kFewWarps], total = 0.0f, top_x = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kFewWarps; ++w) {
-      total += s_l[w][r] * pow2_down(s_mz[w][r] - top_z);
-      wt[w] = pow2_down(s_m[w][r] - top);
+      total += s_l[w][r] * exp2_fast(s_m[w][r] - base);
+      top_x = fmaxf(top_x, s_m[w][r] - base + s_x[w][r]);
     }
+    top_x = top_x == -INFINITY ? 0.0f : ceilf(top_x);
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) wt[w] = exp2_fast(s_m[w][r] - base + (s_x[w][r] - top_x));
     const bool none = total == 0.0f || s >= vis.count;  // no key seen, or a row of padding: zeros
-    // the warps' values times 2^(top - top_z - 14) / total, in two factors: the power need not be normal
-    const int unit = __float2int_rz(top - top_z) - kWeightBias, half_unit = unit >> 1;
+    // the warps' values times 2^(top_x - 14) / total, in two factors: the power need not be normal
+    const int unit = __float2int_rz(top_x) - kWeightBias, half_unit = unit >> 1;
     const float f1 = none ? 0.0f : scale_value(127 + half_unit) / total, f2 = scale_value(127 + unit - half_unit);
     const long long out_row = (static_cast<long long>(b) * a.seq + s) * a.q_heads + head;
     T* out = static_cast<T*>(a.out.p) + b * a.out.sb + s * a.out.ss + head * a.out.sh;
@@ -417,7 +424,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
         a.part_o[(split * all_rows + out_row) * a.pool.d + col] = v;
     }
     if (lane == 0) {
-      const float lse2 = none ? -INFINITY : top_z + log2f(total);
+      const float lse2 = none ? -INFINITY : base + log2f(total);
       if (a.splits > 1)
         a.part_lse[split * all_rows + out_row] = lse2;
       else if (a.lse != nullptr)

@@ -31,9 +31,6 @@ __device__ __forceinline__ float scale_value(int e) {
   return __uint_as_float(bits);
 }
 
-// 2^x for a whole number x <= 0; zero below 2^-126 and for minus infinity.
-__device__ __forceinline__ float pow2_down(float x) { return x < -126.0f ? 0.0f : scale_value(127 + __float2int_rz(x)); }
-
 // Biased exponent E of the smallest power of two 2^(E - 127) that brings |x| to at most
 // 448 = 1.75 * 2^8, from x's bits without the sign: 1 (the least) for zeros, 255 for
 // infinities and NaN.

@@ -155,6 +155,19 @@ def test_zeros_of_all_the_weight(S, page):
         assert bool((out == 0).all())
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("spread", [0, 4])
+@BOTH_FORMS
+def test_a_single_key_comes_out_as_it_is(S, spread, dt):
+    """The value of the only key that a row sees is a code times a power of two: no rounding at all."""
+    c = Case([700], S=S, nq=4, nkv=2, d=64, bt=16, dt=dt, causal=True, window=1, spread=spread, gain=3.0)
+    for longest in (None, 1, 10 ** 6):
+        out, lse = c.run(max_length=longest)
+        ref, _, _, _ = c.reference()
+        assert torch.equal(out.double(), ref)
+    c.check(out, lse)
+
+
 @pytest.mark.parametrize("seed", range(6))
 @pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 50)])
 @BOTH_FORMS
