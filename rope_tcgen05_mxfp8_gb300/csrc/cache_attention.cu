@@ -46,6 +46,8 @@
 // m follows its maximum lazily: O in tensor memory is rescaled only when that has grown by more
 // than 2^8, which after the first tiles is hardly ever; weights then reach 2^15 instead of 2^7,
 // which costs nothing.
+#include <type_traits>
+
 #include "fp32x2.cuh"
 #include "internal.h"
 #include "kv_cache.cuh"
@@ -544,28 +546,25 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
   // references of the weights and (where scales lie apart) of the sum, minus infinity before a key
   // is seen; the sum
   float m = -INFINITY, n = -INFINITY, l = 0.0f;
-  bool apart = false;
-  for (int j = 0; j < w.n; ++j) {
-    const int slot = j & (kMetaSlots - 1);
-    bool ok = wait_for(&sm->meta_full[slot], (j / kMetaSlots) & 1, sm, a.status, kErrEpilogueTmemFullWait);
+  int j = 0;
+  auto scored = [&]() {  // the tile's scores and what goes with its keys are there
+    bool ok = wait_for(&sm->meta_full[j & (kMetaSlots - 1)], (j / kMetaSlots) & 1, sm, a.status, kErrEpilogueTmemFullWait);
     ok = ok && wait_for(&sm->s_full[x], j & 1, sm, a.status, kErrEpilogueTmemFullWait);
-    if (!__all_sync(0xffffffffu, ok)) return;
-    tc_fence_after();
-    const TileMeta& meta = sm->meta[slot];
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) tc_fence_after();
+    return ok;
+  };
+  auto weigh = [&](auto are_apart) {  // scores to weights, with the value scales near one another or apart
+    constexpr bool kApart = decltype(are_apart)::value;
+    const TileMeta& meta = sm->meta[j & (kMetaSlots - 1)];
     const int key0 = (w.key_tile0 + j) * kTileKeys;
-    if (meta.apart != 0 && !apart) {
-      apart = true;
-      const float up = ceilf(m);
-      n = up - meta.origin;
-      if (m != -INFINITY) l *= exp2_fast(m - up);
-    }
     // the weights' reference follows the tile's maximum of z + x, and the sum with it
     auto follow = [&](float top) {
-      if (!__any_sync(0xffffffffu, top > m + kGrowth || (apart && m != ceilf(m)))) return;
-      const float now = apart ? fmaxf(ceilf(m), ceilf(top)) : fmaxf(m, top);
+      if (!__any_sync(0xffffffffu, top > m + kGrowth || (kApart && m != ceilf(m)))) return;
+      const float now = kApart ? fmaxf(ceilf(m), ceilf(top)) : fmaxf(m, top);
       const float f = exp2_fast(m - (now == -INFINITY ? 0.0f : now));
       m = now;
-      if (!apart) l *= f;
+      if (!kApart) l *= f;
       if (j == 0) return;
       for (int c = 0; c < (d > 64 ? 8 : 4); ++c) {
         uint32_t o[16];
@@ -576,7 +575,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
         tmem_st_32x32b_x16(t_o + 16 * c, o);
       }
     };
-    if (dead || (key0 >= all_lo && key0 + kTileKeys <= all_hi && meta.there == 0xFFu && meta.vnan == 0 && !apart)) {
+    if (!kApart && (dead || (key0 >= all_lo && key0 + kTileKeys <= all_hi && meta.there == 0xFFu && meta.vnan == 0))) {
       float top = -INFINITY;
 #pragma unroll 2
       for (int c = 0; c < 4; ++c) {
@@ -646,7 +645,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
       }
       follow(top);
       const float up = kBias - (m == -INFINITY ? 0.0f : m), unit = meta.origin - kBias;
-      if (apart) {
+      if constexpr (kApart) {
         const float now = fmaxf(n, ceilf(top_z));
         l *= exp2_fast(n - (now == -INFINITY ? 0.0f : now));
         n = now;
@@ -675,7 +674,7 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
           pk[i] = pack_pair<__half>(e);
         }
         tmem_st_32x32b_x8(t_s + 8 * g, pk);
-        if (apart) {
+        if constexpr (kApart) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float e = exp2_fast(fmaf(__uint_as_float(z[i]), mul, up_n));
@@ -690,6 +689,21 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     tc_fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) arrive_leader(&sm->p_full[x]);
+  };
+  for (; j < w.n; ++j) {
+    if (!scored()) return;
+    if (sm->meta[j & (kMetaSlots - 1)].apart != 0) break;
+    weigh(std::false_type{});
+  }
+  const bool apart = j < w.n;
+  if (apart) {
+    const float up = ceilf(m);
+    n = up - sm->meta[j & (kMetaSlots - 1)].origin;
+    if (m != -INFINITY) l *= exp2_fast(m - up);
+    for (; j < w.n; ++j) {
+      if (!scored()) return;
+      weigh(std::true_type{});
+    }
   }
 
   // the row's result

@@ -40,6 +40,8 @@
 // row's largest weight is 2^2 or more: down to 2^-16 of it weights keep fp16's digits, and what is
 // 2^-27 of it is lost. A key that is all a row sees has a weight of just 2^(14 + x_t - x): its value
 // comes out as it is.
+#include <type_traits>
+
 #include "kv_cache.cuh"
 #include "qkv_cte.h"
 #include "vec_io.cuh"
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
   // the largest of them, and the sum's too), mz of the sum where they lie apart; the sum
   float m[2] = {-INFINITY, -INFINITY}, mz[2], l[2] = {0.0f, 0.0f};
   int most = 1, least = kScaleNan;  // exponents of the largest and the least value scale so far
-  bool apart = false;
+  float grown = 1.0f;               // 2^-(what the largest one has grown by)
 
   KeyGroup now[2], next[2];
   uint4 kr[4][2], vr[2][4];
@@ -231,7 +233,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
   entries(c + kFewWarps);
   load_k(now);
   load_v(now, c);
-  for (; c < c1; c += kFewWarps) {
+  // One step: the warp's next 32 keys, with the value scales near one another or apart.
+  auto step = [&](auto are_apart) {
+    constexpr bool kApart = decltype(are_apart)::value;
     find(next, c + kFewWarps);
     entries(c + 2 * kFewWarps);
     // scores
@@ -266,32 +270,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
         top[k >> 1] = fmaxf(top[k >> 1], z[n][k]);
       }
     }
-    int newmost = most;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (now[i].row >= 0 && now[i].ev != kScaleNan) {
-        newmost = max(newmost, now[i].ev);
-        least = min(least, now[i].ev);
-      }
-    if (!apart && newmost - least > kFewNear) {
-      apart = true;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        mz[k] = ceilf(m[k]);
-        const float f = m[k] == -INFINITY ? 1.0f : exp2_fast(m[k] - mz[k]);
-        l[k] *= f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          o[j][2 * k] *= f;
-          o[j][2 * k + 1] *= f;
-        }
-        m[k] = mz[k] + static_cast<float>(most - 127);
-      }
-    }
-    // the scores become weights
-    float keep[2];
-    if (!apart) {
-      float use[2];
+    float keep[2], use[2];
+    if constexpr (!kApart) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         top[k] = fmaxf(m[k], quad_max(top[k]));
@@ -299,17 +279,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
         const float f = exp2_fast(m[k] - use[k]);
         m[k] = top[k];
         l[k] *= f;
-        keep[k] = f * scale_value(max(127 - (newmost - most), 1));
-      }
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float fv = scale_value(max(127 + kWeightBias + now[n >> 1].ev - newmost, 1));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float e = exp2_fast(z[n][k] - use[k >> 1]);
-          l[k >> 1] += e;
-          z[n][k] = !whole && z[n][k] == -INFINITY ? 0.0f : e * fv;  // (a scale that is NaN shows where it is seen)
-        }
+        keep[k] = f * grown;
       }
     } else {
 #pragma unroll
@@ -337,7 +307,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
         }
       }
     }
-    most = newmost;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -348,9 +317,19 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
     // weights and values
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      const float fv = scale_value(max(127 + kWeightBias + now[i].ev - most, 1));
       uint32_t pa[4];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
+        if constexpr (!kApart) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float& w = z[2 * i + n][k];
+            const float e = exp2_fast(w - use[k >> 1]);
+            l[k >> 1] += e;
+            w = !whole && w == -INFINITY ? 0.0f : e * fv;  // (a scale that is NaN shows where it is seen)
+          }
+        }
         pa[2 * n] = pack_pair<__half>(make_float2(z[2 * i + n][0], z[2 * i + n][1]));
         pa[2 * n + 1] = pack_pair<__half>(make_float2(z[2 * i + n][2], z[2 * i + n][3]));
       }
@@ -371,6 +350,36 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) cache_attention_few_kernel(
     load_v(next, c + kFewWarps);
     now[0] = next[0];
     now[1] = next[1];
+  };
+  bool apart = false;
+  for (; c < c1; c += kFewWarps) {
+    int newmost = most;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (now[i].row >= 0 && now[i].ev != kScaleNan) {
+        newmost = max(newmost, now[i].ev);
+        least = min(least, now[i].ev);
+      }
+    apart = newmost - least > kFewNear;
+    if (apart) break;
+    grown = scale_value(max(127 - (newmost - most), 1));
+    most = newmost;
+    step(std::false_type{});
+  }
+  if (apart) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      mz[k] = ceilf(m[k]);
+      const float f = m[k] == -INFINITY ? 1.0f : exp2_fast(m[k] - mz[k]);
+      l[k] *= f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        o[j][2 * k] *= f;
+        o[j][2 * k + 1] *= f;
+      }
+      m[k] = mz[k] + static_cast<float>(most - 127);
+    }
+    for (; c < c1; c += kFewWarps) step(std::true_type{});
   }
 
   // the warps' parts: element 16 n + j of a row lies at 8 j + n
