@@ -18,15 +18,15 @@
 // product would have to be 8-bit, and weights and queries rounded to three digits are not
 // attention; the conversion is shared by 512 rows.
 //
-// What bounds it (972 x 4096, 38 heads of 128: 70 us, 1.11 PFLOP/s, 0.59 of the measured rate; 4680 x
-// 32760, 40 heads 0.54): a tile of 128 keys takes some 4300 clocks for 2048 of products. An
+// What bounds it (972 x 4096, 38 heads of 128: 72.5 us, 1.07 PFLOP/s, 0.57 of the measured rate; 4680 x
+// 32760, 40 heads 0.53): a tile of 128 keys takes some 4300 clocks for 2048 of products. An
 // instruction with A from shared memory takes 86 to 95 clocks instead of 64 by itself, and each
 // row tile goes round a chain of softmax (2000), arrival from the other CTA, O += P V and the
 // next S. Tried: a CTA by itself (twice the conversion per SM: 700 TFLOP/s), P through shared
 // memory so that S is free sooner (870), two softmax threads per row (590, held by the three
 // conversion warps that were left room for), one row tile per pair and two blocks per SM (830).
-// Short key ranges are bound by what comes before and after: 32760 queries over 128 keys take 375
-// us, 11 a pair of blocks, so that over 512 keys (582) more than half is not products.
+// Short key ranges are bound by what comes before and after: 32760 queries over 128 keys take 378
+// us, 11 a pair of blocks, so that over 512 keys (585) more than half is not products.
 //
 // Scales. A key's block scale multiplies its score in fp32. A value's block scale 2^x_t multiplies
 // its weight before the rounding to fp16 (the products take no more digits at this rate; by 2^-11
@@ -38,10 +38,10 @@
 // The sum of the 2^z_t has a reference n of its own. As long as the value scales met lie within
 // 2^60 of one another its terms are the weights without their 2^x_t, one exponential for both,
 // and n is m less the first tile's largest x. Beyond (a page of zeros has the least scale there
-// is) the terms are taken by themselves, as 2^(z_t - n), in the path that masked tiles take, and both
-// references are whole numbers: a difference of two that are large is exact then. (Otherwise m is
-// the maximum itself: a key that is all a row sees has a weight of just 2^7, which fp16 holds, and
-// its value comes out as it is.)
+// is) the terms are taken by themselves, as 2^(z_t - n) (4680 x 32760, 40 heads 3610 us, were it done
+// all the time, 3116 otherwise), and both references are whole numbers: a difference of two that are
+// large is exact then. (Otherwise m is the maximum itself: a key that is all a row sees has a weight
+// of just 2^7, which fp16 holds, and its value comes out as it is.)
 //
 // m follows its maximum lazily: O in tensor memory is rescaled only when that has grown by more
 // than 2^8, which after the first tiles is hardly ever; weights then reach 2^15 instead of 2^7,
@@ -558,8 +558,9 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
     constexpr bool kApart = decltype(are_apart)::value;
     const TileMeta& meta = sm->meta[j & (kMetaSlots - 1)];
     const int key0 = (w.key_tile0 + j) * kTileKeys;
-    // the weights' reference follows the tile's maximum of z + x, and the sum with it
-    auto follow = [&](float top) {
+    float top = -INFINITY, top_z = -INFINITY;  // the tile's maxima of z + x and, where that is wanted, of z
+    // the weights' reference follows the first, and the sum with it unless it has its own
+    auto follow = [&]() {
       if (!__any_sync(0xffffffffu, top > m + kGrowth || (kApart && m != ceilf(m)))) return;
       const float now = kApart ? fmaxf(ceilf(m), ceilf(top)) : fmaxf(m, top);
       const float f = exp2_fast(m - (now == -INFINITY ? 0.0f : now));
@@ -575,8 +576,13 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
         tmem_st_32x32b_x16(t_o + 16 * c, o);
       }
     };
-    if (!kApart && (dead || (key0 >= all_lo && key0 + kTileKeys <= all_hi && meta.there == 0xFFu && meta.vnan == 0))) {
-      float top = -INFINITY;
+    auto follow_sum = [&]() {
+      const float now = fmaxf(n, ceilf(top_z)), use = now == -INFINITY ? 0.0f : now;
+      l *= exp2_fast(n - use);
+      n = now;
+      return -use;
+    };
+    if (dead || (key0 >= all_lo && key0 + kTileKeys <= all_hi && meta.there == 0xFFu && meta.vnan == 0)) {
 #pragma unroll 2
       for (int c = 0; c < 4; ++c) {
         float z[32];
@@ -592,9 +598,11 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
           t[g] = fmaxf(t[g], z[16 * g + 15]);
         }
         top = max3(top, fmaf(t[0], coef * kx.x, kx.y), fmaf(t[1], coef * kx.z, kx.w));
+        if (kApart) top_z = max3(top_z, t[0] * (coef * kx.x), t[1] * (coef * kx.z));
       }
-      follow(top);
+      follow();
       const float up = kBias - (m == -INFINITY ? 0.0f : m), unit = meta.origin - kBias;
+      const float up_n = kApart ? follow_sum() : 0.0f;
 #pragma unroll 2
       for (int c = 0; c < 4; ++c) {
         float z[32];
@@ -615,12 +623,25 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
             sum = fadd2(sum, e);
             pk[8 * g + i] = pack_pair<__half>(e);
           }
-          l = fmaf(sum.x + sum.y, exp2_fast(unit - (g == 0 ? kx.y : kx.w)), l);
+          if constexpr (kApart) {
+            const float2 nn = make_float2(up_n, up_n);
+            sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float2 e = ffma2(make_float2(z[16 * g + 2 * i], z[16 * g + 2 * i + 1]), cc, nn);
+              e.x = exp2_fast(e.x);
+              e.y = exp2_fast(e.y);
+              sum = fadd2(sum, e);
+            }
+            l += sum.x + sum.y;
+          } else {
+            l = fmaf(sum.x + sum.y, exp2_fast(unit - (g == 0 ? kx.y : kx.w)), l);
+          }
         }
         tmem_st_32x32b_x16(t_s + 16 * c, pk);
       }
     } else {
-      // Masked, with a NaN among the value scales, or with scales far apart: 16 keys at a time.
+      // Masked, or with a NaN among the value scales: 16 keys at a time, scores read twice.
       // Bit i of `seen`: the row sees key i of the group.
       const uint32_t there = meta.there, vnan = meta.vnan;
       auto seen_bits = [&](int g) {
@@ -629,7 +650,6 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
         bits &= from <= 0 ? 0xFFFFu : from >= 16 ? 0u : ~((1u << from) - 1u);
         return (there >> g & 1) != 0 ? bits : 0u;
       };
-      float top = -INFINITY, top_z = -INFINITY;
 #pragma unroll 1
       for (int g = 0; g < 8; ++g) {
         uint32_t z[16];
@@ -640,17 +660,12 @@ __device__ __forceinline__ void softmax_role(const CacheAttentionArgs& a, const 
 #pragma unroll
         for (int i = 0; i < 16; ++i) t = fmaxf(t, (seen >> i & 1) ? __uint_as_float(z[i]) : -INFINITY);
         t *= coef * meta.kx[g].x;
-        top_z = fmaxf(top_z, t);
+        if (kApart) top_z = fmaxf(top_z, t);
         top = fmaxf(top, t + meta.kx[g].y);
       }
-      follow(top);
+      follow();
       const float up = kBias - (m == -INFINITY ? 0.0f : m), unit = meta.origin - kBias;
-      if constexpr (kApart) {
-        const float now = fmaxf(n, ceilf(top_z));
-        l *= exp2_fast(n - (now == -INFINITY ? 0.0f : now));
-        n = now;
-      }
-      const float up_n = n == -INFINITY ? 0.0f : -n;
+      const float up_n = kApart ? follow_sum() : 0.0f;
 #pragma unroll 1
       for (int g = 0; g < 8; ++g) {
         uint32_t z[16], pk[8];

@@ -10,13 +10,13 @@
 // them in registers, where the global loads put them. No shared memory, no barrier and no
 // conversion pass stands between memory and the product. tcgen05 would want the same codes
 // converted and stored to shared memory first, for a tile whose 128 rows would be mostly
-// padding (17 rows over 4096 keys, 40 heads: 27 us here, 56 there).
+// padding (17 rows over 4096 keys, 40 heads: 26 us here, 53 there).
 //
-// What bounds it: 4 sequences of 32760 tokens, 40 heads of 128, one row each (1.34 GB) take 289 us,
-// 4.6 TB/s of 6.8: the warps' chains of product, maximum, exponential and product, about 400
+// What bounds it: 4 sequences of 32760 tokens, 40 heads of 128, one row each (1.34 GB) take 273 us,
+// 4.9 TB/s of 6.8: the warps' chains of product, maximum, exponential and product, some 900
 // instructions per 8 KB. More warps did not help (8 rows a tile in 168 or 128 registers: 276 and
 // 295 us against 278 at the time), nor did integer operations in place of the conversion
-// instructions (321). One token over 512 keys takes 9.7 us, latencies alone. Keys are divided among
+// instructions (321). One token over 512 keys takes 9.4 us, latencies alone. Keys are divided among
 // blocks by waves (see the host's attention_shape) and the parts joined by a second, small kernel.
 //
 // Layouts. Lane 4g + t holds column g of the B operand and rows g, g + 8 of A and C.
@@ -35,11 +35,11 @@
 // x_t. Beyond, that would take the digits of weights that matter, for the sake of large values that
 // the row does not see or whose weight is negligible: a weight is then 2^(z_t + x_t - m), m the row's
 // own maximum of that over the keys it sees, and the sum of the 2^z_t has a reference and exponentials
-// of its own (13 % slower: 327 us for the 289 above, were it done all the time); both references are
-// whole numbers then, so that their difference is exact however large they are. Held 2^14 above, the
-// row's largest weight is 2^2 or more: down to 2^-16 of it weights keep fp16's digits, and what is
-// 2^-27 of it is lost. A key that is all a row sees has a weight of just 2^(14 + x_t - x): its value
-// comes out as it is.
+// of its own (297 us for the 273 above, were it done all the time); both references are whole numbers
+// then, so that their difference is exact however large they are. Held 2^14 above, the row's largest
+// weight is 2^2 or more: down to 2^-16 of it weights keep fp16's digits, and what is 2^-27 of it is
+// lost. While scales lie near, a key that is all a row sees has a weight of just 2^(14 + x_t - x), and
+// its value comes out as it is.
 #include <type_traits>
 
 #include "kv_cache.cuh"

@@ -26,11 +26,11 @@ constexpr int kMaxSplits = 64;
 // rows leave part of every product empty. us a call in a captured graph, few rows' form / tcgen05,
 // heads of 128, 40 or 8 key heads:
 //         40: over 512   over 4096     4 x 32760     8: over 512   over 4096    32760
-//   17    12.1 / 13.9    27.4 / 53.0    581 / 1331   12.1 / 14.0   17.4 / 19.2  39.5 / 62.9
-//   32    12.2 / 13.9    29.3 / 53.5    597 / 1331   12.2 / 13.8   16.9 / 18.8  39.0 / 62.6
-//   64    14.6 / 14.0    52.5 / 55.4   1110 / 1351   12.2 / 13.8   19.7 / 19.1  60.5 / 63.1
-//   96    14.9 / 14.2    59.9 / 57.6   1625 / 1367   12.4 / 13.8   22.1 / 20.2  83.0 / 64.3
-//   128   23.7 / 14.4    96.5 / 60.6   2081 / 1383   12.2 / 14.2   24.9 / 20.4   114 / 64.4
+//   17    11.4 / 13.8    26.0 / 53.2    550 / 1325   11.4 / 13.7   16.6 / 18.9  37.2 / 62.3
+//   32    11.6 / 13.7    27.6 / 54.0    566 / 1325   11.5 / 13.7   16.5 / 18.7  37.4 / 62.5
+//   64    13.8 / 13.8    49.3 / 55.8   1046 / 1345   11.6 / 13.7   19.0 / 19.0  56.4 / 62.9
+//   96    14.4 / 14.0    55.6 / 58.2   1525 / 1361   11.7 / 13.7   21.3 / 20.2  76.6 / 64.1
+//   128   22.7 / 14.3    92.0 / 60.9   1893 / 1377   11.8 / 14.0   23.6 / 20.4   106 / 64.2
 constexpr int64_t kFewMaxRows = 64;
 // Blocks that run at a time: of the form for few rows two on each of 152 SMs, of the other a pair on
 // two SMs. Not the current device's count: the workspace is a function of the sizes alone, asked
