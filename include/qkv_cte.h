@@ -596,7 +596,7 @@ int qkv_cte_cache_read(qkv_cte_cache_plan_t plan, const qkv_cte_cache_pages* pag
  * of -infinity; a row that sees a token and has an element of q that is not finite becomes NaN.
  * Products and statistics are fp32, out is rounded once. Before they multiply the codes,
  * weights are rounded to fp16 with their value scale, as p_t 2^(sf_t - 127): each by 2^-11 of
- * itself, or by 2^-26 of the row's largest such product over the tokens that it sees where that is
+ * itself, or by 2^-27 of the row's largest such product over the tokens that it sees where that is
  * more (pages so much smaller than another that the row attends to are lost beside it).
  *
  * q, out    : dtype (bf16 or fp16) [batch, seq, n_q_heads, d_head] with strides in elements,
