@@ -31,10 +31,11 @@
 // Scales. A key's block scale multiplies its score in fp32. A value's block scale 2^x_t multiplies
 // its weight before the rounding to fp16 (the products take no more digits at this rate; by 2^-11
 // at most, an eighth of what a result's rounding to bf16 may cost and as much as one to fp16, and
-// it averages out over the keys), so what is rounded is 2^(z_t + x_t - m), with m the row's own maximum of z_t + x_t over the keys it sees: neither a
-// key that it does not see nor one whose weight makes its large values negligible takes digits from
-// the others. With 2^7 above, the row's largest weight is 2^6 or more: down to 2^-20 of it weights
-// keep fp16's digits, and what is 2^-31 of it is lost.
+// it averages out over the keys), so what is rounded is 2^(z_t + x_t - m), with m the row's own
+// maximum of z_t + x_t over the keys it sees: neither a key that it does not see nor one whose
+// weight makes its large values negligible takes digits from the others. With 2^7 above, the row's
+// largest weight is 2^6 or more: down to 2^-20 of it weights keep fp16's digits, and what is 2^-31
+// of it is lost.
 // The sum of the 2^z_t has a reference n of its own. As long as the value scales met lie within
 // 2^60 of one another its terms are the weights without their 2^x_t, one exponential for both,
 // and n is m less the first tile's largest x. Beyond (a page of zeros has the least scale there
